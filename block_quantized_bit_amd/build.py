@@ -2,7 +2,7 @@
 
     python -m block_quantized_bit_amd.build
 
-quant.hip and act.hip (bit-exact quantizers) are compiled with -ffp-contract=off so
+quant.hip, act.hip and cache.hip (bit-exact quantizers) are compiled with -ffp-contract=off so
 no multiply-add is fused; every HIP file is compiled with packed-fp32 ops
 disabled.  gemm.hip is compiled with LLVM's iterative ILP machine scheduler: with
 it the register allocator keeps the GEMM accumulators in place across the K loop
@@ -33,6 +33,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 SOURCES = [
     ("quant.hip", ["-ffp-contract=off"]),
     ("act.hip", ["-ffp-contract=off"]),
+    ("cache.hip", ["-ffp-contract=off"]),
+    ("attn.hip", []),
     ("gemv.hip", []),
     ("gemm.hip", ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]),
     ("gemm_nvfp4_wide.hip", []),

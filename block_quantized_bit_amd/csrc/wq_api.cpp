@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -171,6 +172,78 @@ wq_status scratch_for_current_device(void** out) {
     });
     if (g_scratch_err[dev] != hipSuccess || !g_scratch_ptr[dev]) return WQ_ERR_HIP;
     *out = g_scratch_ptr[dev];
+    return WQ_OK;
+}
+
+// A cache descriptor; fills what of q (the sequences) follows from it.
+wq_status check_cache(const wq_cache_desc* d, wq::Seqs* q, bool* q41) {
+    if (!d || d->reserved != 0) return WQ_ERR_INVALID_ARG;
+    if (d->format < WQ_NF4 || d->format > WQ_Q6_K) return WQ_ERR_INVALID_ARG;
+    if (d->format != WQ_Q4_0 && d->format != WQ_Q4_1) return WQ_ERR_UNSUPPORTED;
+    if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128 && d->head_dim != 256) return WQ_ERR_UNSUPPORTED;
+    if (d->kv_heads < 1 || d->kv_heads > 65535) return WQ_ERR_SHAPE;
+    if (d->page < wq::kUnit || d->page % wq::kUnit != 0 || d->page > (1 << 24)) return WQ_ERR_SHAPE;
+    if (d->pages < 1 || d->pages > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+    *q41 = d->format == WQ_Q4_1;
+    q->heads = d->kv_heads;
+    q->page = d->page;
+    q->upp = d->page / wq::kUnit;
+    q->pages = d->pages;
+    q->unit_bytes = wq::cache_unit_bytes(*q41, d->head_dim);
+    const int64_t page_bytes = q->unit_bytes * q->upp * d->kv_heads;   // < 2^14 2^19 2^16
+    if (d->pages > (int64_t(1) << 46) / page_bytes) return WQ_ERR_SHAPE;
+    return WQ_OK;
+}
+
+wq_status check_seqs(const wq_seqs* s, wq::Seqs* q) {
+    if (!s || s->reserved != 0) return WQ_ERR_INVALID_ARG;
+    if (s->batch < 0 || s->batch > (1 << 20) || s->rows < 0) return WQ_ERR_SHAPE;
+    if (!s->len) return WQ_ERR_INVALID_ARG;
+    if (!aligned(s->len, 4) || !aligned(s->table, 4) || !aligned(s->row_start, 4)) return WQ_ERR_ALIGNMENT;
+    if (!s->row_start && s->rows < s->batch) return WQ_ERR_SHAPE;
+    if (s->table ? s->table_ld < 1 : s->table_ld != 0) return WQ_ERR_INVALID_ARG;
+    q->table_ld = s->table ? s->table_ld : 1;
+    if ((int64_t)q->table_ld * q->page > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+    q->row_start = s->row_start;
+    q->len = s->len;
+    q->table = s->table;
+    q->batch = s->batch;
+    q->rows = s->rows;
+    return WQ_OK;
+}
+
+// Rows of K and V (or Q, Y): width elements each.
+wq_status check_rows(const void* p, int64_t ld, int64_t width) {
+    if (!p) return WQ_ERR_INVALID_ARG;
+    if (ld < width || ld % 8 != 0 || ld > kMaxOut) return WQ_ERR_INVALID_ARG;
+    return aligned(p, 16) ? WQ_OK : WQ_ERR_ALIGNMENT;
+}
+
+wq_status check_cache_rows(const wq_cache_desc* d, const wq_seqs* s, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                           int32_t dt, const void* cache, wq::Seqs* q, bool* q41) {
+    wq_status st = check_cache(d, q, q41);
+    if (st != WQ_OK) return st;
+    if ((st = check_seqs(s, q)) != WQ_OK) return st;
+    if (dt != WQ_BF16 && dt != WQ_F32) return WQ_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)d->kv_heads * d->head_dim;
+    if ((st = check_rows(k, ldk, width)) != WQ_OK) return st;
+    if ((st = check_rows(v, ldv, width)) != WQ_OK) return st;
+    if (!cache) return WQ_ERR_INVALID_ARG;
+    if (!aligned(cache, 16)) return WQ_ERR_ALIGNMENT;
+    // chunks of 8 channels, 256 to a workgroup, at most 2^31 - 1 workgroups
+    if ((int64_t)q->rows > (int64_t(0x7FFFFFFF) * 256) / (width / 8)) return WQ_ERR_SHAPE;
+    return WQ_OK;
+}
+
+wq_status check_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, wq::AttnArgs* a) {
+    wq_status st = check_cache(d, &a->s, &a->q41);
+    if (st != WQ_OK) return st;
+    if ((st = check_seqs(s, &a->s)) != WQ_OK) return st;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % d->kv_heads != 0) return WQ_ERR_SHAPE;
+    if ((int64_t)a->s.rows > 0x7FFFFFFF / q_heads) return WQ_ERR_SHAPE;   // rows and heads: the launch's workgroups
+    a->q_heads = q_heads;
+    a->group = q_heads / d->kv_heads;
+    a->dim = d->head_dim;
     return WQ_OK;
 }
 
@@ -385,6 +458,78 @@ wq_status wq_matmul_w4a4(const wq_desc* d, int64_t m, const void* xcodes, const 
     p.out.ldy[0] = ldy;
     p.out.end[0] = p.out.end[1] = p.out.end[2] = p.n;
     return run_matmul(p, stream);
+}
+
+wq_status wq_cache_size(const wq_cache_desc* d, size_t* bytes) {
+    wq::Seqs q{};
+    bool q41;
+    wq_status st = check_cache(d, &q, &q41);
+    if (st != WQ_OK) return st;
+    if (!bytes) return WQ_ERR_INVALID_ARG;
+    *bytes = (size_t)(q.unit_bytes * q.upp * q.heads) * (size_t)q.pages;
+    return WQ_OK;
+}
+
+wq_status wq_cache_write(const wq_cache_desc* d, const wq_seqs* s, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                         int32_t xdt, void* cache, void* stream) {
+    wq::Seqs q{};
+    bool q41;
+    wq_status st = check_cache_rows(d, s, k, ldk, v, ldv, xdt, cache, &q, &q41);
+    if (st != WQ_OK) return st;
+    if (q.rows == 0 || q.batch == 0) return WQ_OK;
+    return from_hip(wq::launch_cache_write(q, q41, d->head_dim, xdt == WQ_F32, k, ldk, v, ldv, static_cast<uint8_t*>(cache),
+                                           static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_cache_read(const wq_cache_desc* d, const wq_seqs* s, const void* cache, void* k, int64_t ldk, void* v,
+                        int64_t ldv, int32_t ydt, void* stream) {
+    wq::Seqs q{};
+    bool q41;
+    wq_status st = check_cache_rows(d, s, k, ldk, v, ldv, ydt, cache, &q, &q41);
+    if (st != WQ_OK) return st;
+    if (q.rows == 0 || q.batch == 0) return WQ_OK;
+    return from_hip(wq::launch_cache_read(q, q41, d->head_dim, ydt == WQ_F32, static_cast<const uint8_t*>(cache), k, ldk, v,
+                                          ldv, static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_attn_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, size_t* bytes) {
+    wq::AttnArgs a{};
+    wq_status st = check_attn(d, s, q_heads, &a);
+    if (st != WQ_OK) return st;
+    if (!bytes) return WQ_ERR_INVALID_ARG;
+    *bytes = a.s.rows == 0 || a.s.batch == 0 ? 0 : wq::attn_workspace_bytes(a);
+    return WQ_OK;
+}
+
+wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq, const void* cache,
+                  float scale, int32_t causal, int32_t window, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes,
+                  void* stream) {
+    wq::AttnArgs a{};
+    wq_status st = check_attn(d, s, q_heads, &a);
+    if (st != WQ_OK) return st;
+    const int64_t width = (int64_t)q_heads * d->head_dim;
+    if ((st = check_rows(q, ldq, width)) != WQ_OK) return st;
+    if ((st = check_rows(y, ldy, width)) != WQ_OK) return st;
+    if (!cache) return WQ_ERR_INVALID_ARG;
+    if (!aligned(cache, 16)) return WQ_ERR_ALIGNMENT;
+    if (!std::isfinite(scale)) return WQ_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return WQ_ERR_INVALID_ARG;
+    if (window < 0 || (window > 0 && !causal)) return WQ_ERR_INVALID_ARG;
+    if (a.s.rows == 0 || a.s.batch == 0) return WQ_OK;
+    if (ws) {
+        if (!aligned(ws, 16)) return WQ_ERR_ALIGNMENT;
+        if (ws_bytes < wq::attn_workspace_bytes(a)) return WQ_ERR_WORKSPACE;
+    }
+    a.q = q;
+    a.ldq = ldq;
+    a.cache = static_cast<const uint8_t*>(cache);
+    a.y = y;
+    a.ldy = ldy;
+    a.ws = static_cast<uint8_t*>(ws);
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.causal = causal == 1;
+    a.window = window;
+    return from_hip(wq::launch_attn(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

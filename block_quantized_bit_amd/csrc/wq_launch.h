@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "cache_layout.h"
+
 namespace wq {
 
 // Offsets inside the scales buffer (bytes).
@@ -69,5 +71,26 @@ hipError_t launch_quantize_act(int64_t m, int64_t k, const uint16_t* x, int64_t 
 // xe[m][k] = bf16(+-e2m1 * s) (exact) and *gprod = g_w * g_x, with g_w read at gw.
 hipError_t launch_expand_act(int64_t m, int64_t k, const uint8_t* codes, const uint8_t* scales,
                              const uint8_t* gw, uint16_t* xe, float* gprod, hipStream_t s);
+
+// 4-bit key/value cache (cache.hip): rows of K and V, bf16 or fp32, into and out of the pool.
+hipError_t launch_cache_write(const Seqs& q, bool q41, int dim, bool f32, const void* k, int64_t ldk, const void* v,
+                              int64_t ldv, uint8_t* cache, hipStream_t s);
+hipError_t launch_cache_read(const Seqs& q, bool q41, int dim, bool f32, const uint8_t* cache, void* k, int64_t ldk,
+                             void* v, int64_t ldv, hipStream_t s);
+
+// Attention over the cache (attn.hip).
+struct AttnArgs {
+    Seqs s;
+    const uint16_t* q;
+    const uint8_t* cache;
+    uint16_t* y;
+    int64_t ldq, ldy;
+    uint8_t* ws;           // null: no split of a sequence over workgroups
+    float scale_log2;      // softmax scale times log2(e)
+    int32_t q_heads, group, dim, window;
+    bool q41, causal;
+};
+size_t attn_workspace_bytes(const AttnArgs& a);
+hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 
 }  // namespace wq

@@ -22,7 +22,8 @@ WQ_BF16, WQ_F32 = 1, 2
 
 EXPORTS = ("wq_status_str", "wq_packed_size", "wq_quantize", "wq_dequantize",
            "wq_workspace_size", "wq_matmul", "wq_matmul_noalloc", "wq_matmul_qkv",
-           "wq_act_packed_size", "wq_quantize_act", "wq_w4a4_workspace_size", "wq_matmul_w4a4")
+           "wq_act_packed_size", "wq_quantize_act", "wq_w4a4_workspace_size", "wq_matmul_w4a4",
+           "wq_cache_size", "wq_cache_write", "wq_cache_read", "wq_attn_workspace_size", "wq_attn")
 
 # Format names accepted by the harness; aliases follow the NF4 option's names
 # ("asr: add a 4-bit nf4 option for the Whisper engine": nf4, aliases 4bit, int4).
@@ -53,10 +54,49 @@ class wq_packed(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class wq_cache_desc(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("pages", ctypes.c_int64), ("reserved", ctypes.c_int32)]
+
+
+class wq_seqs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("row_start", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_ld", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 def desc(fmt, n: int, k: int, dq: bool = False, block: int = 0) -> wq_desc:
     if isinstance(fmt, str):
         fmt = format_from_name(fmt)
     return wq_desc(int(fmt), int(block), int(n), int(k), 256 if dq else 0, 0)
+
+
+def cache_desc(fmt, head_dim: int, kv_heads: int, page: int, pages: int) -> wq_cache_desc:
+    if isinstance(fmt, str):
+        fmt = format_from_name(fmt)
+    return wq_cache_desc(int(fmt), int(head_dim), int(kv_heads), int(page), int(pages), 0)
+
+
+def seqs(batch: int, rows: int, len, table=None, row_start=None, table_ld: int | None = None) -> wq_seqs:  # noqa: A002
+    """The sequences of a cache or attention call.  `len`, `table` and `row_start` are int32 device tensors (contiguous;
+    `table` [batch, pages per sequence]) or device addresses (a table's address needs `table_ld`); the result keeps
+    tensors alive and passes their addresses."""
+    for name, t, n in (("len", len, batch), ("table", table, None), ("row_start", row_start, batch + 1)):
+        if t is None or isinstance(t, int):
+            continue
+        if str(t.dtype) != "torch.int32" or not t.is_contiguous():
+            raise ValueError(f"seqs: {name} must be a contiguous int32 tensor, got {t.dtype}")
+        if n is not None and t.numel() < n:
+            raise ValueError(f"seqs: {name} has {t.numel()} entries; {n} are needed")
+    if table is not None and not isinstance(table, int):
+        if table.dim() != 2 or table.shape[0] < batch:
+            raise ValueError(f"seqs: table must be [batch, pages per sequence], got {tuple(table.shape)}")
+        if table_ld is not None and table_ld != table.shape[1]:
+            raise ValueError(f"seqs: table has {table.shape[1]} entries per sequence, not {table_ld}")
+        table_ld = table.shape[1]
+    s = wq_seqs(int(batch), int(rows), _ptr(row_start), _ptr(len), _ptr(table), int(table_ld or 0), 0)
+    s.tensors = (row_start, len, table)
+    return s
 
 
 _lib = None
@@ -96,6 +136,17 @@ def lib():
         L.wq_w4a4_workspace_size.argtypes = [pd, i64, ctypes.POINTER(ctypes.c_size_t)]
         L.wq_matmul_w4a4.restype = ctypes.c_int
         L.wq_matmul_w4a4.argtypes = [pd, i64, P, P, wq_packed, P, P, ctypes.c_int32, i64, P, ctypes.c_size_t, P]
+        pc, ps, i32, sz = ctypes.POINTER(wq_cache_desc), ctypes.POINTER(wq_seqs), ctypes.c_int32, ctypes.c_size_t
+        L.wq_cache_size.restype = ctypes.c_int
+        L.wq_cache_size.argtypes = [pc, ctypes.POINTER(sz)]
+        L.wq_cache_write.restype = ctypes.c_int
+        L.wq_cache_write.argtypes = [pc, ps, P, i64, P, i64, i32, P, P]
+        L.wq_cache_read.restype = ctypes.c_int
+        L.wq_cache_read.argtypes = [pc, ps, P, P, i64, P, i64, i32, P]
+        L.wq_attn_workspace_size.restype = ctypes.c_int
+        L.wq_attn_workspace_size.argtypes = [pc, ps, i32, ctypes.POINTER(sz)]
+        L.wq_attn.restype = ctypes.c_int
+        L.wq_attn.argtypes = [pc, ps, i32, P, i64, P, ctypes.c_float, i32, i32, P, i64, P, sz, P]
         _lib = L
     return _lib
 
@@ -205,3 +256,35 @@ def wq_matmul_w4a4(d: wq_desc, m: int, xcodes, xscales, codes, scales, bias, y, 
                               wq_packed(_ptr(codes), _ptr(scales)), _ptr(bias), _ptr(y), int(ydt), int(ldy),
                               _ptr(ws), int(ws_bytes), _stream(stream))
     return _check(st, "wq_matmul_w4a4", check)
+
+
+def wq_cache_size(d: wq_cache_desc) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().wq_cache_size(ctypes.byref(d), ctypes.byref(b)), "wq_cache_size", True)
+    return b.value
+
+
+def wq_cache_write(d: wq_cache_desc, s: wq_seqs, k, ldk: int, v, ldv: int, xdt: int, cache, stream=None, check=True) -> int:
+    st = lib().wq_cache_write(ctypes.byref(d), ctypes.byref(s), _ptr(k), int(ldk), _ptr(v), int(ldv), int(xdt), _ptr(cache),
+                              _stream(stream))
+    return _check(st, "wq_cache_write", check)
+
+
+def wq_cache_read(d: wq_cache_desc, s: wq_seqs, cache, k, ldk: int, v, ldv: int, ydt: int, stream=None, check=True) -> int:
+    st = lib().wq_cache_read(ctypes.byref(d), ctypes.byref(s), _ptr(cache), _ptr(k), int(ldk), _ptr(v), int(ldv), int(ydt),
+                             _stream(stream))
+    return _check(st, "wq_cache_read", check)
+
+
+def wq_attn_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().wq_attn_workspace_size(ctypes.byref(d), ctypes.byref(s), int(q_heads), ctypes.byref(b)),
+           "wq_attn_workspace_size", True)
+    return b.value
+
+
+def wq_attn(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scale: float, causal, window: int, y, ldy: int,
+            ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
+    st = lib().wq_attn(ctypes.byref(d), ctypes.byref(s), int(q_heads), _ptr(q), int(ldq), _ptr(cache), float(scale),
+                       int(causal), int(window), _ptr(y), int(ldy), _ptr(ws), int(ws_bytes), _stream(stream))
+    return _check(st, "wq_attn", check)

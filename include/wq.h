@@ -258,6 +258,111 @@ wq_status wq_matmul_w4a4(const wq_desc* d, int64_t m, const void* xcodes, const 
                          const uint16_t* bias, void* y, int32_t ydt, int64_t ldy, void* ws, size_t ws_bytes,
                          void* stream);
 
+/* ---- 4-bit key/value cache, and attention over it -----------------------------
+ * The fused projection writes K and V rows of a decoder's cache ("Run quantized
+ * Whisper on the fused Metal decode path", "Summary"); here the rows are held in
+ * q4_0 or q4_1, quantized as they are written, and attention reads them packed.
+ *
+ * A block is 32 channels of one token of one head, quantized by the format's rule
+ * above (q4_0: d, q4_1: d and m), after clamping to +-32768 so that every stored
+ * value is a finite fp16 number (infinities are clamped too; a NaN is stored as
+ * -32768).  Bit-exact: codes and scales are a pure function of the block.
+ *
+ * The cache is one buffer of `pages` pages; a page holds `page` tokens, K and V of
+ * all heads.  A page is written token by token in any order; bytes of other tokens
+ * are not touched.  The buffer needs no initialization. */
+
+/*   format   : WQ_Q4_0 or WQ_Q4_1 (else WQ_ERR_UNSUPPORTED)
+ *   head_dim : 64, 96, 128 or 256 (else WQ_ERR_UNSUPPORTED)
+ *   kv_heads : 1 .. 65535
+ *   page     : tokens per page, a multiple of 32, at most 2^24
+ *   pages    : 1 .. 2^31 - 1; the whole cache is at most 2^46 bytes */
+typedef struct {
+    int32_t format;
+    int32_t head_dim;
+    int32_t kv_heads;
+    int32_t page;
+    int64_t pages;
+    int32_t reserved;   /* must be 0 */
+} wq_cache_desc;
+
+/* The sequences of a call.  Rows are tokens: row r of K, V, Q and Y is one token of
+ * one sequence, the rows of a sequence are consecutive, and they are its last ones:
+ * with n rows, row i of sequence b is its token len[b] - n + i.
+ *   batch     : sequences, 1 .. 2^20 (0: the call does nothing)
+ *   rows      : rows of the call's tensors, 0 .. 2^31 - 1.  Rows behind the last
+ *               sequence (padding) are neither read nor written.
+ *   row_start : device int32 [batch + 1], ascending: sequence b has the rows
+ *               row_start[b] .. row_start[b + 1] - 1 (none is allowed); NULL: one row
+ *               each, row b is sequence b's (then rows >= batch)
+ *   len       : device int32 [batch], tokens of each sequence, the call's rows
+ *               included.  A row whose token would be negative has no token.
+ *   table     : device int32 [batch][table_ld]: page of the tokens page * j ..
+ *               page * j + page - 1 of sequence b; NULL: page b is all of sequence b
+ *               (table_ld must be 0).  An entry outside 0 .. pages - 1 is no page:
+ *               its tokens are absent (not written, read as zeros, not attended to),
+ *               and so are tokens past the last entry.
+ *   table_ld  : entries per sequence, 1 ..; table_ld * page <= 2^31 - 1
+ * The device arrays are read when the work runs, so a captured graph can be replayed
+ * with other lengths and pages.  Several sequences may share pages that they read; the
+ * rows that one wq_cache_write call writes must be at distinct places. */
+typedef struct {
+    int32_t batch;
+    int32_t rows;
+    const int32_t* row_start;
+    const int32_t* len;
+    const int32_t* table;
+    int32_t table_ld;
+    int32_t reserved;   /* must be 0 */
+} wq_seqs;
+
+/* Host-only.  Bytes of the cache buffer: pages * page * kv_heads * head_dim * 9/8 (q4_0:
+ * 4.5 bits for K and for V) or * 10/8 (q4_1: 5 bits). */
+wq_status wq_cache_size(const wq_cache_desc* d, size_t* bytes);
+
+/* Quantize the rows of K and V into the cache (16-byte aligned).
+ *   k, v : [rows, kv_heads * head_dim] of type xdt (WQ_BF16 or WQ_F32), 16-byte aligned,
+ *          leading dimensions ldk, ldv >= kv_heads * head_dim, multiples of 8, at most
+ *          2^31 - 1
+ * Rows without a token (see wq_seqs) are skipped. */
+wq_status wq_cache_write(const wq_cache_desc* d, const wq_seqs* s, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                         int32_t xdt, void* cache, void* stream);
+
+/* Read the rows' tokens back: k and v (as above, type ydt) receive the values that the
+ * cache stands for, rounded to nearest even for WQ_BF16; rows without a token receive
+ * zeros.  Any tokens can be read: with row_start covering len[b] rows, all of them. */
+wq_status wq_cache_read(const wq_cache_desc* d, const wq_seqs* s, const void* cache, void* k, int64_t ldk, void* v,
+                        int64_t ldv, int32_t ydt, void* stream);
+
+/* Host-only.  Workspace bytes wq_attn can use for such a call: partial results where few
+ * rows attend to long sequences and a sequence is shared out over workgroups.  It goes by
+ * the sizes in d and s alone (table_ld * page bounds the lengths), not by device data.  0
+ * means the call never uses one.  Same rules as for wq_workspace_size: without one the
+ * call does not split; no initialization; not shared by calls that may run at the same
+ * time (two streams, two graphs replayed side by side). */
+wq_status wq_attn_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, size_t* bytes);
+
+/* Y = softmax(scale * Q K^T) V over the cache, for each row and query head.
+ *   q_heads : a multiple of kv_heads, at most 65535; query head i reads key/value head
+ *             i / (q_heads / kv_heads)
+ *   q       : bf16 [rows, q_heads * head_dim], 16-byte aligned, ldq % 8 == 0,
+ *             q_heads * head_dim <= ldq <= 2^31 - 1
+ *   scale   : finite factor of the scores
+ *   causal  : 1: the row at token p sees the tokens 0 .. p; 0: every row sees all len[b]
+ *             tokens (cross-attention: the rows are then no tokens of the cache)
+ *   window  : with causal, > 0: the row sees only its last `window` tokens (itself among
+ *             them); 0: no limit
+ *   y       : bf16 [rows, q_heads * head_dim], as q with ldy; must not overlap q
+ *   ws      : workspace (16-byte aligned, see wq_attn_workspace_size) or NULL
+ * A row that sees no token gets zeros.  Scores, the softmax's maximum and sum and the
+ * sums over tokens are fp32; probabilities, values and (in calls with many rows) keys are
+ * rounded to fp16 for the matrix products.  Per element |y - y_ref| <=
+ * (2^-9 + 2^-9 A) * sum_t p_t |v^_t| plus the final bf16 rounding, where A is the row's
+ * largest |scale| * sum_c |q_c k^_tc| and y_ref is exact for the values in the cache. */
+wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq, const void* cache,
+                  float scale, int32_t causal, int32_t window, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes,
+                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,228 @@
+"""wq_cache_write and wq_cache_read against the oracle's quantizers: every stored value bit for bit, in bf16 and fp32, at
+every head size, with ragged rows, starts anywhere in a page, bad pages, padding rows and strides; nothing else in the
+cache changes."""
+import numpy as np
+import pytest
+import torch
+
+from block_quantized_bit_amd import wq
+from block_quantized_bit_amd.inputs import bf16_bits_to_f32, f32_to_bf16_bits
+
+from cache_helpers import Q4_0, Q4_1, Case, stored
+from gpu_helpers import DEV, dev_bf16, require_gpu, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _dev(x, dt, pad):
+    """[rows, width] fp32 (already bf16 values where dt is bf16) -> device rows with `pad` NaN columns."""
+    rows, width = x.shape
+    if dt == wq.WQ_F32:
+        a = np.full((rows, width + pad), np.nan, np.float32)
+        a[:, :width] = x
+        return torch.from_numpy(a).to(DEV)
+    a = np.full((rows, width + pad), 0x7FC0, np.uint16)
+    a[:, :width] = f32_to_bf16_bits(x)
+    return dev_bf16(a)
+
+
+def _values(c, dt, kind):
+    """K and V rows of the call, fp32 [rows, heads, dim] (bf16 numbers where dt is bf16)."""
+    shape = (c.rows, c.heads, c.dim)
+    out = []
+    for _ in range(2):
+        x = c.rng.standard_normal(shape, dtype=np.float32)
+        if kind == "wide":                             # every binade there is: scales that are subnormal or at the limit
+            x = x * np.exp2(c.rng.integers(-40, 20, shape[:2] + (1,))).astype(np.float32)
+        elif kind == "ties":                           # equal magnitudes of both signs, codes on the border, constant blocks
+            x = np.rint(x * 2) / 2
+            x[..., : c.dim // 2] = np.sign(x[..., : c.dim // 2])
+            x[0] = 0.0
+            x[-1] = -3.0
+        out.append(x if dt == wq.WQ_F32 else bf16_bits_to_f32(f32_to_bf16_bits(x)))
+    return out
+
+
+def _read(c, dt, pad=0, seqs=None, rows=None):
+    rows = c.rows if rows is None else rows
+    width = c.heads * c.dim
+    out = []
+    for _ in range(2):
+        out.append(torch.full((rows, width + pad), float("nan"), dtype=torch.float32, device=DEV) if dt == wq.WQ_F32 else
+                   torch.full((rows, width + pad), 0x7BAD, dtype=torch.int16, device=DEV))
+    wq.wq_cache_read(c.desc, seqs or c.seqs, c.cache, out[0], width + pad, out[1], width + pad, dt)
+    torch.cuda.synchronize()
+    return [o.cpu().numpy() for o in out]
+
+
+def _expected(c, x, dt, O):
+    """What reading the call's rows gives: raw bits, with the untouched value in rows that are no sequence's."""
+    val = stored(O, c.fmt, x).reshape(c.rows, -1).copy()
+    bits = val.view(np.uint32).copy() if dt == wq.WQ_F32 else f32_to_bf16_bits(val)
+    for b in range(c.batch):
+        for i in range(c.counts[b]):
+            t = c.lens[b] - c.counts[b] + i
+            if t < 0 or (b, t // c.page) in c.bad:
+                bits[c.start[b] + i] = 0
+    bits[c.start[-1]:] = np.float32("nan").view(np.uint32) if dt == wq.WQ_F32 else 0x7BAD
+    return bits
+
+
+def _same(got, want, dt):
+    got = got.view(np.uint32 if dt == wq.WQ_F32 else np.uint16)
+    negative_zero = np.uint32(0x80000000) if dt == wq.WQ_F32 else np.uint16(0x8000)
+    # a zero's sign is free: (q - 8) d is -0 where d < 0
+    got, want = (np.where(a == negative_zero, 0, a) for a in (got, want))
+    assert np.array_equal(got, want), f"{(got != want).sum()} of {got.size} differ, first at {np.argwhere(got != want)[0]}"
+
+
+SHAPES = [  # dim, heads, page, rows per sequence, tokens per sequence
+    (64, 20, 448, [1], [224]),
+    (64, 3, 32, [5, 0, 33, 1, 64], [5, 40, 70, 1, 64]),
+    (96, 5, 96, [7, 100, 2], [300, 100, 97]),
+    (128, 8, 64, [1] * 9, [1, 2, 3, 4, 5, 63, 64, 65, 200]),
+    (128, 2, 64, [130, 4, 3], [131, 2, 3]),            # the second sequence has rows without a token
+    (256, 1, 32, [31, 65], [100, 65]),
+    (256, 2, 128, [1, 300], [128, 301]),
+]
+
+
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("xdt", [wq.WQ_BF16, wq.WQ_F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+@pytest.mark.parametrize("kind", ["normal", "wide", "ties"])
+def test_write_then_read(orc, fmt, xdt, shape, kind):
+    dim, heads, page, counts, lens = SHAPES[shape]
+    say("cache", fmt, xdt, SHAPES[shape], kind)
+    c = Case(fmt, dim, heads, page, counts, lens, seed=shape, one_row=set(counts) == {1} and shape % 2 == 1, pad_rows=shape % 3)
+    k, v = _values(c, xdt, kind)
+    pad = 8 * (shape % 2)
+    K, V = (_dev(x.reshape(c.rows, -1), xdt, pad) for x in (k, v))
+    width = heads * dim
+    wq.wq_cache_write(c.desc, c.seqs, K, width + pad, V, width + pad, xdt, c.cache)
+    for ydt in (wq.WQ_BF16, wq.WQ_F32):
+        for got, x in zip(_read(c, ydt, pad), (k, v)):
+            assert np.all(got[:, width:].view(np.uint16) == (0x7BAD if ydt == wq.WQ_BF16 else got[:1, width:].view(np.uint16)))
+            _same(np.ascontiguousarray(got[:, :width]), _expected(c, x, ydt, orc), ydt)
+
+
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+def test_other_tokens_keep_their_bytes(orc, fmt):
+    """Tokens written one at a time in any order leave what one call with all of them leaves, byte for byte, and both
+    leave every byte outside the tokens as it was."""
+    dim, heads, page, lens = 96, 3, 64, [70, 1, 33]
+    a = Case(fmt, dim, heads, page, lens, lens, seed=3)
+    b = Case(fmt, dim, heads, page, lens, lens, seed=3)
+    before = a.cache.clone()
+    assert torch.equal(before, b.cache)
+    k, v = _values(a, wq.WQ_F32, "normal")
+    K, V = (_dev(x.reshape(a.rows, -1), wq.WQ_F32, 0) for x in (k, v))
+    wq.wq_cache_write(a.desc, a.seqs, K, heads * dim, V, heads * dim, wq.WQ_F32, a.cache)
+    order = a.rng.permutation(a.rows)
+    for row in order:
+        q = int(np.searchsorted(a.start, row, side="right")) - 1
+        n = torch.tensor([row - a.start[q] + 1], dtype=torch.int32, device=DEV)
+        one = wq.seqs(1, 1, n, b.d_table[q:q + 1])
+        wq.wq_cache_write(b.desc, one, K[row:row + 1], heads * dim, V[row:row + 1], heads * dim, wq.WQ_F32, b.cache)
+    torch.cuda.synchronize()
+    assert torch.equal(a.cache, b.cache)
+    per_token = heads * dim * (9 if fmt == Q4_0 else 10) // 8
+    assert int((a.cache != before).sum()) <= sum(lens) * per_token
+    # a second write of the same rows changes nothing; one of no tokens neither
+    wq.wq_cache_write(a.desc, a.seqs, K, heads * dim, V, heads * dim, wq.WQ_F32, a.cache)
+    none = wq.seqs(3, a.rows, torch.zeros(3, dtype=torch.int32, device=DEV), a.d_table, a.d_start)
+    wq.wq_cache_write(a.desc, none, K, heads * dim, V, heads * dim, wq.WQ_F32, a.cache)
+    torch.cuda.synchronize()
+    assert torch.equal(a.cache, b.cache)
+
+
+def test_bad_pages(orc):
+    """Tokens whose page is no page are not written and read as zeros; the others are as ever."""
+    c = Case(Q4_0, 64, 2, 32, [100, 64, 10], [100, 64, 33], bad=[(0, 1), (0, 3), (1, 0), (2, 0)])
+    k, v = _values(c, wq.WQ_BF16, "normal")
+    K, V = (_dev(x.reshape(c.rows, -1), wq.WQ_BF16, 0) for x in (k, v))
+    wq.wq_cache_write(c.desc, c.seqs, K, 128, V, 128, wq.WQ_BF16, c.cache)
+    for got, x in zip(_read(c, wq.WQ_BF16), (k, v)):
+        _same(got, _expected(c, x, wq.WQ_BF16, orc), wq.WQ_BF16)
+
+
+def test_lengths_past_the_last_page(orc):
+    """Tokens behind the last table entry are absent; lengths of any size are no fault."""
+    c = Case(Q4_1, 64, 2, 32, [40, 3, 3], [40, 3, 3])
+    k, v = _values(c, wq.WQ_BF16, "normal")
+    K, V = (_dev(x.reshape(c.rows, -1), wq.WQ_BF16, 0) for x in (k, v))
+    wq.wq_cache_write(c.desc, c.seqs, K, 128, V, 128, wq.WQ_BF16, c.cache)
+    torch.cuda.synchronize()
+    before = c.cache.clone()
+    per = c.table.shape[1]
+    for lens in ([per * 32 + 40, 2**31 - 1, -2**31], [-1, -5, 2**31 - 1]):
+        far = wq.seqs(3, c.rows, torch.tensor(lens, dtype=torch.int32, device=DEV), c.d_table, c.d_start)
+        wq.wq_cache_write(c.desc, far, K, 128, V, 128, wq.WQ_BF16, c.cache)
+        for got in _read(c, wq.WQ_BF16, seqs=far):
+            assert not got.any()
+    assert torch.equal(before, c.cache)
+
+
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+def test_extreme_inputs(orc, fmt):
+    """Infinities and magnitudes past the limit are stored as +-32768 (or near it), NaN as -32768; all that is read back is
+    finite, also as fp16, and blocks without such values are untouched by their neighbours."""
+    c = Case(fmt, 128, 1, 32, [6], [6])
+    x = c.rng.standard_normal((6, 1, 128), dtype=np.float32)
+    x[0, 0, 3], x[1, 0, 40], x[2, 0, 70], x[3, 0, 100] = np.inf, -np.inf, np.nan, 3e38
+    x[4, 0, :] = 1e-30
+    K = _dev(x.reshape(6, -1), wq.WQ_F32, 0)
+    wq.wq_cache_write(c.desc, c.seqs, K, 128, K, 128, wq.WQ_F32, c.cache)
+    want = stored(orc, fmt, x).reshape(6, -1)
+    for got in _read(c, wq.WQ_F32):
+        _same(got, want.view(np.uint32), wq.WQ_F32)
+        assert np.isfinite(got.astype(np.float16)).all()
+
+
+def test_without_a_table(orc):
+    """No table: sequence b is page b."""
+    c = Case(Q4_0, 64, 4, 224, [200, 1, 224], [200, 7, 224], paged=False)
+    k, v = _values(c, wq.WQ_BF16, "normal")
+    K, V = (_dev(x.reshape(c.rows, -1), wq.WQ_BF16, 0) for x in (k, v))
+    wq.wq_cache_write(c.desc, c.seqs, K, 256, V, 256, wq.WQ_BF16, c.cache)
+    for got, x in zip(_read(c, wq.WQ_BF16), (k, v)):
+        _same(got, _expected(c, x, wq.WQ_BF16, orc), wq.WQ_BF16)
+
+
+def test_many_sequences(orc):
+    """More sequences than a workgroup has threads, some without rows."""
+    rng = np.random.default_rng(1)
+    counts = [int(n) for n in rng.integers(0, 4, 700)]
+    lens = [n + int(e) for n, e in zip(counts, rng.integers(0, 50, 700))]
+    c = Case(Q4_0, 64, 1, 32, counts, lens)
+    k, v = _values(c, wq.WQ_BF16, "normal")
+    K, V = (_dev(x.reshape(c.rows, -1), wq.WQ_BF16, 0) for x in (k, v))
+    wq.wq_cache_write(c.desc, c.seqs, K, 64, V, 64, wq.WQ_BF16, c.cache)
+    for got, x in zip(_read(c, wq.WQ_BF16), (k, v)):
+        _same(got, _expected(c, x, wq.WQ_BF16, orc), wq.WQ_BF16)
+
+
+def test_offsets_past_32_bits(orc):
+    """A pool of over 4 GiB; the pages in use are its last ones."""
+    d = wq.cache_desc("q4_0", 256, 8, 256, 8700)
+    size = wq.wq_cache_size(d)
+    assert size > 1 << 32
+    cache = torch.empty(size, dtype=torch.uint8, device=DEV)
+    table = torch.tensor([[8699, 8697]], dtype=torch.int32, device=DEV)
+    rng = np.random.default_rng(2)
+    x = bf16_bits_to_f32(f32_to_bf16_bits(rng.standard_normal((300, 8 * 256), dtype=np.float32)))
+    K = _dev(x, wq.WQ_BF16, 0)
+    s = wq.seqs(1, 300, torch.tensor([300], dtype=torch.int32, device=DEV), table,
+                torch.tensor([0, 300], dtype=torch.int32, device=DEV))
+    out = [torch.empty((300, 8 * 256), dtype=torch.float32, device=DEV) for _ in range(2)]
+    wq.wq_cache_write(d, s, K, 2048, K, 2048, wq.WQ_BF16, cache)
+    wq.wq_cache_read(d, s, cache, out[0], 2048, out[1], 2048, wq.WQ_F32)
+    torch.cuda.synchronize()
+    want = stored(orc, Q4_0, x.reshape(300, 8, 256)).reshape(300, -1)
+    for o in out:
+        _same(o.cpu().numpy(), want.view(np.uint32), wq.WQ_F32)
