@@ -1,0 +1,221 @@
+// attn_common.h -- shared by the attention kernels: which rows and tokens a tile has, where a sequence's units are, and
+// the cross-lane and conversion helpers.
+//
+// Both kernels compute the transposed products S^T = K Q^T and Y^T = V^T P^T.  A tile's columns are query rows times the
+// query heads that share a key/value head, so the keys and values of one head serve a whole tile; and a lane's scores
+// after the first product are, in the cache's order of tokens, the lane's operand of the second.
+#pragma once
+
+#include <cfloat>
+
+#include "cache_layout.h"
+#include "wq_device.h"
+#include "wq_launch.h"
+
+namespace wq {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The call's int32 arrays are only read and indexed uniformly: as constant memory they are scalar loads.
+typedef const int32_t __attribute__((address_space(4))) * const_i32;
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int read_const(const int32_t* p, int64_t i) { return ((const_i32)(uintptr_t)p)[i]; }
+
+// Columns per tile: `rows` rows of the sequence times the group's heads, or one row's `ht` runs of heads.
+struct TileShape {
+    int rows, ht;
+};
+__host__ __device__ inline TileShape tile_shape(int cols, int group) {
+    return group <= cols ? TileShape{cols / group, 1} : TileShape{1, (group + cols - 1) / cols};
+}
+// Tiles of a call with `rows` rows and `batch` sequences: at most this many.
+__host__ __device__ inline int64_t tile_bound(const TileShape& ts, int rows, int batch, bool one_row) {
+    if (one_row) return (int64_t)batch * ts.ht;
+    return ((int64_t)rows / ts.rows + (ts.rows > 1 ? (rows < batch ? rows : batch) : 0)) * ts.ht;
+}
+
+// Rows, tokens and units of a sequence.
+struct SeqInfo {
+    int r0, n;        // its rows
+    int tokens;       // in the cache
+    int64_t pos0;     // token of its first row (causal)
+};
+
+__device__ inline SeqInfo seq_info(const AttnArgs& a, int b) {   // b per lane
+    SeqInfo q;
+    int r0, r1;
+    seq_rows(a.s, b, &r0, &r1);
+    q.r0 = r0;
+    q.n = r1 - r0;
+    q.tokens = seq_tokens(a.s, b);
+    q.pos0 = (int64_t)a.s.len[b] - q.n;
+    return q;
+}
+
+// The same for a uniform b, through scalar loads.
+__device__ inline SeqInfo seq_info_uniform(const AttnArgs& a, int b) {
+    const Seqs& s = a.s;
+    SeqInfo q;
+    int r0 = b, r1 = b + 1;
+    if (s.row_start) {
+        r0 = read_const(s.row_start, b);
+        r1 = read_const(s.row_start, b + 1);
+        r0 = r0 < 0 ? 0 : r0 > s.rows ? s.rows : r0;
+        r1 = r1 < r0 ? r0 : r1 > s.rows ? s.rows : r1;
+    }
+    const int len = read_const(s.len, b), cap = s.table_ld * s.page;
+    q.r0 = r0;
+    q.n = r1 - r0;
+    q.tokens = len < 0 ? 0 : len < cap ? len : cap;
+    q.pos0 = (int64_t)len - q.n;
+    return q;
+}
+
+// Tokens [lo, hi) that row i of the sequence sees.
+__device__ inline void row_tokens(const AttnArgs& a, const SeqInfo& q, int i, int* lo, int* hi) {
+    *lo = 0;
+    *hi = q.tokens;
+    if (a.causal) {
+        const int64_t p = q.pos0 + i + 1;
+        *hi = p < 0 ? 0 : p < *hi ? (int)p : *hi;
+        if (a.window > 0 && p > a.window) *lo = p - a.window < *hi ? (int)(p - a.window) : *hi;
+    }
+}
+
+// Units [u0, u1) that hold the tokens of rows [i0, i1) of the sequence.
+__device__ inline void row_units(const AttnArgs& a, const SeqInfo& q, int i0, int i1, int* u0, int* u1) {
+    int lo, hi, x;
+    row_tokens(a, q, i0, &lo, &x);
+    row_tokens(a, q, i1 - 1, &x, &hi);
+    *u0 = lo / kUnit;
+    *u1 = hi > lo ? (hi + kUnit - 1) / kUnit : *u0;
+}
+
+__device__ inline int tiles_of(const TileShape& ts, int n) { return (n + ts.rows - 1) / ts.rows * ts.ht; }
+
+// Inclusive prefix sum over the wave.
+__device__ inline uint32_t wave_scan(uint32_t v) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(v, d, 64);
+        v += (threadIdx.x & 63) >= (unsigned)d ? o : 0;
+    }
+    return v;
+}
+
+// The sequence whose share of a running total contains `target`: weight(b) is sequence b's share.  Returns the total;
+// *seq is -1 if target is not below it, else *seq and the total before it.
+template <class F>
+__device__ inline uint32_t find_seq(int batch, uint32_t target, F weight, int* seq, uint32_t* before) {
+    const int lane = threadIdx.x & 63;
+    uint32_t run = 0;
+    *seq = -1;
+    *before = 0;
+    for (int b0 = 0; b0 < batch; b0 += 64) {
+        const int b = b0 + lane;
+        const uint32_t w = b < batch ? weight(b) : 0;
+        const uint32_t incl = wave_scan(w);
+        const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+        if (*seq < 0 && target - run < sum) {   // run <= target here
+            const int l = __builtin_ctzll(__ballot(incl > target - run));
+            *seq = b0 + l;
+            *before = run + (uint32_t)__builtin_amdgcn_readlane((int)(incl - w), l);
+        }
+        run += sum;
+    }
+    return run;
+}
+
+// Where the units of one head of one sequence are, unit by unit.
+struct UnitWalk {
+    const Seqs* s;
+    int64_t row;     // of the table
+    int h, b;
+    int j, k;        // page and unit within it
+
+    __device__ void start(const Seqs& q, int seq, int head, int unit) {
+        s = &q;
+        b = seq;
+        h = head;
+        row = (int64_t)seq * q.table_ld;
+        j = unit / q.upp;
+        k = unit - j * q.upp;
+    }
+    __device__ void step(int n) {
+        k += n;
+        while (k >= s->upp) {
+            k -= s->upp;
+            j++;
+        }
+    }
+    // byte offset of the unit, or -1
+    __device__ int64_t at() const {
+        if (j >= s->table_ld) return -1;
+        const int64_t p = s->table ? (int64_t)read_const(s->table, row + j) : (int64_t)b;
+        if (p < 0 || p >= s->pages) return -1;
+        return ((p * s->heads + h) * s->upp + k) * s->unit_bytes;
+    }
+};
+
+__device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The codes of a word as fp16 1024 + q, two to a register.  K words: nibbles i and i + 4.
+__device__ inline f16x2 nibble_pair(uint32_t w, int i) {
+    return __builtin_bit_cast(f16x2, ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u);
+}
+// V words (masked to one nibble per byte): bytes 0, 1 or 2, 3.
+__device__ inline f16x2 byte_pair(uint32_t w, int hi) {
+    return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, hi ? 0x04030402u : 0x04010400u));
+}
+// 1024 + q -> the value: (q - 8) d, or q d + m with one rounding.  Both subtractions are exact.
+template <bool Q41>
+__device__ inline f16x2 code_value(f16x2 u, f16x2 d, f16x2 m) {
+    if constexpr (Q41) {
+        const f16x2 c = u - (_Float16)1024.0f;
+        return __builtin_elementwise_fma(c, d, m);
+    } else {
+        const f16x2 c = u - (_Float16)1032.0f;
+        return c * d;
+    }
+}
+__device__ inline f16x2 as_f16x2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+__device__ inline uint32_t pack_f16(float a, float b) { return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b}); }
+__device__ inline uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// Probabilities are held as 2^(x - ref): at most 2^15, the top of fp16, and 2^7 when ref is set, so that ref moves
+// seldom and a probability keeps all of fp16's bits down to 2^-21 of the largest.
+constexpr float kRefBelow = 7.0f, kRefMost = 15.0f;
+
+// Partial results of a sequence that is shared out: [slot][cols][dim] sums, then [slot][cols] (reference, sum of p).
+struct Partials {
+    float* o;
+    float* ml;
+    int dim, cols;
+    __device__ float* sums(int slot, int col) const { return o + ((int64_t)slot * cols + col) * dim; }
+    __device__ float* stat(int slot, int col) const { return ml + ((int64_t)slot * cols + col) * 2; }
+};
+__host__ __device__ inline int64_t partial_bytes(int slots, int cols, int dim) { return (int64_t)slots * cols * (dim + 2) * 4; }
+
+// The query column of a tile: row within the sequence and query head, or no column.
+__device__ inline bool tile_col(const AttnArgs& a, const TileShape& ts, int tile, int col, int n, int* row, int* head) {
+    if (ts.ht == 1) {
+        const int r = col / a.group;
+        *row = tile * ts.rows + r;
+        *head = col - r * a.group;
+        return r < ts.rows && *row < n;
+    }
+    *row = tile / ts.ht;
+    *head = (tile - *row * ts.ht) * a.tile_cols + col;
+    return *head < a.group;
+}
+
+}  // namespace wq
