@@ -11,16 +11,38 @@ namespace wq {
 // Few columns per sequence (single tokens, drafted tokens): tiles of 16 columns, every wave its own units.
 // ---------------------------------------------------------------------------------------------------------------
 
-// One unit's operands in a lane's registers.
+// Each wave keeps a ring of units in LDS, filled by loads that go there directly (no registers), so that several units
+// per wave are on their way while one is computed on.  The unit is contiguous in the cache and keeps its layout.
 template <int NB, bool Q41>
-struct UnitRegs {
-    uint32_t kw[2 * NB], vw[2 * NB];
-    uint32_t kd[2][NB][2], vd[2][NB][2];                            // [tile][block][token pair]
-    uint32_t km[Q41 ? 2 : 1][Q41 ? NB : 1][2], vm[Q41 ? 2 : 1][Q41 ? NB : 1][2];
+struct UnitRing {
+    static constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), bytes = 2 * half, plane = cache_plane_bytes(dim);
+    static constexpr int full = bytes / 1024, rest = bytes % 1024 / 16;   // whole 1 KiB loads, lanes of a last one
+    static constexpr int loads = full + (rest ? 1 : 0);
 };
 
+// The request for one unit: 16 bytes a lane, to LDS at m0 + offset + 16 lane.  The compiler does not see the write (and
+// sets m0 itself where it needs it); the memory clobbers keep LDS reads in order with it, and the counted waits below are the only ones there are for it.
+template <int BYTES>
+__device__ inline void request_unit(const uint8_t* src, uint32_t lds) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t off = lane * 16;
+    constexpr int full = BYTES / 1024, rest = BYTES % 1024 / 16;
+#pragma unroll
+    for (int c = 0; c < full + (rest ? 1 : 0); c++) {
+        if (c < full || lane < rest) {
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                         :: "s"(lds + c * 1024), "v"(off), "s"(src + c * 1024) : "memory");
+        }
+    }
+}
+template <int N>
+__device__ inline void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 template <int NB>
-__device__ inline void load_words(const uint8_t* p, int lane, uint32_t* w) {
+__device__ inline void read_words(const uint8_t* p, int lane, uint32_t* w) {
 #pragma unroll
     for (int c = 0; c < NB / 2; c++) {
         const u32x4 v = *reinterpret_cast<const u32x4*>(p + c * 1024 + lane * 16);
@@ -34,41 +56,27 @@ __device__ inline void load_words(const uint8_t* p, int lane, uint32_t* w) {
     }
 }
 
-template <int NB>
-__device__ inline void load_scales(const uint8_t* p, int g, uint32_t (*d)[NB][2]) {
+// Scales of blocks b0 .. b0 + BG - 1 of one tile: [block][token pair].
+template <int NB, int BG>
+__device__ inline void read_scales(const uint8_t* p, int g, int tile, int b0, uint32_t (&d)[BG][2]) {
+    const uint8_t* q = p + ((tile * 4 + g) * NB + b0) * 8;
+    if constexpr (NB % 2 == 0) {
 #pragma unroll
-    for (int tile = 0; tile < 2; tile++) {
-        const uint8_t* q = p + (tile * 4 + g) * NB * 8;
-        if constexpr (NB % 2 == 0) {
+        for (int b = 0; b < BG; b += 2) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(q + b * 8);
+            d[b][0] = v[0];
+            d[b][1] = v[1];
+            d[b + 1][0] = v[2];
+            d[b + 1][1] = v[3];
+        }
+    } else {
 #pragma unroll
-            for (int b = 0; b < NB; b += 2) {
-                const u32x4 v = *reinterpret_cast<const u32x4*>(q + b * 8);
-                d[tile][b][0] = v[0];
-                d[tile][b][1] = v[1];
-                d[tile][b + 1][0] = v[2];
-                d[tile][b + 1][1] = v[3];
-            }
-        } else {
-#pragma unroll
-            for (int b = 0; b < NB; b++) {
-                const u32x2 v = *reinterpret_cast<const u32x2*>(q + b * 8);
-                d[tile][b][0] = v[0];
-                d[tile][b][1] = v[1];
-            }
+        for (int b = 0; b < BG; b++) {
+            const u32x2 v = *reinterpret_cast<const u32x2*>(q + b * 8);
+            d[b][0] = v[0];
+            d[b][1] = v[1];
         }
     }
-}
-
-template <int NB, bool Q41>
-__device__ inline void load_unit(const uint8_t* p, int lane, UnitRegs<NB, Q41>* r) {
-    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), plane = cache_plane_bytes(dim);
-    const int g = lane >> 4;
-    load_words<NB>(p, lane, r->kw);
-    load_scales<NB>(p + 16 * dim, g, r->kd);
-    if constexpr (Q41) load_scales<NB>(p + 16 * dim + plane, g, r->km);
-    load_words<NB>(p + half, lane, r->vw);
-    load_scales<NB>(p + half + 16 * dim, g, r->vd);
-    if constexpr (Q41) load_scales<NB>(p + half + 16 * dim + plane, g, r->vm);
 }
 
 // A column's running softmax and its part of the sums.
@@ -80,29 +88,36 @@ struct ColState {
 
 // K codes are multiplied as the bf16 integers 128 + q, exact, with the sum's start at -(128 + 8) sum q (q4_0; -128 sum q
 // for q4_1), so that a block's product is the exact-code sum in fp32, and its fp16 scale is applied after it.
-template <int NB, bool Q41>
-__device__ inline void unit_step(const UnitRegs<NB, Q41>& r, const bf16x8 (&qf)[NB], const float (&c0)[NB], float sl2, int t0,
-                                 int lo, int hi, int tokens, bool masked, ColState<NB>* st) {
-    const int g = (threadIdx.x & 63) >> 4;
+template <int NB, bool Q41, bool MASKED>
+__device__ inline void unit_step(const uint8_t* unit, const bf16x8 (&qf)[NB], const float (&c0)[NB], float sl2, int t0, int lo,
+                                 int hi, int tokens, uint32_t bf128, ColState<NB>* st) {
+    using R = UnitRing<NB, Q41>;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
     float x[8];
+    uint32_t kw[2 * NB];
+    read_words<NB>(unit, lane, kw);
 #pragma unroll
     for (int tile = 0; tile < 2; tile++) {
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t kd[NB][2], km[NB][2];
+        if (NB > 4 && tile) asm volatile("" ::: "memory");
+        read_scales<NB, NB>(unit + 16 * R::dim, g, tile, 0, kd);
+        if constexpr (Q41) read_scales<NB, NB>(unit + 16 * R::dim + R::plane, g, tile, 0, km);
 #pragma unroll
         for (int b = 0; b < NB; b++) {
-            const uint32_t w = r.kw[tile * NB + b];
+            const uint32_t w = kw[tile * NB + b];
             u32x4 u;
 #pragma unroll
-            for (int i = 0; i < 4; i++) u[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+            for (int i = 0; i < 4; i++) u[i] = nibble_pair(w, i, bf128);
             const f32x4 c = {c0[b], c0[b], c0[b], c0[b]};
             const f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, u), qf[b], c, 0, 0, 0);
-            const f16x2 d01 = as_f16x2(r.kd[tile][b][0]), d23 = as_f16x2(r.kd[tile][b][1]);
+            const f16x2 d01 = as_f16x2(kd[b][0]), d23 = as_f16x2(kd[b][1]);
             s[0] = fmaf((float)d01[0], p[0], s[0]);
             s[1] = fmaf((float)d01[1], p[1], s[1]);
             s[2] = fmaf((float)d23[0], p[2], s[2]);
             s[3] = fmaf((float)d23[1], p[3], s[3]);
             if constexpr (Q41) {
-                const f16x2 m01 = as_f16x2(r.km[tile][b][0]), m23 = as_f16x2(r.km[tile][b][1]);
+                const f16x2 m01 = as_f16x2(km[b][0]), m23 = as_f16x2(km[b][1]);
                 const float sx = c0[b] * -0.0078125f;   // sum q over the block
                 s[0] = fmaf((float)m01[0], sx, s[0]);
                 s[1] = fmaf((float)m01[1], sx, s[1]);
@@ -111,19 +126,24 @@ __device__ inline void unit_step(const UnitRegs<NB, Q41>& r, const bf16x8 (&qf)[
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++) x[4 * tile + i] = s[i] * sl2;
+        for (int i = 0; i < 4; i++) x[4 * tile + i] = s[i];
     }
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};    // token pairs that are in the cache: what lies behind them is anything
-    if (masked) {
+    float e[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
+    for (int j = 0; j < 8; j++) {
+        e[j] = fmaf(x[j], sl2, -st->ref);
+        if constexpr (MASKED) {
             const int t = t0 + (j >> 2) * 16 + 4 * g + (j & 3);
-            x[j] = t >= lo && t < hi ? x[j] : -INFINITY;
+            e[j] = t >= lo && t < hi ? e[j] : -INFINITY;
             if (t >= tokens) keep[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
         }
     }
-    float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    if (__any(mx - st->ref > kRefMost)) {
+    const float most = fmaxf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])), fmaxf(fmaxf(e[4], e[5]), fmaxf(e[6], e[7])));
+    if (__any(most > kRefMost)) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; j++) mx = fmaxf(mx, e[j] == -INFINITY ? -INFINITY : x[j] * sl2);
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         const float ref = fmaxf(st->ref, mx - kRefBelow);
@@ -132,31 +152,48 @@ __device__ inline void unit_step(const UnitRegs<NB, Q41>& r, const bf16x8 (&qf)[
         for (int i = 0; i < 2 * NB; i++) st->o[i] *= alpha;
         st->l *= alpha;
         st->ref = ref;
+#pragma unroll
+        for (int j = 0; j < 8; j++) e[j] = e[j] == -INFINITY ? -INFINITY : fmaf(x[j], sl2, -ref);
     }
     u32x4 p;
 #pragma unroll
-    for (int j = 0; j < 8; j++) x[j] = exp2_fast(x[j] - st->ref);
+    for (int j = 0; j < 8; j++) x[j] = exp2_fast(e[j]);
     st->l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 #pragma unroll
     for (int j = 0; j < 4; j++) p[j] = pack_f16(x[2 * j], x[2 * j + 1]);
     const f16x8 pf = __builtin_bit_cast(f16x8, p);
+    // (at most four blocks' scales in registers at a time)
+    constexpr int BG = NB > 4 ? 4 : NB;
 #pragma unroll
-    for (int b = 0; b < NB; b++) {
-        u32x4 vlo, vhi;
+    for (int b0 = 0; b0 < NB; b0 += BG) {
+        if (b0 > 0) asm volatile("" ::: "memory");
+        uint32_t vw[2 * BG], vd[2][BG][2], vm[2][BG][2];
+        read_words<BG>(unit + R::half + b0 * 512, lane, vw);
 #pragma unroll
         for (int tile = 0; tile < 2; tile++) {
-            const uint32_t w = r.vw[2 * b + tile], wl = w & 0x0F0F0F0Fu, wh = (w >> 4) & 0x0F0F0F0Fu;
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const f16x2 d = as_f16x2(r.vd[tile][b][i] & keep[2 * tile + i]);
-                f16x2 m = {};
-                if constexpr (Q41) m = as_f16x2(r.vm[tile][b][i] & keep[2 * tile + i]);
-                vlo[2 * tile + i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wl, i), d, m));
-                vhi[2 * tile + i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wh, i), d, m));
-            }
+            read_scales<NB, BG>(unit + R::half + 16 * R::dim, g, tile, b0, vd[tile]);
+            if constexpr (Q41) read_scales<NB, BG>(unit + R::half + 16 * R::dim + R::plane, g, tile, b0, vm[tile]);
         }
-        st->o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vlo), pf, st->o[2 * b], 0, 0, 0);
-        st->o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vhi), pf, st->o[2 * b + 1], 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < BG; b++) {
+            u32x4 vlo, vhi;
+#pragma unroll
+            for (int tile = 0; tile < 2; tile++) {
+                const uint32_t w = vw[2 * b + tile], wl = w & 0x0F0F0F0Fu, wh = (w >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const uint32_t in = MASKED ? keep[2 * tile + i] : ~0u;
+                    const f16x2 d = as_f16x2(vd[tile][b][i] & in);
+                    f16x2 m = {};
+                    if constexpr (Q41) m = as_f16x2(vm[tile][b][i] & in);
+                    vlo[2 * tile + i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wl, i), d, m));
+                    vhi[2 * tile + i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wh, i), d, m));
+                }
+            }
+            f32x4* const o = st->o + 2 * (b0 + b);
+            o[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vlo), pf, o[0], 0, 0, 0);
+            o[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vhi), pf, o[1], 0, 0, 0);
+        }
     }
 }
 
@@ -180,12 +217,32 @@ __device__ inline uint32_t work_share(uint32_t total, int workgroups, int least)
     return s > (uint32_t)least ? s : (uint32_t)least;
 }
 
+struct SpanWeight {
+    const AttnArgs& a;
+    TileShape ts;
+    __device__ uint32_t operator()(int b) const {
+        const SeqInfo q = seq_info(a, b);
+        int u0;
+        return (uint32_t)(tiles_of(ts, q.n) * a.s.heads * span_units(a, q, &u0));
+    }
+};
+struct TokenShare {
+    SeqTotals<SpanWeight> t;
+    uint32_t total, share;
+    __device__ TokenShare(const AttnArgs& a, const TileShape& ts) : t(a.s.batch, SpanWeight{a, ts}) {
+        total = t.total();
+        share = work_share(total, a.workgroups, a.least_units);
+    }
+};
+
 // A tile's columns x units [ua, ub) of one head, by the workgroup.  part: where the sums go (null: the tile is whole,
 // and y is written).
-template <int NB, bool Q41, int NW>
+template <int NB, bool Q41, int NW, int D>
 __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqInfo& q, int seq, int tile, int h, int ua, int ub,
-                              float* part_o, float* part_ml, float* lds_o, float* lds_f) {
+                              float* part_o, float* part_ml, uint8_t* lds) {
     constexpr int dim = 32 * NB, ld = dim + 4;
+    float* const lds_o = reinterpret_cast<float*>(lds);
+    float* const lds_f = lds_o + NW * 16 * ld;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), g = lane >> 4, col = lane & 15;
     int row, head;
     const bool valid = tile_col(a, ts, tile, col, q.n, &row, &head);
@@ -195,6 +252,25 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
     row_tokens(a, q, first, &x, &hi_least);
     row_tokens(a, q, last, &lo_most, &x);
 
+    constexpr int bytes = UnitRing<NB, Q41>::bytes, loads = UnitRing<NB, Q41>::loads;
+    const uint8_t* const ring = lds + wave * D * bytes;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)ring;
+    const int n = ub > ua + wave ? (ub - ua - wave + NW - 1) / NW : 0;   // this wave's units: ua + wave + NW i
+    UnitWalk walk;
+    walk.start(a.s, seq, h, ua + wave);
+    uint32_t absent = 0;    // bit i % 32: unit i's page is none; its request is then any unit, for the count
+    int put = 0, get = 0;   // byte offsets of the slots to fill and to read next
+    const auto next = [](int at) { return at + bytes == D * bytes ? 0 : at + bytes; };
+    const auto request = [&](int i) {
+        const int64_t at = walk.at();
+        walk.step(NW);
+        request_unit<bytes>(a.cache + (at < 0 ? 0 : at), uniform(ring_at + put));
+        put = next(put);
+        absent = at < 0 ? absent | 1u << (i & 31) : absent & ~(1u << (i & 31));
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; i++)
+        if (i < n) request(i);
     bf16x8 qf[NB];
     const uint16_t* qp = a.q + (int64_t)(q.r0 + row) * a.ldq + (int64_t)(h * a.group + head) * dim + 8 * g;
 #pragma unroll
@@ -217,45 +293,30 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
         for (int b = 0; b < NB; b++) c0[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qf[b], (f32x4){0, 0, 0, 0}, 0, 0, 0)[0];
     }
 
+    const uint32_t bf128 = held(0x43004300u);
     ColState<NB> st;
 #pragma unroll
     for (int i = 0; i < 2 * NB; i++) st.o[i] = (f32x4){0, 0, 0, 0};
     st.ref = -FLT_MAX;
     st.l = 0.0f;
 
-    int u = ua + wave;
-    if (u < ub) {
-        UnitWalk walk;
-        walk.start(a.s, seq, h, u);
-        UnitRegs<NB, Q41> A, B;
-        int64_t at = walk.at();
-        if (at >= 0) load_unit<NB, Q41>(a.cache + at, lane, &A);
-        const auto step = [&](const UnitRegs<NB, Q41>& r, int unit) {
-            const int t0 = unit * kUnit;
-            const bool masked = t0 < lo_most || t0 + kUnit > hi_least;
-            unit_step<NB, Q41>(r, qf, c0, a.scale_log2, t0, lo, hi, q.tokens, masked, &st);
-        };
-        while (true) {
-            int64_t at2 = -1;
-            if (u + NW < ub) {
-                walk.step(NW);
-                at2 = walk.at();
-                if (at2 >= 0) load_unit<NB, Q41>(a.cache + at2, lane, &B);
-            }
-            if (at >= 0) step(A, u);
-            u += NW;
-            if (u >= ub) break;
-            at = -1;
-            if (u + NW < ub) {
-                walk.step(NW);
-                at = walk.at();
-                if (at >= 0) load_unit<NB, Q41>(a.cache + at, lane, &A);
-            }
-            if (at2 >= 0) step(B, u);
-            u += NW;
-            if (u >= ub) break;
+    for (int i = 0; i < n; i++) {
+        if (i + D - 1 < n) {
+            wait_lds();     // unit i - 1's reads, whose slot the request fills
+            request(i + D - 1);
+            wait_loads<(D - 1) * loads>();
+        } else {
+            wait_loads<0>();
         }
+        const int t0 = (ua + wave + NW * i) * kUnit;
+        const bool masked = t0 < lo_most || t0 + kUnit > hi_least;
+        if (!(absent >> (i & 31) & 1)) {
+            if (masked) unit_step<NB, Q41, true>(ring + get, qf, c0, a.scale_log2, t0, lo, hi, q.tokens, bf128, &st);
+            else unit_step<NB, Q41, false>(ring + get, qf, c0, a.scale_log2, t0, lo, hi, q.tokens, bf128, &st);
+        }
+        get = next(get);
     }
+    __syncthreads();   // the rings' space is the join's now
 
     // the waves' sums, joined in LDS
     st.l += __shfl_xor(st.l, 16, 64);
@@ -301,24 +362,26 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
 // Sequences shared out evenly: workgroup i takes units [i share, (i + 1) share) of the call's work, whatever the lengths
 // are; a tile that more than one workgroup has a part of is joined by k_attn_join.  With `splits` 0 every workgroup has
 // one whole tile.
-template <int NB, bool Q41, int NW>
-__global__ __launch_bounds__(NW * 64) void k_attn_token(AttnArgs a) {
-    __shared__ float lds_o[NW * 16 * (32 * NB + 4)];
-    __shared__ float lds_f[2 * NW * 16];
+template <int NB, bool Q41, int NW, int D>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_token(AttnArgs a) {
+    constexpr int ring_bytes = NW * D * UnitRing<NB, Q41>::bytes, join_bytes = NW * 16 * (32 * NB + 4 + 2) * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[ring_bytes > join_bytes ? ring_bytes : join_bytes];
     const TileShape ts = tile_shape(kTokenCols, a.group);
     const int heads = a.s.heads;
     if (a.workgroups == 0) {
         const int item = blockIdx.x;
-        int seq = -1;
-        uint32_t before = 0;
+        int seq;
+        uint32_t before;
         if (!a.s.row_start) {
             seq = item / (ts.ht * heads);
             before = seq * (ts.ht * heads);
         } else {
-            find_seq(a.s.batch, item, [&](int b) { int r0, r1; seq_rows(a.s, b, &r0, &r1); return (uint32_t)(tiles_of(ts, r1 - r0) * heads); },
-                     &seq, &before);
-            seq = uniform(seq);
-            before = uniform(before);
+            const auto count = [&](int b) {
+                int r0, r1;
+                seq_rows(a.s, b, &r0, &r1);
+                return (uint32_t)(tiles_of(ts, r1 - r0) * heads);
+            };
+            seq = SeqTotals(a.s.batch, count).find(item, &before);
         }
         if (seq < 0 || seq >= a.s.batch) return;
         const SeqInfo q = seq_info_uniform(a, seq);
@@ -327,24 +390,14 @@ __global__ __launch_bounds__(NW * 64) void k_attn_token(AttnArgs a) {
         if (first >= end) return;
         int u0, u1;
         row_units(a, q, first, end, &u0, &u1);
-        token_segment<NB, Q41, NW>(a, ts, q, seq, tile, h, u0, u1, nullptr, nullptr, lds_o, lds_f);
+        token_segment<NB, Q41, NW, D>(a, ts, q, seq, tile, h, u0, u1, nullptr, nullptr, lds);
         return;
     }
-    const auto weight = [&](int b) {
-        const SeqInfo q = seq_info(a, b);
-        int u0;
-        return (uint32_t)(tiles_of(ts, q.n) * heads * span_units(a, q, &u0));
-    };
-    int seq;
-    uint32_t before;
-    const uint32_t total = find_seq(a.s.batch, 0u, weight, &seq, &before);
-    const uint32_t share = work_share(total, a.workgroups, a.least_units);
-    uint32_t w = blockIdx.x * share;
-    const uint32_t end = min(w + share, total);
+    const TokenShare sh(a, ts);
+    uint32_t w = blockIdx.x * sh.share, before;
+    const uint32_t end = min(w + sh.share, sh.total);
     if (w >= end) return;
-    find_seq(a.s.batch, w, weight, &seq, &before);
-    seq = uniform(seq);
-    before = uniform(before);
+    int seq = sh.t.find(w, &before);
     while (w < end) {
         const SeqInfo q = seq_info_uniform(a, seq);
         int u0;
@@ -356,15 +409,14 @@ __global__ __launch_bounds__(NW * 64) void k_attn_token(AttnArgs a) {
             float *po = nullptr, *pm = nullptr;
             if (s1 - s0 < span) {
                 const int slot = 2 * blockIdx.x + (s0 > 0 ? 0 : 1);
-                const Partials p = {reinterpret_cast<float*>(a.ws), reinterpret_cast<float*>(a.ws) + (int64_t)2 * a.workgroups * kTokenCols * a.dim,
-                                    a.dim, kTokenCols};
+                const Partials p(a);
                 po = p.sums(slot, 0);
                 pm = p.stat(slot, 0);
             }
             // (a span of one unit stands for none where the rows see nothing)
             int r0, r1;
             row_units(a, q, 0, q.n, &r0, &r1);
-            token_segment<NB, Q41, NW>(a, ts, q, seq, tile, h, u0 + s0, min(u0 + s1, r1), po, pm, lds_o, lds_f);
+            token_segment<NB, Q41, NW, D>(a, ts, q, seq, tile, h, u0 + s0, min(u0 + s1, r1), po, pm, lds);
             w += s1 - s0;
         }
         before += items * span;
@@ -372,65 +424,62 @@ __global__ __launch_bounds__(NW * 64) void k_attn_token(AttnArgs a) {
     }
 }
 
-// Joins the parts of a shared-out tile: y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i, in order.  One wave
-// per column.
-__device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, int col, uint16_t* y, int first_slot, int step) {
-    const int lane = threadIdx.x & 63;
-    const auto slot = [&](int i) { return i == 0 ? first_slot : first_slot - (step == 2 ? 1 : 0) + step * i; };
+// Joins the parts of a shared-out tile: y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  One workgroup per
+// column: thread (w, c) sums channels 4 c .. 4 c + 3 of parts w, w + 4, ..., and the four sums meet in LDS, in order.
+__device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, int col, uint16_t* y, int first_slot, int next_slot,
+                                   int step, float* lds) {
+    const int tid = threadIdx.x, c = tid & 63, w = tid >> 6;
+    const auto slot = [&](int i) { return i == 0 ? first_slot : next_slot + step * (i - 1); };
     float ref = -FLT_MAX;
-    for (int i = lane; i < n; i += 64) ref = fmaxf(ref, p.stat(slot(i), col)[0]);
+    for (int i = c; i < n; i += 64) ref = fmaxf(ref, p.stat(slot(i), col)[0]);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) ref = fmaxf(ref, __shfl_xor(ref, d, 64));
-    float l = 0.0f, o[4] = {};
-    for (int i = 0; i < n; i++) {
+    float l = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    const bool mine = 4 * c < a.dim;
+#pragma unroll 4
+    for (int i = w; i < n; i += 4) {
         const float* st = p.stat(slot(i), col);
         const float f = exp2_fast(st[0] - ref);
         l += f * st[1];
-        const float* s = p.sums(slot(i), col);
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (lane + 64 * j < a.dim) o[j] += f * s[lane + 64 * j];
+        if (mine) o += f * *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
     }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    if (mine) *reinterpret_cast<f32x4*>(lds + (w * 64 + c) * 4) = o;
+    if (c == 0) lds[1024 + w] = l;
+    __syncthreads();
+    if (w == 0 && mine) {
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-        if (lane + 64 * j < a.dim) y[lane + 64 * j] = __builtin_bit_cast(uint16_t, (__bf16)(o[j] * inv));
+        for (int k = 1; k < 4; k++) {
+            o += *reinterpret_cast<const f32x4*>(lds + (k * 64 + c) * 4);
+            l += lds[1024 + k];
+        }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        *reinterpret_cast<u32x2*>(y + 4 * c) = (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+    }
 }
 
+// Workgroup (i, column): the tile, if there is one, that workgroup i began and did not end.
 __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
+    __shared__ __attribute__((aligned(16))) float lds[1024 + 4];
     const TileShape ts = tile_shape(kTokenCols, a.group);
-    const int heads = a.s.heads, wave = uniform(threadIdx.x >> 6);
-    const uint32_t item = blockIdx.x;
-    const auto weight = [&](int b) {
-        const SeqInfo q = seq_info(a, b);
-        int u0;
-        return (uint32_t)(tiles_of(ts, q.n) * heads * span_units(a, q, &u0));
-    };
-    const auto count = [&](int b) { int r0, r1; seq_rows(a.s, b, &r0, &r1); return (uint32_t)(tiles_of(ts, r1 - r0) * heads); };
-    int seq, other;
-    uint32_t before, items_before, x;
-    find_seq(a.s.batch, item, count, &seq, &items_before);
-    seq = uniform(seq);
-    if (seq < 0) return;
-    // the total, and what comes before this sequence
-    const uint32_t total = find_seq(a.s.batch, 0u, weight, &other, &x);
-    before = find_seq(seq, 0u, weight, &other, &x);
-    const uint32_t share = work_share(total, a.workgroups, a.least_units);
+    const int heads = a.s.heads, col = blockIdx.y;
+    const TokenShare sh(a, ts);
+    const uint32_t edge = (blockIdx.x + 1) * sh.share;
+    if (edge >= sh.total) return;
+    uint32_t before;
+    const int seq = sh.t.find(edge, &before);
     const SeqInfo q = seq_info_uniform(a, seq);
     int u0;
-    const uint32_t span = span_units(a, q, &u0), in = item - uniform(items_before);
-    const uint32_t w0 = before + in * span, w1 = w0 + span;
-    const int i0 = w0 / share, i1 = (w1 - 1) / share;
-    if (i0 == i1) return;
+    const uint32_t span = span_units(a, q, &u0), in = (edge - before) / span, w0 = before + in * span;
+    if (w0 == edge || w0 < blockIdx.x * sh.share) return;
+    const int parts = (w0 + span - 1) / sh.share - blockIdx.x + 1;
     const int tile = in / heads, h = in - tile * heads;
-    const Partials p = {reinterpret_cast<float*>(a.ws), reinterpret_cast<float*>(a.ws) + (int64_t)2 * a.workgroups * kTokenCols * a.dim, a.dim,
-                        kTokenCols};
-    const int first = 2 * i0 + 1;   // the part that starts the tile; the others start their workgroups
-    for (int col = wave; col < kTokenCols; col += 4) {
-        int row, head;
-        if (!tile_col(a, ts, tile, col, q.n, &row, &head)) continue;
-        join_column(a, p, i1 - i0 + 1, col, a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * a.dim, first, 2);
-    }
+    int row, head;
+    if (!tile_col(a, ts, tile, col, q.n, &row, &head)) return;
+    const Partials p(a);
+    // the first part is the one that starts the tile, the others start their workgroups
+    const int first = 2 * blockIdx.x + 1;
+    join_column(a, p, parts, col, a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * a.dim, first, first + 1, 2, lds);
 }
 
 namespace {
@@ -449,10 +498,10 @@ int share_workgroups(const AttnArgs& a) {
     return kShareWorkgroups;
 }
 
-template <int NB, int NW>
+template <int NB, int NW, int D>
 void launch_token(const AttnArgs& a, dim3 grid, hipStream_t s) {
-    if (a.q41) hipLaunchKernelGGL((k_attn_token<NB, true, NW>), grid, dim3(NW * 64), 0, s, a);
-    else hipLaunchKernelGGL((k_attn_token<NB, false, NW>), grid, dim3(NW * 64), 0, s, a);
+    if (a.q41) hipLaunchKernelGGL((k_attn_token<NB, true, NW, D>), grid, dim3(NW * 64), 0, s, a);
+    else hipLaunchKernelGGL((k_attn_token<NB, false, NW, D>), grid, dim3(NW * 64), 0, s, a);
 }
 
 }  // namespace
@@ -466,16 +515,18 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     a.tile_cols = kTokenCols;
     a.workgroups = a.ws ? share_workgroups(a) : 0;
     a.least_units = kShareLeast;
+    a.slots = 2 * a.workgroups;
     const TileShape ts = tile_shape(kTokenCols, a.group);
     const int64_t items = tile_bound(ts, a.s.rows, a.s.batch, !a.s.row_start) * a.s.heads;
     const dim3 grid((unsigned)(a.workgroups ? a.workgroups : items));
     switch (a.dim) {
-    case 64: launch_token<2, 4>(a, grid, s); break;
-    case 96: launch_token<3, 4>(a, grid, s); break;
-    case 128: launch_token<4, 4>(a, grid, s); break;
-    default: launch_token<8, 4>(a, grid, s); break;
+    case 64: launch_token<2, 4, 4>(a, grid, s); break;
+    case 96: launch_token<3, 4, 3>(a, grid, s); break;
+    case 128: launch_token<4, 4, 3>(a, grid, s); break;
+    default: launch_token<8, 4, 2>(a, grid, s); break;
     }
-    if (a.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3((unsigned)items), dim3(256), 0, s, a);
+    const int cols = std::min(kTokenCols, (a.s.row_start ? ts.rows : 1) * a.group);   // that a tile can have
+    if (a.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3(a.workgroups - 1, cols), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

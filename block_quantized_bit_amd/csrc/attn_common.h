@@ -109,66 +109,109 @@ __device__ inline uint32_t wave_scan(uint32_t v) {
     return v;
 }
 
-// The sequence whose share of a running total contains `target`: weight(b) is sequence b's share.  Returns the total;
-// *seq is -1 if target is not below it, else *seq and the total before it.
+// Running totals over the sequences of a call: weight(b) is sequence b's share (b per lane).  The first 64 sequences'
+// shares stay in registers, so that a call of at most 64 reads their lengths once for all questions.
 template <class F>
-__device__ inline uint32_t find_seq(int batch, uint32_t target, F weight, int* seq, uint32_t* before) {
-    const int lane = threadIdx.x & 63;
-    uint32_t run = 0;
-    *seq = -1;
-    *before = 0;
-    for (int b0 = 0; b0 < batch; b0 += 64) {
-        const int b = b0 + lane;
-        const uint32_t w = b < batch ? weight(b) : 0;
-        const uint32_t incl = wave_scan(w);
-        const uint32_t sum = (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
-        if (*seq < 0 && target - run < sum) {   // run <= target here
-            const int l = __builtin_ctzll(__ballot(incl > target - run));
-            *seq = b0 + l;
-            *before = run + (uint32_t)__builtin_amdgcn_readlane((int)(incl - w), l);
-        }
-        run += sum;
-    }
-    return run;
-}
+struct SeqTotals {
+    F weight;
+    int batch;
+    uint32_t w, incl;   // of sequence `lane`
 
-// Where the units of one head of one sequence are, unit by unit.
+    __device__ SeqTotals(int n, F f) : weight(f), batch(n) {
+        const int lane = threadIdx.x & 63;
+        w = lane < n ? weight(lane) : 0;
+        incl = wave_scan(w);
+    }
+    static __device__ uint32_t last(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+    __device__ uint32_t total() const {
+        uint32_t run = last(incl);
+        for (int b0 = 64; b0 < batch; b0 += 64) {
+            const int b = b0 + (threadIdx.x & 63);
+            run += last(wave_scan(b < batch ? weight(b) : 0));
+        }
+        return run;
+    }
+    // The sequence whose share contains `target` (below the total), and the total before it; -1 if there is none.
+    __device__ int find(uint32_t target, uint32_t* before) const {
+        uint32_t run = 0, v = w, in = incl;
+        for (int b0 = 0; b0 < batch; b0 += 64) {
+            if (b0 > 0) {
+                const int b = b0 + (threadIdx.x & 63);
+                v = b < batch ? weight(b) : 0;
+                in = wave_scan(v);
+            }
+            const uint32_t sum = last(in);
+            if (target - run < sum) {
+                const int l = __builtin_ctzll(__ballot(in > target - run));
+                *before = run + (uint32_t)__builtin_amdgcn_readlane((int)(in - v), l);
+                return b0 + l;
+            }
+            run += sum;
+        }
+        *before = run;
+        return -1;
+    }
+};
+
+// Where the units of one head of one sequence are, unit by unit.  The table entry of the next unit is requested a step
+// before it is used.
 struct UnitWalk {
-    const Seqs* s;
-    int64_t row;     // of the table
-    int h, b;
-    int j, k;        // page and unit within it
+    const int32_t* table;   // this sequence's row, or null
+    int upp, table_ld;
+    int j, k;               // page and unit within it
+    int64_t pages, head_units, unit_bytes, per_page;
+    int entry;              // of page j
 
     __device__ void start(const Seqs& q, int seq, int head, int unit) {
-        s = &q;
-        b = seq;
-        h = head;
-        row = (int64_t)seq * q.table_ld;
-        j = unit / q.upp;
-        k = unit - j * q.upp;
+        upp = q.upp;
+        table_ld = q.table_ld;
+        table = q.table ? q.table + (int64_t)seq * q.table_ld : nullptr;
+        pages = q.pages;
+        unit_bytes = q.unit_bytes;
+        per_page = (int64_t)q.heads * q.upp;
+        head_units = (int64_t)head * q.upp;
+        j = unit / upp;
+        k = unit - j * upp;
+        entry = seq;
+        read();
+    }
+    __device__ void read() {
+        if (table) entry = j < table_ld ? read_const(table, j) : -1;
+        else if (j > 0) entry = -1;
     }
     __device__ void step(int n) {
         k += n;
-        while (k >= s->upp) {
-            k -= s->upp;
-            j++;
+        if (k >= upp) {
+            do {
+                k -= upp;
+                j++;
+            } while (k >= upp);
+            read();
         }
     }
     // byte offset of the unit, or -1
     __device__ int64_t at() const {
-        if (j >= s->table_ld) return -1;
-        const int64_t p = s->table ? (int64_t)read_const(s->table, row + j) : (int64_t)b;
-        if (p < 0 || p >= s->pages) return -1;
-        return ((p * s->heads + h) * s->upp + k) * s->unit_bytes;
+        return entry >= 0 && entry < pages ? ((int64_t)entry * per_page + head_units + k) * unit_bytes : -1;
     }
 };
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The codes of a word as fp16 1024 + q, two to a register.  K words: nibbles i and i + 4.
-__device__ inline f16x2 nibble_pair(uint32_t w, int i) {
-    return __builtin_bit_cast(f16x2, ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u);
+// (w & mask) | bits in one instruction: with both as literals the compiler spends two (an instruction takes one literal).
+__device__ inline uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(bits));
+    return r;
 }
+// A constant in a register.
+__device__ inline uint32_t held(uint32_t c) {
+    uint32_t r = c;
+    asm("" : "+v"(r));
+    return r;
+}
+// The codes of a word, two to a register, nibbles i and i + 4, under the bits of a number whose last place is 1
+// (fp16 1024: 0x64006400, bf16 128: 0x43004300).
+__device__ inline uint32_t nibble_pair(uint32_t w, int i, uint32_t bits) { return and_or(w >> (4 * i), 0x000F000Fu, bits); }
 // V words (masked to one nibble per byte): bytes 0, 1 or 2, 3.
 __device__ inline f16x2 byte_pair(uint32_t w, int hi) {
     return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, hi ? 0x04030402u : 0x04010400u));
@@ -200,6 +243,8 @@ struct Partials {
     float* o;
     float* ml;
     int dim, cols;
+    __device__ explicit Partials(const AttnArgs& a)
+        : o(reinterpret_cast<float*>(a.ws)), ml(o + (int64_t)a.slots * a.tile_cols * a.dim), dim(a.dim), cols(a.tile_cols) {}
     __device__ float* sums(int slot, int col) const { return o + ((int64_t)slot * cols + col) * dim; }
     __device__ float* stat(int slot, int col) const { return ml + ((int64_t)slot * cols + col) * 2; }
 };
