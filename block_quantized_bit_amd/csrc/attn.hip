@@ -424,45 +424,66 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
     }
 }
 
-// Joins the parts of a shared-out tile: y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  One workgroup per
-// column: thread (w, c) sums channels 4 c .. 4 c + 3 of parts w, w + 4, ..., and the four sums meet in LDS, in order.
-__device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, int col, uint16_t* y, int first_slot, int next_slot,
-                                   int step, float* lds) {
-    const int tid = threadIdx.x, c = tid & 63, w = tid >> 6;
-    const auto slot = [&](int i) { return i == 0 ? first_slot : next_slot + step * (i - 1); };
-    float ref = -FLT_MAX;
-    for (int i = c; i < n; i += 64) ref = fmaxf(ref, p.stat(slot(i), col)[0]);
+// Joins the parts of a tile's column: y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  Every thread sums four
+// channels of some of the parts; their sums meet in LDS, in order.
+constexpr int kJoinParts = 512;
+struct JoinLds {
+    float f[kJoinParts], red[4], sum[1024];
+};
+template <class F>
+__device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, int col, uint16_t* y, F slot, JoinLds& lds) {
+    const int tid = threadIdx.x, quads = a.dim / 4, groups = 256 / quads, gr = tid / quads, c = tid - gr * quads;
+    float ref = -FLT_MAX, m0[2], l0[2];
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int i = tid + 256 * k;
+        m0[k] = -FLT_MAX;
+        l0[k] = 0.0f;
+        if (i < n) {
+            const float* st = p.stat(slot(i), col);
+            m0[k] = st[0];
+            l0[k] = st[1];
+        }
+        ref = fmaxf(ref, m0[k]);
+    }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) ref = fmaxf(ref, __shfl_xor(ref, d, 64));
-    float l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-    const bool mine = 4 * c < a.dim;
-#pragma unroll 4
-    for (int i = w; i < n; i += 4) {
-        const float* st = p.stat(slot(i), col);
-        const float f = exp2_fast(st[0] - ref);
-        l += f * st[1];
-        if (mine) o += f * *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
-    }
-    if (mine) *reinterpret_cast<f32x4*>(lds + (w * 64 + c) * 4) = o;
-    if (c == 0) lds[1024 + w] = l;
+    __syncthreads();                          // (the last column's reads of lds are done)
+    if ((tid & 63) == 0) lds.red[tid >> 6] = ref;
     __syncthreads();
-    if (w == 0 && mine) {
+    ref = fmaxf(fmaxf(lds.red[0], lds.red[1]), fmaxf(lds.red[2], lds.red[3]));
+    float l = 0.0f;
 #pragma unroll
-        for (int k = 1; k < 4; k++) {
-            o += *reinterpret_cast<const f32x4*>(lds + (k * 64 + c) * 4);
-            l += lds[1024 + k];
-        }
+    for (int k = 0; k < 2; k++) {
+        const int i = tid + 256 * k;
+        const float f = exp2_fast(m0[k] - ref);
+        if (i < n) lds.f[i] = f;
+        l += i < n ? f * l0[k] : 0.0f;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d, 64);
+    __syncthreads();
+    if ((tid & 63) == 0) lds.red[tid >> 6] = l;
+    f32x4 o = {0, 0, 0, 0};
+    if (gr < groups) {
+#pragma unroll 8
+        for (int i = gr; i < n; i += groups) o += lds.f[i] * *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
+        *reinterpret_cast<f32x4*>(lds.sum + tid * 4) = o;
+    }
+    __syncthreads();
+    if (tid < quads) {
+        for (int k = 1; k < groups; k++) o += *reinterpret_cast<const f32x4*>(lds.sum + (k * quads + c) * 4);
+        l = (lds.red[0] + lds.red[1]) + (lds.red[2] + lds.red[3]);
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         *reinterpret_cast<u32x2*>(y + 4 * c) = (u32x2){pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
     }
 }
 
-// Workgroup (i, column): the tile, if there is one, that workgroup i began and did not end.
+// Workgroup i: the tile, if there is one, that workgroup i of k_attn_token began and did not end.
 __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
-    __shared__ __attribute__((aligned(16))) float lds[1024 + 4];
+    __shared__ __attribute__((aligned(16))) JoinLds lds;
     const TileShape ts = tile_shape(kTokenCols, a.group);
-    const int heads = a.s.heads, col = blockIdx.y;
+    const int heads = a.s.heads;
     const TokenShare sh(a, ts);
     const uint32_t edge = (blockIdx.x + 1) * sh.share;
     if (edge >= sh.total) return;
@@ -474,28 +495,391 @@ __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
     if (w0 == edge || w0 < blockIdx.x * sh.share) return;
     const int parts = (w0 + span - 1) / sh.share - blockIdx.x + 1;
     const int tile = in / heads, h = in - tile * heads;
-    int row, head;
-    if (!tile_col(a, ts, tile, col, q.n, &row, &head)) return;
     const Partials p(a);
     // the first part is the one that starts the tile, the others start their workgroups
-    const int first = 2 * blockIdx.x + 1;
-    join_column(a, p, parts, col, a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * a.dim, first, first + 1, 2, lds);
+    const auto slot = [](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0); };
+    for (int col = blockIdx.y; col < kTokenCols; col += gridDim.y) {
+        int row, head;
+        if (!tile_col(a, ts, tile, col, q.n, &row, &head)) break;   // columns without a query are the last ones
+        join_column(a, p, parts, col, a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * a.dim, slot, lds);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// Many rows per sequence (prompts): tiles of 128 columns, keys and values made fp16 once per workgroup.
+// ---------------------------------------------------------------------------------------------------------------
+
+constexpr int kRowCols = 128, kStep = 2;   // columns per tile; units (of 32 tokens) per step
+
+// One 16-byte chunk of a unit's K or V codes with the scales of its four words, on its way to LDS.
+template <bool Q41>
+struct Chunk {
+    u32x4 w;
+    uint32_t d[4][2], m[Q41 ? 4 : 1][2];   // K: d[i][0] one scale; V: the scales of four tokens
+};
+
+// Word i of chunk `c` (16 bytes) of a unit's codes: lane and word index.
+template <int NB>
+__device__ inline void chunk_word(int c, int i, int* lane, int* wi) {
+    constexpr int full = NB / 2;
+    if (NB % 2 == 0 || c < full * 64) {
+        *lane = c & 63;
+        *wi = (c >> 6) * 4 + i;
+    } else {
+        *lane = (c - full * 64) * 2 + (i >> 1);
+        *wi = full * 4 + (i & 1);
+    }
+}
+
+template <int NB, bool Q41, bool V>
+__device__ inline void load_chunk(const uint8_t* codes, int c, Chunk<Q41>* r) {
+    constexpr int dim = 32 * NB, plane = cache_plane_bytes(dim);
+    r->w = *reinterpret_cast<const u32x4*>(codes + c * 16);
+    const uint8_t* const sc = codes + 16 * dim;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        int lane, wi;
+        chunk_word<NB>(c, i, &lane, &wi);
+        if constexpr (V) {
+            const int b = wi >> 1, tile = wi & 1, at = ((tile * 4 + (lane >> 4)) * NB + b) * 8;
+            const u32x2 d = *reinterpret_cast<const u32x2*>(sc + at);
+            r->d[i][0] = d[0];
+            r->d[i][1] = d[1];
+            if constexpr (Q41) {
+                const u32x2 m = *reinterpret_cast<const u32x2*>(sc + plane + at);
+                r->m[i][0] = m[0];
+                r->m[i][1] = m[1];
+            }
+        } else {
+            const int tile = wi / NB, b = wi - tile * NB, t = lane & 15;
+            const int at = (((tile * 4 + (t >> 2)) * NB + b) * 4 + (t & 3)) * 2;
+            r->d[i][0] = *reinterpret_cast<const uint16_t*>(sc + at) * 0x10001u;
+            if constexpr (Q41) r->m[i][0] = *reinterpret_cast<const uint16_t*>(sc + plane + at) * 0x10001u;
+        }
+    }
+}
+
+// The chunk's values as fp16 into the operand layouts of the 32 x 32 x 16 products (1 KiB fragments, 16 bytes a lane):
+// K: fragment s (channels 16 s ..), lane 32 (g % 2) + token; V: fragment (block, 16-token tile), lane 32 (g % 2) +
+// channel, half g / 2 of its 16 bytes.  `left`: tokens of the unit that are in the cache (V's others are made zero).
+template <int NB, bool Q41, bool V>
+__device__ inline void store_chunk(const Chunk<Q41>& r, int c, int left, uint32_t f1024, uint8_t* out) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        int lane, wi;
+        chunk_word<NB>(c, i, &lane, &wi);
+        const int g = lane >> 4, x = lane & 15;
+        const uint32_t w = r.w[i];
+        if constexpr (V) {
+            const int b = wi >> 1, tile = wi & 1, t = 16 * tile + 4 * g;
+            uint32_t keep[2];
+            keep[0] = (t < left ? 0x0000FFFFu : 0u) | (t + 1 < left ? 0xFFFF0000u : 0u);
+            keep[1] = (t + 2 < left ? 0x0000FFFFu : 0u) | (t + 3 < left ? 0xFFFF0000u : 0u);
+            u32x2 lo, hi;
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const f16x2 d = as_f16x2(r.d[i][k] & keep[k]);
+                f16x2 m = {};
+                if constexpr (Q41) m = as_f16x2(r.m[i][k] & keep[k]);
+                lo[k] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(w & 0x0F0F0F0Fu, k), d, m));
+                hi[k] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair((w >> 4) & 0x0F0F0F0Fu, k), d, m));
+            }
+            uint8_t* const p = out + (b * 2 + tile) * 1024 + ((g & 1) * 32 + x) * 16 + (g >> 1) * 8;
+            *reinterpret_cast<u32x2*>(p) = lo;
+            *reinterpret_cast<u32x2*>(p + 256) = hi;
+        } else {
+            const int tile = wi / NB, b = wi - tile * NB;
+            const f16x2 d = as_f16x2(r.d[i][0]);
+            f16x2 m = {};
+            if constexpr (Q41) m = as_f16x2(r.m[i][0]);
+            u32x4 v;
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                v[k] = __builtin_bit_cast(uint32_t, code_value<Q41>(as_f16x2(nibble_pair(w, k, f1024)), d, m));
+            *reinterpret_cast<u32x4*>(out + (2 * b + (g >> 1)) * 1024 + ((g & 1) * 32 + 16 * tile + x) * 16) = v;
+        }
+    }
+}
+
+template <int NB, bool Q41>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_rows(AttnArgs a) {
+    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), unit_lds = 64 * dim;   // fp16 bytes of a unit's K, or V
+    constexpr int chunks = kStep * dim;                            // 16-byte chunks of K codes in a step, and of V codes
+    constexpr int rounds = (2 * chunks + 255) / 256;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStep * unit_lds];
+    uint8_t* const lk = lds;
+    uint8_t* const lv = lds + kStep * unit_lds;
+    const TileShape ts = tile_shape(kRowCols, a.group);
+    const int heads = a.s.heads, tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), hl = lane >> 5;
+    // heads vary fastest, so that a head's tiles (which read the same keys and values) tend to the same die; later tiles,
+    // which see more, come first
+    int at = blockIdx.x;
+    const int h = at % heads;
+    at /= heads;
+    const int split = at % a.splits;
+    at /= a.splits;
+    int seq, tile;
+    uint32_t before;
+    if (!a.s.row_start) {
+        seq = at / ts.ht;
+        before = seq * ts.ht;
+        tile = at - before;
+    } else {
+        const auto count = [&](int b) {
+            int r0, r1;
+            seq_rows(a.s, b, &r0, &r1);
+            return (uint32_t)tiles_of(ts, r1 - r0);
+        };
+        seq = SeqTotals(a.s.batch, count).find(at, &before);
+        if (seq < 0) return;
+    }
+    const SeqInfo q = seq_info_uniform(a, seq);
+    tile = tiles_of(ts, q.n) - 1 - (at - (int)before);
+    const int first = ts.ht == 1 ? tile * ts.rows : tile / ts.ht, end = min(first + ts.rows, q.n);
+    int u0, u1;
+    row_units(a, q, first, end, &u0, &u1);
+    if (a.splits > 1) {
+        const int per = ((u1 - u0 + a.splits - 1) / a.splits + kStep - 1) / kStep * kStep;
+        u0 += split * per;
+        u1 = min(u1, u0 + per);
+    }
+
+    // this wave's 32 columns
+    const int col = wave * 32 + (lane & 31);
+    int row, head;
+    const bool valid = tile_col(a, ts, tile, col, q.n, &row, &head);
+    int lo, hi, lo_most, hi_least, x;
+    row_tokens(a, q, valid ? row : first, &lo, &hi);
+    row_tokens(a, q, first, &x, &hi_least);
+    row_tokens(a, q, end - 1, &lo_most, &x);
+    // queries as fp16, scaled by a power of two per column so that the largest is in [2^14, 2^15)
+    f16x8 qf[2 * NB];
+    float sl2 = a.scale_log2;
+    {
+        const uint16_t* qp = a.q + (int64_t)(q.r0 + row) * a.ldq + (int64_t)(h * a.group + head) * dim + 8 * hl;
+        u32x4 v[2 * NB];
+        uint32_t big = 0;
+#pragma unroll
+        for (int s = 0; s < 2 * NB; s++) {
+            v[s] = (u32x4){0, 0, 0, 0};
+            if (valid) v[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+#pragma unroll
+            for (int k = 0; k < 4; k++) big = max(big, max(v[s][k] & 0x7FFFu, (v[s][k] >> 16) & 0x7FFFu));
+        }
+        big = max(big, (uint32_t)__shfl_xor((int)big, 32, 64));
+        const int k = min(141 - (int)(big >> 7), 100);              // exponent bits of bf16: value < 2^(e - 126)
+        const float up = ldexpf(1.0f, big == 0 ? 0 : k);
+        sl2 *= ldexpf(1.0f, big == 0 ? 0 : -k);
+#pragma unroll
+        for (int s = 0; s < 2 * NB; s++) {
+            float f[8];
+#pragma unroll
+            for (int k2 = 0; k2 < 4; k2++) {
+                f[2 * k2] = __uint_as_float(v[s][k2] << 16) * up;
+                f[2 * k2 + 1] = __uint_as_float(v[s][k2] & 0xFFFF0000u) * up;
+            }
+            const u32x4 p = {pack_f16(f[0], f[4]), pack_f16(f[1], f[5]), pack_f16(f[2], f[6]), pack_f16(f[3], f[7])};
+            qf[s] = __builtin_bit_cast(f16x8, p);
+        }
+    }
+
+    f32x16 o[NB];
+#pragma unroll
+    for (int b = 0; b < NB; b++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[b][i] = 0.0f;
+    float ref = -FLT_MAX, l = 0.0f;
+    const uint32_t f1024 = held(0x64006400u);
+
+    // the step's units: where they are, or -1
+    int64_t where[kStep];
+    Chunk<Q41> r[rounds];
+    UnitWalk walk;
+    walk.start(a.s, seq, h, u0);
+    const auto fetch = [&](int u) {
+#pragma unroll
+        for (int k = 0; k < kStep; k++) {
+            where[k] = u + k < u1 ? walk.at() : -1;
+            walk.step(1);
+        }
+#pragma unroll
+        for (int i = 0; i < rounds; i++) {
+            const int id = i * 256 + tid, base = i * 256 + wave * 64;   // (chunks is a multiple of 64)
+            if (base >= 2 * chunks) break;
+            const bool v = base >= chunks;
+            const int c = v ? id - chunks : id, k = c / dim;
+            const int64_t p = k ? where[1] : where[0];
+            if (p < 0) continue;
+            const uint8_t* const codes = a.cache + p;
+            if (v) load_chunk<NB, Q41, true>(codes + half, c - k * dim, &r[i]);
+            else load_chunk<NB, Q41, false>(codes, c - k * dim, &r[i]);
+        }
+    };
+    if (u0 < u1) fetch(u0);
+    for (int u = u0; u < u1; u += kStep) {
+        __syncthreads();   // the last step's reads are done
+#pragma unroll
+        for (int i = 0; i < rounds; i++) {
+            const int id = i * 256 + tid, base = i * 256 + wave * 64;
+            if (base >= 2 * chunks) break;
+            const bool v = base >= chunks;
+            const int c = v ? id - chunks : id, k = c / dim;
+            const int left = (k ? where[1] : where[0]) < 0 ? 0 : q.tokens - (u + k) * kUnit;
+            if (left <= 0) r[i] = {};
+            if (v) store_chunk<NB, Q41, true>(r[i], c - k * dim, left, f1024, lv + k * unit_lds);
+            else store_chunk<NB, Q41, false>(r[i], c - k * dim, left, f1024, lk + k * unit_lds);
+        }
+        bool there[kStep];
+#pragma unroll
+        for (int k = 0; k < kStep; k++) there[k] = where[k] >= 0;
+        __syncthreads();
+        if (u + kStep < u1) fetch(u + kStep);
+#pragma unroll
+        for (int k = 0; k < kStep; k++) {
+            if (!there[k]) continue;
+            f32x16 s;
+#pragma unroll
+            for (int i = 0; i < 16; i++) s[i] = 0.0f;
+#pragma unroll
+            for (int f = 0; f < 2 * NB; f++) {
+                const f16x8 kf = *reinterpret_cast<const f16x8*>(lk + k * unit_lds + f * 1024 + lane * 16);
+                s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[f], s, 0, 0, 0);
+            }
+            const int t0 = (u + k) * kUnit;
+            float e[16];
+            if (t0 < lo_most || t0 + kUnit > hi_least) {
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int t = t0 + 8 * (i >> 2) + 4 * hl + (i & 3);
+                    e[i] = t >= lo && t < hi ? s[i] * sl2 : -INFINITY;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; i++) e[i] = s[i] * sl2;
+            }
+            float mx = e[0];
+#pragma unroll
+            for (int i = 1; i < 16; i++) mx = fmaxf(mx, e[i]);
+            if (__any(mx - ref > kRefMost)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+                const float r2 = fmaxf(ref, mx - kRefBelow), alpha = r2 == ref ? 1.0f : exp2_fast(ref - r2);
+#pragma unroll
+                for (int b = 0; b < NB; b++) o[b] *= alpha;
+                l *= alpha;
+                ref = r2;
+            }
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                e[i] = exp2_fast(e[i] - ref);
+                sum += e[i];
+            }
+            l += sum;
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const u32x4 p = {pack_f16(e[8 * c], e[8 * c + 1]), pack_f16(e[8 * c + 2], e[8 * c + 3]),
+                                 pack_f16(e[8 * c + 4], e[8 * c + 5]), pack_f16(e[8 * c + 6], e[8 * c + 7])};
+                const f16x8 pf = __builtin_bit_cast(f16x8, p);
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    const f16x8 vf = *reinterpret_cast<const f16x8*>(lv + k * unit_lds + (b * 2 + c) * 1024 + lane * 16);
+                    o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf, o[b], 0, 0, 0);
+                }
+            }
+        }
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (!valid) return;
+    if (a.splits > 1) {
+        const Partials p(a);
+        const int slot = ((int)before + tile) * heads + h;
+        float* const po = p.sums(slot * a.splits + split, col);
+#pragma unroll
+        for (int b = 0; b < NB; b++)
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                *reinterpret_cast<f32x4*>(po + 32 * b + 8 * k + 4 * hl) = (f32x4){o[b][4 * k], o[b][4 * k + 1], o[b][4 * k + 2], o[b][4 * k + 3]};
+        if (hl == 0) {
+            float* const st = p.stat(slot * a.splits + split, col);
+            st[0] = ref;
+            st[1] = l;
+        }
+        return;
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    uint16_t* const y = a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * dim;
+#pragma unroll
+    for (int b = 0; b < NB; b++)
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            *reinterpret_cast<u32x2*>(y + 32 * b + 8 * k + 4 * hl) = (u32x2){pack_bf16(o[b][4 * k] * inv, o[b][4 * k + 1] * inv),
+                                                                            pack_bf16(o[b][4 * k + 2] * inv, o[b][4 * k + 3] * inv)};
+}
+
+// Workgroup (tile, head): the tile's columns, each shared out over a.splits workgroups of k_attn_rows.
+__global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
+    __shared__ __attribute__((aligned(16))) JoinLds lds;
+    const TileShape ts = tile_shape(kRowCols, a.group);
+    const int heads = a.s.heads, h = blockIdx.x % heads, at = blockIdx.x / heads;
+    int seq;
+    uint32_t before;
+    if (!a.s.row_start) {
+        seq = at / ts.ht;
+        before = seq * ts.ht;
+    } else {
+        const auto count = [&](int b) {
+            int r0, r1;
+            seq_rows(a.s, b, &r0, &r1);
+            return (uint32_t)tiles_of(ts, r1 - r0);
+        };
+        seq = SeqTotals(a.s.batch, count).find(at, &before);
+        if (seq < 0) return;
+    }
+    const SeqInfo q = seq_info_uniform(a, seq);
+    const int tile = at - before;
+    const Partials p(a);
+    const auto slot = [&](int i) { return (int)blockIdx.x * a.splits + i; };
+    for (int col = blockIdx.y; col < kRowCols; col += gridDim.y) {
+        int row, head;
+        if (!tile_col(a, ts, tile, col, q.n, &row, &head)) break;
+        join_column(a, p, a.splits, col, a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * a.dim, slot, lds);
+    }
 }
 
 namespace {
 
 // Workgroups that a shared-out call has, and the units that each takes at least.
-constexpr int kShareWorkgroups = 512, kShareLeast = 16;
+constexpr int kShareWorkgroups = kJoinParts, kShareLeast = 16;
+// Columns per sequence, on average, from which a call takes tiles of 128 columns.
+constexpr int kManyCols = 33;
+// Tiles of 128 columns: workgroups that fill the chip twice, and units that a part has at least.
+constexpr int kRowWorkgroups = 512, kRowLeast = 16;
 
-// Sequences are shared out where their tiles alone would leave compute units without work, and a sequence can be long
-// enough to be worth the second launch that joins the parts.
-int share_workgroups(const AttnArgs& a) {
-    const TileShape ts = tile_shape(kTokenCols, a.group);
-    const int64_t items = tile_bound(ts, a.s.rows, a.s.batch, !a.s.row_start) * a.s.heads;
-    const int64_t units = ((int64_t)a.s.table_ld * a.s.page) / kUnit;
-    if (units < 32 || items >= 4096) return 0;
-    if (items * units > 0x7FFFFFFF) return 0;     // work is counted in 32 bits
-    return kShareWorkgroups;
+// How a call runs.
+struct Schedule {
+    bool rows;           // tiles of 128 columns
+    int64_t items;       // tiles x heads (at most)
+    int workgroups;      // 16 columns: sequences shared out over so many (0: not)
+    int splits;          // 128 columns: parts per tile
+    int slots() const { return rows ? (splits > 1 ? (int)items * splits : 0) : 2 * workgroups; }
+    int cols() const { return rows ? kRowCols : kTokenCols; }
+};
+
+Schedule schedule(const AttnArgs& a, bool share) {
+    Schedule s{};
+    s.rows = a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch;
+    const TileShape ts = tile_shape(s.cols(), a.group);
+    s.items = tile_bound(ts, a.s.rows, a.s.batch, !a.s.row_start) * a.s.heads;
+    s.splits = 1;
+    const int64_t units = ((int64_t)a.s.table_ld * a.s.page) / kUnit;   // of the longest sequence there can be
+    if (!share) return s;
+    if (s.rows) {
+        const int64_t most = std::min<int64_t>(kRowWorkgroups / s.items, units / kRowLeast);
+        s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 64));
+    } else if (units >= 32 && s.items < 4096 && s.items * units <= 0x7FFFFFFF) {   // (work is counted in 32 bits)
+        s.workgroups = kShareWorkgroups;
+    }
+    return s;
 }
 
 template <int NB, int NW, int D>
@@ -503,30 +887,48 @@ void launch_token(const AttnArgs& a, dim3 grid, hipStream_t s) {
     if (a.q41) hipLaunchKernelGGL((k_attn_token<NB, true, NW, D>), grid, dim3(NW * 64), 0, s, a);
     else hipLaunchKernelGGL((k_attn_token<NB, false, NW, D>), grid, dim3(NW * 64), 0, s, a);
 }
+template <int NB>
+void launch_rows(const AttnArgs& a, dim3 grid, hipStream_t s) {
+    if (a.q41) hipLaunchKernelGGL((k_attn_rows<NB, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_attn_rows<NB, false>), grid, dim3(256), 0, s, a);
+}
 
 }  // namespace
 
 size_t attn_workspace_bytes(const AttnArgs& a) {
-    return (size_t)partial_bytes(2 * share_workgroups(a), kTokenCols, a.dim);
+    const Schedule s = schedule(a, true);
+    return (size_t)partial_bytes(s.slots(), s.cols(), a.dim);
 }
 
 hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     AttnArgs a = args;
-    a.tile_cols = kTokenCols;
-    a.workgroups = a.ws ? share_workgroups(a) : 0;
+    const Schedule c = schedule(a, a.ws != nullptr);
+    a.tile_cols = c.cols();
+    a.workgroups = c.workgroups;
     a.least_units = kShareLeast;
-    a.slots = 2 * a.workgroups;
-    const TileShape ts = tile_shape(kTokenCols, a.group);
-    const int64_t items = tile_bound(ts, a.s.rows, a.s.batch, !a.s.row_start) * a.s.heads;
-    const dim3 grid((unsigned)(a.workgroups ? a.workgroups : items));
+    a.splits = c.splits;
+    a.slots = c.slots();
+    const TileShape ts = tile_shape(a.tile_cols, a.group);
+    const int cols = std::min(a.tile_cols, (a.s.row_start ? ts.rows : 1) * a.group);   // that a tile can have
+    if (c.rows) {
+        const dim3 grid((unsigned)(c.items * c.splits));
+        switch (a.dim) {
+        case 64: launch_rows<2>(a, grid, s); break;
+        case 96: launch_rows<3>(a, grid, s); break;
+        case 128: launch_rows<4>(a, grid, s); break;
+        default: launch_rows<8>(a, grid, s); break;
+        }
+        if (c.splits > 1) hipLaunchKernelGGL(k_attn_join_rows, dim3((unsigned)c.items, std::min(cols, 16)), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)(c.workgroups ? c.workgroups : c.items));
     switch (a.dim) {
     case 64: launch_token<2, 4, 4>(a, grid, s); break;
     case 96: launch_token<3, 4, 3>(a, grid, s); break;
     case 128: launch_token<4, 4, 3>(a, grid, s); break;
     default: launch_token<8, 4, 2>(a, grid, s); break;
     }
-    const int cols = std::min(kTokenCols, (a.s.row_start ? ts.rows : 1) * a.group);   // that a tile can have
-    if (a.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3(a.workgroups - 1, cols), dim3(256), 0, s, a);
+    if (c.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3(c.workgroups - 1, std::min(cols, 4)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

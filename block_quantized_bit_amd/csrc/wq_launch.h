@@ -91,6 +91,7 @@ struct AttnArgs {
     int32_t tile_cols;     // columns (rows x heads) per tile of the kernel that runs
     int32_t workgroups;    // > 0: sequences are shared out over so many
     int32_t least_units;   // units that each then takes at least
+    int32_t splits;        // tiles of 128 columns: parts that each tile's tokens are shared out in
     int32_t slots;         // partial results that the workspace holds
     bool q41, causal;
 };

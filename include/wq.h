@@ -357,7 +357,7 @@ wq_status wq_attn_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32
  * A row that sees no token gets zeros.  Scores, the softmax's maximum and sum and the
  * sums over tokens are fp32; probabilities, values and (in calls with many rows) keys are
  * rounded to fp16 for the matrix products.  Per element |y - y_ref| <=
- * (2^-9 + 2^-9 A) * sum_t p_t |v^_t| plus the final bf16 rounding, where A is the row's
+ * (2^-9 + 2^-9 A) * sum_t (p_t + 2^-23) |v^_t| plus the final bf16 rounding, where A is the row's
  * largest |scale| * sum_c |q_c k^_tc| and y_ref is exact for the values in the cache. */
 wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq, const void* cache,
                   float scale, int32_t causal, int32_t window, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes,

@@ -92,7 +92,7 @@ class Case:
 
 
 def attend(case, O, k, v, q, group, scale, causal, window):
-    """float64 attention: (y, sum p |v^|, A) with A the largest |scale| sum |q k^| of a row's visible tokens."""
+    """float64 attention: (y, sum (p + 2^-23) |v^|, A) with A the largest |scale| sum |q k^| of a row's visible tokens."""
     hq = case.heads * group
     y = np.zeros((case.rows, hq, case.dim))
     ab, A = np.zeros_like(y), np.zeros((case.rows, hq, 1))
@@ -120,7 +120,7 @@ def attend(case, O, k, v, q, group, scale, causal, window):
                 e = np.exp(s - s.max())
                 e /= e.sum()
                 y[row, h] = e @ V
-                ab[row, h] = e @ np.abs(V)
+                ab[row, h] = (e + 2.0 ** -23) @ np.abs(V)
                 A[row, h] = abs(scale) * (np.abs(K) @ np.abs(qv)).max()
     return y, ab, A
 
@@ -148,12 +148,15 @@ def run_attn(case, q_bits, group, scale, causal, window, *, ws="asked", pad=0, s
 
 
 def check_attn(y, ref, ab, A, what=""):
-    """|y - ref| <= (2^-9 + 2^-9 A) sum p |v^| + the bf16 rounding of y.
+    """|y - ref| <= (2^-9 + 2^-9 A) sum (p + 2^-23) |v^| + the bf16 rounding of y.
 
     Where it comes from, in steps of u = 2^-11 (half a step of fp16): a probability is off by u from its rounding to
     fp16, a value by u, and each score by at most u A where keys are rounded (their products with q by u each), which
     moves p by a factor e^(+-2 u A) (its own score and the sum's).  Together (2 u + 2 u A) (1 + o(1)) of sum p |v^|, and
     the fp32 sums of up to 2^17 terms in tiles and exp2 add under u (1 + A).  2^-9 = 4 u leaves a third to spare.
+    Below 2^-14 fp16's steps are 2^-24, whatever the number: a small probability is off by up to 2^-25.  The kernels hold
+    2^(x - ref) with the largest at least 2^7 (ref is set 7 below the largest score so far, and larger scores only add), so
+    the sum that divides is at least 2^7 and a probability is off by at most 2^-32 = 2^-9 2^-23 that way.
     The output is off by half a step, 2^-8 |y| at most."""
     tol = (2.0 ** -9 + 2.0 ** -9 * A) * ab + 2.0 ** -8 * np.abs(ref) + 1e-30
     err = np.abs(y.astype(np.float64) - ref)
