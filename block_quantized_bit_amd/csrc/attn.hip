@@ -199,22 +199,31 @@ __device__ inline void unit_step(const uint8_t* unit, const bf16x8 (&qf)[NB], co
 
 constexpr int kTokenCols = 16;
 
-// Units of a sequence's items, for sharing out: every tile of it takes all of them; at least one, so that tiles whose
-// rows see nothing are visited (and written).
+// Units [*u0, *u0 + return) of a sequence's rows: every tile of it takes all of them.
 __device__ inline int span_units(const AttnArgs& a, const SeqInfo& q, int* u0) {
     int u1;
-    if (q.n == 0) {
-        *u0 = 0;
-        return 0;
-    }
+    *u0 = 0;
+    if (q.n == 0) return 0;
     row_units(a, q, 0, q.n, u0, &u1);
-    return u1 > *u0 ? u1 - *u0 : 1;
+    return u1 - *u0;
 }
+
+// What beginning a tile costs a workgroup (queries, the first requests' way to memory, joining the waves), in units: the
+// work that is shared out counts it, so that workgroups with many short sequences end with the others.
+constexpr int kTileCost = 8;
 
 // The stretch of the call's work, in units over all (sequence, tile, head), that a workgroup takes: `share` each.
 __device__ inline uint32_t work_share(uint32_t total, int workgroups, int least) {
     const uint32_t s = (total + workgroups - 1) / workgroups;
     return s > (uint32_t)least ? s : (uint32_t)least;
+}
+
+// The tile that a workgroup began and did not end, for k_attn_join_token: parts 0 if there is none.
+struct OpenTile {
+    int parts, tile, head, r0, n;
+};
+__device__ inline OpenTile* open_tile(const AttnArgs& a, int workgroup) {
+    return reinterpret_cast<OpenTile*>(a.ws + partial_bytes(a.slots, a.tile_cols, a.dim)) + workgroup;
 }
 
 struct SpanWeight {
@@ -223,7 +232,7 @@ struct SpanWeight {
     __device__ uint32_t operator()(int b) const {
         const SeqInfo q = seq_info(a, b);
         int u0;
-        return (uint32_t)(tiles_of(ts, q.n) * a.s.heads * span_units(a, q, &u0));
+        return (uint32_t)(tiles_of(ts, q.n) * a.s.heads * (kTileCost + span_units(a, q, &u0)));
     }
 };
 struct TokenShare {
@@ -376,12 +385,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
             seq = item / (ts.ht * heads);
             before = seq * (ts.ht * heads);
         } else {
-            const auto count = [&](int b) {
-                int r0, r1;
-                seq_rows(a.s, b, &r0, &r1);
-                return (uint32_t)(tiles_of(ts, r1 - r0) * heads);
-            };
-            seq = SeqTotals(a.s.batch, count).find(item, &before);
+            seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(item / heads, &before);
+            before *= heads;
         }
         if (seq < 0 || seq >= a.s.batch) return;
         const SeqInfo q = seq_info_uniform(a, seq);
@@ -396,32 +401,31 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
     const TokenShare sh(a, ts);
     uint32_t w = blockIdx.x * sh.share, before;
     const uint32_t end = min(w + sh.share, sh.total);
-    if (w >= end) return;
-    int seq = sh.t.find(w, &before);
+    OpenTile open = {};
+    int seq = w < end ? sh.t.find(w, &before) : 0;
     while (w < end) {
         const SeqInfo q = seq_info_uniform(a, seq);
         int u0;
-        const int span = span_units(a, q, &u0);
+        const int units = span_units(a, q, &u0), span = kTileCost + units;
         const uint32_t items = tiles_of(ts, q.n) * heads;
         while (w < end && w - before < items * span) {
             const int item = (w - before) / span, s0 = (w - before) - item * span, s1 = min((uint32_t)span, s0 + (end - w));
             const int tile = item / heads, h = item - tile * heads;
             float *po = nullptr, *pm = nullptr;
             if (s1 - s0 < span) {
-                const int slot = 2 * blockIdx.x + (s0 > 0 ? 0 : 1);
                 const Partials p(a);
+                const int slot = 2 * blockIdx.x + (s0 > 0 ? 0 : 1);
                 po = p.sums(slot, 0);
                 pm = p.stat(slot, 0);
+                if (s0 == 0) open = {(int)((w + span - 1) / sh.share - blockIdx.x) + 1, tile, h, q.r0, q.n};
             }
-            // (a span of one unit stands for none where the rows see nothing)
-            int r0, r1;
-            row_units(a, q, 0, q.n, &r0, &r1);
-            token_segment<NB, Q41, NW, D>(a, ts, q, seq, tile, h, u0 + s0, min(u0 + s1, r1), po, pm, lds);
+            token_segment<NB, Q41, NW, D>(a, ts, q, seq, tile, h, u0 + max(0, s0 - kTileCost), u0 + max(0, s1 - kTileCost), po, pm, lds);
             w += s1 - s0;
         }
         before += items * span;
         seq++;
     }
+    if (threadIdx.x == 0) *open_tile(a, blockIdx.x) = open;
 }
 
 // Joins the parts of a tile's column: y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  Every thread sums four
@@ -434,6 +438,14 @@ template <class F>
 __device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, int col, uint16_t* y, F slot, JoinLds& lds) {
     const int tid = threadIdx.x, quads = a.dim / 4, groups = 256 / quads, gr = tid / quads, c = tid - gr * quads;
     float ref = -FLT_MAX, m0[2], l0[2];
+    constexpr int ahead = 8;                  // parts requested before their factors are known
+    f32x4 early[ahead];
+#pragma unroll
+    for (int k = 0; k < ahead; k++) {
+        const int i = gr + k * groups;
+        early[k] = (f32x4){0, 0, 0, 0};
+        if (gr < groups && i < n) early[k] = *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
+    }
 #pragma unroll
     for (int k = 0; k < 2; k++) {
         const int i = tid + 256 * k;
@@ -466,8 +478,11 @@ __device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, 
     if ((tid & 63) == 0) lds.red[tid >> 6] = l;
     f32x4 o = {0, 0, 0, 0};
     if (gr < groups) {
-#pragma unroll 8
-        for (int i = gr; i < n; i += groups) o += lds.f[i] * *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
+#pragma unroll
+        for (int k = 0; k < ahead; k++)
+            if (gr + k * groups < n) o += lds.f[gr + k * groups] * early[k];
+#pragma unroll 4
+        for (int i = gr + ahead * groups; i < n; i += groups) o += lds.f[i] * *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
         *reinterpret_cast<f32x4*>(lds.sum + tid * 4) = o;
     }
     __syncthreads();
@@ -483,25 +498,16 @@ __device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, 
 __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) JoinLds lds;
     const TileShape ts = tile_shape(kTokenCols, a.group);
-    const int heads = a.s.heads;
-    const TokenShare sh(a, ts);
-    const uint32_t edge = (blockIdx.x + 1) * sh.share;
-    if (edge >= sh.total) return;
-    uint32_t before;
-    const int seq = sh.t.find(edge, &before);
-    const SeqInfo q = seq_info_uniform(a, seq);
-    int u0;
-    const uint32_t span = span_units(a, q, &u0), in = (edge - before) / span, w0 = before + in * span;
-    if (w0 == edge || w0 < blockIdx.x * sh.share) return;
-    const int parts = (w0 + span - 1) / sh.share - blockIdx.x + 1;
-    const int tile = in / heads, h = in - tile * heads;
+    const int32_t* const d = &open_tile(a, blockIdx.x)->parts;
+    const OpenTile t = {read_const(d, 0), read_const(d, 1), read_const(d, 2), read_const(d, 3), read_const(d, 4)};
+    if (t.parts == 0) return;
     const Partials p(a);
     // the first part is the one that starts the tile, the others start their workgroups
     const auto slot = [](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0); };
     for (int col = blockIdx.y; col < kTokenCols; col += gridDim.y) {
         int row, head;
-        if (!tile_col(a, ts, tile, col, q.n, &row, &head)) break;   // columns without a query are the last ones
-        join_column(a, p, parts, col, a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * a.dim, slot, lds);
+        if (!tile_col(a, ts, t.tile, col, t.n, &row, &head)) break;   // columns without a query are the last ones
+        join_column(a, p, t.parts, col, a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim, slot, lds);
     }
 }
 
@@ -618,23 +624,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
     at /= heads;
     const int split = at % a.splits;
     at /= a.splits;
-    int seq, tile;
     uint32_t before;
-    if (!a.s.row_start) {
-        seq = at / ts.ht;
-        before = seq * ts.ht;
-        tile = at - before;
-    } else {
-        const auto count = [&](int b) {
-            int r0, r1;
-            seq_rows(a.s, b, &r0, &r1);
-            return (uint32_t)tiles_of(ts, r1 - r0);
-        };
-        seq = SeqTotals(a.s.batch, count).find(at, &before);
-        if (seq < 0) return;
-    }
+    const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
+    if (seq < 0) return;
     const SeqInfo q = seq_info_uniform(a, seq);
-    tile = tiles_of(ts, q.n) - 1 - (at - (int)before);
+    const int tile = tiles_of(ts, q.n) - 1 - (at - (int)before);
     const int first = ts.ht == 1 ? tile * ts.rows : tile / ts.ht, end = min(first + ts.rows, q.n);
     int u0, u1;
     row_units(a, q, first, end, &u0, &u1);
@@ -821,20 +815,9 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) JoinLds lds;
     const TileShape ts = tile_shape(kRowCols, a.group);
     const int heads = a.s.heads, h = blockIdx.x % heads, at = blockIdx.x / heads;
-    int seq;
     uint32_t before;
-    if (!a.s.row_start) {
-        seq = at / ts.ht;
-        before = seq * ts.ht;
-    } else {
-        const auto count = [&](int b) {
-            int r0, r1;
-            seq_rows(a.s, b, &r0, &r1);
-            return (uint32_t)tiles_of(ts, r1 - r0);
-        };
-        seq = SeqTotals(a.s.batch, count).find(at, &before);
-        if (seq < 0) return;
-    }
+    const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
+    if (seq < 0) return;
     const SeqInfo q = seq_info_uniform(a, seq);
     const int tile = at - before;
     const Partials p(a);
@@ -849,7 +832,7 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
 namespace {
 
 // Workgroups that a shared-out call has, and the units that each takes at least.
-constexpr int kShareWorkgroups = kJoinParts, kShareLeast = 16;
+constexpr int kShareWorkgroups = kJoinParts, kShareLeast = 24;
 // Columns per sequence, on average, from which a call takes tiles of 128 columns.
 constexpr int kManyCols = 33;
 // Tiles of 128 columns: workgroups that fill the chip twice, and units that a part has at least.
@@ -876,7 +859,7 @@ Schedule schedule(const AttnArgs& a, bool share) {
     if (s.rows) {
         const int64_t most = std::min<int64_t>(kRowWorkgroups / s.items, units / kRowLeast);
         s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 64));
-    } else if (units >= 32 && s.items < 4096 && s.items * units <= 0x7FFFFFFF) {   // (work is counted in 32 bits)
+    } else if (units >= 32 && s.items < 4096 && s.items * (units + kTileCost) <= 0x7FFFFFFF) {   // (work is counted in 32 bits)
         s.workgroups = kShareWorkgroups;
     }
     return s;
@@ -897,7 +880,7 @@ void launch_rows(const AttnArgs& a, dim3 grid, hipStream_t s) {
 
 size_t attn_workspace_bytes(const AttnArgs& a) {
     const Schedule s = schedule(a, true);
-    return (size_t)partial_bytes(s.slots(), s.cols(), a.dim);
+    return (size_t)partial_bytes(s.slots(), s.cols(), a.dim) + s.workgroups * sizeof(OpenTile);
 }
 
 hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
@@ -928,7 +911,7 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     case 128: launch_token<4, 4, 3>(a, grid, s); break;
     default: launch_token<8, 4, 2>(a, grid, s); break;
     }
-    if (c.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3(c.workgroups - 1, std::min(cols, 4)), dim3(256), 0, s, a);
+    if (c.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3(c.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

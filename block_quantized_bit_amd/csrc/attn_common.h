@@ -99,6 +99,16 @@ __device__ inline void row_units(const AttnArgs& a, const SeqInfo& q, int i0, in
 
 __device__ inline int tiles_of(const TileShape& ts, int n) { return (n + ts.rows - 1) / ts.rows * ts.ht; }
 
+struct TileCount {
+    const AttnArgs& a;
+    TileShape ts;
+    __device__ uint32_t operator()(int b) const {
+        int r0, r1;
+        seq_rows(a.s, b, &r0, &r1);
+        return (uint32_t)tiles_of(ts, r1 - r0);
+    }
+};
+
 // Inclusive prefix sum over the wave.
 __device__ inline uint32_t wave_scan(uint32_t v) {
 #pragma unroll
