@@ -512,10 +512,8 @@ __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------------------------
-// Many rows per sequence (prompts): tiles of 128 columns, keys and values made fp16 once per workgroup.
+// Many rows per sequence (prompts): tiles of 128 or 256 columns, keys and values made fp16 once per workgroup.
 // ---------------------------------------------------------------------------------------------------------------
-
-constexpr int kRowCols = 128, kStep = 2;   // columns per tile; units (of 32 tokens) per step
 
 // One 16-byte chunk of a unit's K or V codes with the scales of its four words, on its way to LDS.
 template <bool Q41>
@@ -607,15 +605,16 @@ __device__ inline void store_chunk(const Chunk<Q41>& r, int c, int left, uint32_
     }
 }
 
-template <int NB, bool Q41>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_rows(AttnArgs a) {
+// Per step of KS units: every wave makes its share of the step's keys and values fp16 and puts them in LDS, in the order
+// the products take them; then each wave multiplies them with its 32 columns.  Two LDS buffers, one barrier per step; the
+// next step's codes are on their way meanwhile.
+template <int NB, bool Q41, int NW, int KS>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_rows(AttnArgs a) {
     constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), unit_lds = 64 * dim;   // fp16 bytes of a unit's K, or V
-    constexpr int chunks = kStep * dim;                            // 16-byte chunks of K codes in a step, and of V codes
-    constexpr int rounds = (2 * chunks + 255) / 256;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStep * unit_lds];
-    uint8_t* const lk = lds;
-    uint8_t* const lv = lds + kStep * unit_lds;
-    const TileShape ts = tile_shape(kRowCols, a.group);
+    constexpr int chunks = KS * dim;                               // 16-byte chunks of K codes in a step, and of V codes
+    constexpr int threads = NW * 64, rounds = (2 * chunks + threads - 1) / threads, buffer = 2 * KS * unit_lds;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * buffer];
+    const TileShape ts = tile_shape(NW * 32, a.group);
     const int heads = a.s.heads, tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), hl = lane >> 5;
     // heads vary fastest, so that a head's tiles (which read the same keys and values) tend to the same die; later tiles,
     // which see more, come first
@@ -633,7 +632,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
     int u0, u1;
     row_units(a, q, first, end, &u0, &u1);
     if (a.splits > 1) {
-        const int per = ((u1 - u0 + a.splits - 1) / a.splits + kStep - 1) / kStep * kStep;
+        const int per = ((u1 - u0 + a.splits - 1) / a.splits + KS - 1) / KS * KS;
         u0 += split * per;
         u1 = min(u1, u0 + per);
     }
@@ -686,23 +685,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
     const uint32_t f1024 = held(0x64006400u);
 
     // the step's units: where they are, or -1
-    int64_t where[kStep];
+    int64_t where[KS];
     Chunk<Q41> r[rounds];
     UnitWalk walk;
     walk.start(a.s, seq, h, u0);
     const auto fetch = [&](int u) {
 #pragma unroll
-        for (int k = 0; k < kStep; k++) {
+        for (int k = 0; k < KS; k++) {
             where[k] = u + k < u1 ? walk.at() : -1;
             walk.step(1);
         }
 #pragma unroll
         for (int i = 0; i < rounds; i++) {
-            const int id = i * 256 + tid, base = i * 256 + wave * 64;   // (chunks is a multiple of 64)
+            const int id = i * threads + tid, base = i * threads + wave * 64;   // (chunks is a multiple of 64)
             if (base >= 2 * chunks) break;
             const bool v = base >= chunks;
             const int c = v ? id - chunks : id, k = c / dim;
-            const int64_t p = k ? where[1] : where[0];
+            const int64_t p = k ? where[KS - 1] : where[0];
             if (p < 0) continue;
             const uint8_t* const codes = a.cache + p;
             if (v) load_chunk<NB, Q41, true>(codes + half, c - k * dim, &r[i]);
@@ -710,26 +709,27 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
         }
     };
     if (u0 < u1) fetch(u0);
-    for (int u = u0; u < u1; u += kStep) {
-        __syncthreads();   // the last step's reads are done
+    uint8_t* lk = lds;
+    for (int u = u0; u < u1; u += KS) {
+        uint8_t* const lv = lk + KS * unit_lds;
 #pragma unroll
         for (int i = 0; i < rounds; i++) {
-            const int id = i * 256 + tid, base = i * 256 + wave * 64;
+            const int id = i * threads + tid, base = i * threads + wave * 64;
             if (base >= 2 * chunks) break;
             const bool v = base >= chunks;
             const int c = v ? id - chunks : id, k = c / dim;
-            const int left = (k ? where[1] : where[0]) < 0 ? 0 : q.tokens - (u + k) * kUnit;
+            const int left = (k ? where[KS - 1] : where[0]) < 0 ? 0 : q.tokens - (u + k) * kUnit;
             if (left <= 0) r[i] = {};
             if (v) store_chunk<NB, Q41, true>(r[i], c - k * dim, left, f1024, lv + k * unit_lds);
             else store_chunk<NB, Q41, false>(r[i], c - k * dim, left, f1024, lk + k * unit_lds);
         }
-        bool there[kStep];
+        bool there[KS];
 #pragma unroll
-        for (int k = 0; k < kStep; k++) there[k] = where[k] >= 0;
+        for (int k = 0; k < KS; k++) there[k] = where[k] >= 0;
         __syncthreads();
-        if (u + kStep < u1) fetch(u + kStep);
+        if (u + KS < u1) fetch(u + KS);
 #pragma unroll
-        for (int k = 0; k < kStep; k++) {
+        for (int k = 0; k < KS; k++) {
             if (!there[k]) continue;
             f32x16 s;
 #pragma unroll
@@ -741,31 +741,36 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
             }
             const int t0 = (u + k) * kUnit;
             float e[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) e[i] = fmaf(s[i], sl2, -ref);
             if (t0 < lo_most || t0 + kUnit > hi_least) {
+                asm volatile("");   // (a branch: the compiler would else mask every unit)
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     const int t = t0 + 8 * (i >> 2) + 4 * hl + (i & 3);
-                    e[i] = t >= lo && t < hi ? s[i] * sl2 : -INFINITY;
+                    e[i] = t >= lo && t < hi ? e[i] : -INFINITY;
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; i++) e[i] = s[i] * sl2;
             }
-            float mx = e[0];
+            float most = e[0];
 #pragma unroll
-            for (int i = 1; i < 16; i++) mx = fmaxf(mx, e[i]);
-            if (__any(mx - ref > kRefMost)) {
+            for (int i = 1; i < 16; i++) most = fmaxf(most, e[i]);
+            if (__any(most > kRefMost)) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 16; i++) mx = fmaxf(mx, e[i] == -INFINITY ? -INFINITY : s[i] * sl2);
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
                 const float r2 = fmaxf(ref, mx - kRefBelow), alpha = r2 == ref ? 1.0f : exp2_fast(ref - r2);
 #pragma unroll
                 for (int b = 0; b < NB; b++) o[b] *= alpha;
                 l *= alpha;
                 ref = r2;
+#pragma unroll
+                for (int i = 0; i < 16; i++) e[i] = e[i] == -INFINITY ? -INFINITY : fmaf(s[i], sl2, -ref);
             }
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                e[i] = exp2_fast(e[i] - ref);
+                e[i] = exp2_fast(e[i]);
                 sum += e[i];
             }
             l += sum;
@@ -781,6 +786,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
                 }
             }
         }
+        lk = lk == lds ? lds + buffer : lds;
     }
     l += __shfl_xor(l, 32, 64);
     if (!valid) return;
@@ -813,7 +819,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
 // Workgroup (tile, head): the tile's columns, each shared out over a.splits workgroups of k_attn_rows.
 __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) JoinLds lds;
-    const TileShape ts = tile_shape(kRowCols, a.group);
+    const TileShape ts = tile_shape(a.tile_cols, a.group);
     const int heads = a.s.heads, h = blockIdx.x % heads, at = blockIdx.x / heads;
     uint32_t before;
     const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
@@ -822,7 +828,7 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
     const int tile = at - before;
     const Partials p(a);
     const auto slot = [&](int i) { return (int)blockIdx.x * a.splits + i; };
-    for (int col = blockIdx.y; col < kRowCols; col += gridDim.y) {
+    for (int col = blockIdx.y; col < a.tile_cols; col += gridDim.y) {
         int row, head;
         if (!tile_col(a, ts, tile, col, q.n, &row, &head)) break;
         join_column(a, p, a.splits, col, a.y + (int64_t)(q.r0 + row) * a.ldy + (int64_t)(h * a.group + head) * a.dim, slot, lds);
@@ -833,34 +839,40 @@ namespace {
 
 // Workgroups that a shared-out call has, and the units that each takes at least.
 constexpr int kShareWorkgroups = kJoinParts, kShareLeast = 24;
-// Columns per sequence, on average, from which a call takes tiles of 128 columns.
+// Columns per sequence, on average, from which a call takes tiles of 128 or 256 columns.
 constexpr int kManyCols = 33;
 // Tiles of 128 columns: workgroups that fill the chip twice, and units that a part has at least.
 constexpr int kRowWorkgroups = 512, kRowLeast = 16;
 
 // How a call runs.
 struct Schedule {
-    bool rows;           // tiles of 128 columns
+    int cols;            // columns per tile: 16, 128 or 256
     int64_t items;       // tiles x heads (at most)
     int workgroups;      // 16 columns: sequences shared out over so many (0: not)
-    int splits;          // 128 columns: parts per tile
-    int slots() const { return rows ? (splits > 1 ? (int)items * splits : 0) : 2 * workgroups; }
-    int cols() const { return rows ? kRowCols : kTokenCols; }
+    int splits;          // 128, 256 columns: parts per tile
+    int slots() const { return cols == kTokenCols ? 2 * workgroups : splits > 1 ? (int)items * splits : 0; }
 };
 
 Schedule schedule(const AttnArgs& a, bool share) {
     Schedule s{};
-    s.rows = a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch;
-    const TileShape ts = tile_shape(s.cols(), a.group);
-    s.items = tile_bound(ts, a.s.rows, a.s.batch, !a.s.row_start) * a.s.heads;
-    s.splits = 1;
+    const auto items = [&](int cols) {
+        s.cols = cols;
+        s.items = tile_bound(tile_shape(cols, a.group), a.s.rows, a.s.batch, !a.s.row_start) * a.s.heads;
+    };
     const int64_t units = ((int64_t)a.s.table_ld * a.s.page) / kUnit;   // of the longest sequence there can be
-    if (!share) return s;
-    if (s.rows) {
+    s.splits = 1;
+    if (a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch) {
+        items(256);
+        if (s.items < 256 || a.dim == 256) items(128);
         const int64_t most = std::min<int64_t>(kRowWorkgroups / s.items, units / kRowLeast);
-        s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 64));
-    } else if (units >= 32 && s.items < 4096 && s.items * (units + kTileCost) <= 0x7FFFFFFF) {   // (work is counted in 32 bits)
-        s.workgroups = kShareWorkgroups;
+        if (share) s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 64));
+    } else {
+        items(kTokenCols);
+        // Shared out, and joined by a second launch, where a sequence can be long: measured, 8 tiles of 1024 tokens take
+        // 12.9 us whole and 17.0 shared out, of 2048 tokens 22.0 and 17.1; 256 tiles of 2048 24.8 and 30.2, of 4096 42.9
+        // and 42.6 (equal lengths: unequal ones only gain).  Work is counted in 32 bits.
+        if (share && (s.items < 256 ? units >= 48 : units > 128) && s.items * (units + kTileCost) <= 0x7FFFFFFF)
+            s.workgroups = kShareWorkgroups;
     }
     return s;
 }
@@ -870,36 +882,37 @@ void launch_token(const AttnArgs& a, dim3 grid, hipStream_t s) {
     if (a.q41) hipLaunchKernelGGL((k_attn_token<NB, true, NW, D>), grid, dim3(NW * 64), 0, s, a);
     else hipLaunchKernelGGL((k_attn_token<NB, false, NW, D>), grid, dim3(NW * 64), 0, s, a);
 }
-template <int NB>
+template <int NB, int NW, int KS>
 void launch_rows(const AttnArgs& a, dim3 grid, hipStream_t s) {
-    if (a.q41) hipLaunchKernelGGL((k_attn_rows<NB, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_attn_rows<NB, false>), grid, dim3(256), 0, s, a);
+    if (a.q41) hipLaunchKernelGGL((k_attn_rows<NB, true, NW, KS>), grid, dim3(NW * 64), 0, s, a);
+    else hipLaunchKernelGGL((k_attn_rows<NB, false, NW, KS>), grid, dim3(NW * 64), 0, s, a);
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(const AttnArgs& a) {
     const Schedule s = schedule(a, true);
-    return (size_t)partial_bytes(s.slots(), s.cols(), a.dim) + s.workgroups * sizeof(OpenTile);
+    return (size_t)partial_bytes(s.slots(), s.cols, a.dim) + s.workgroups * sizeof(OpenTile);
 }
 
 hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     AttnArgs a = args;
     const Schedule c = schedule(a, a.ws != nullptr);
-    a.tile_cols = c.cols();
+    a.tile_cols = c.cols;
     a.workgroups = c.workgroups;
     a.least_units = kShareLeast;
     a.splits = c.splits;
     a.slots = c.slots();
     const TileShape ts = tile_shape(a.tile_cols, a.group);
     const int cols = std::min(a.tile_cols, (a.s.row_start ? ts.rows : 1) * a.group);   // that a tile can have
-    if (c.rows) {
+    if (c.cols != kTokenCols) {
         const dim3 grid((unsigned)(c.items * c.splits));
+        const bool wide = c.cols == 256;
         switch (a.dim) {
-        case 64: launch_rows<2>(a, grid, s); break;
-        case 96: launch_rows<3>(a, grid, s); break;
-        case 128: launch_rows<4>(a, grid, s); break;
-        default: launch_rows<8>(a, grid, s); break;
+        case 64: wide ? launch_rows<2, 8, 2>(a, grid, s) : launch_rows<2, 4, 2>(a, grid, s); break;
+        case 96: wide ? launch_rows<3, 8, 2>(a, grid, s) : launch_rows<3, 4, 2>(a, grid, s); break;
+        case 128: wide ? launch_rows<4, 8, 2>(a, grid, s) : launch_rows<4, 4, 2>(a, grid, s); break;
+        default: launch_rows<8, 4, 1>(a, grid, s); break;
         }
         if (c.splits > 1) hipLaunchKernelGGL(k_attn_join_rows, dim3((unsigned)c.items, std::min(cols, 16)), dim3(256), 0, s, a);
         return hipGetLastError();
