@@ -515,105 +515,120 @@ __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
 // Many rows per sequence (prompts): tiles of 128 or 256 columns, keys and values made fp16 once per workgroup.
 // ---------------------------------------------------------------------------------------------------------------
 
-// One 16-byte chunk of a unit's K or V codes with the scales of its four words, on its way to LDS.
+// What a thread makes fp16 in a step: two neighbouring words of a unit's K codes and the same two of its V codes.  K's
+// words have one scale each (a token's), V's four (the tokens').
 template <bool Q41>
-struct Chunk {
-    u32x4 w;
-    uint32_t d[4][2], m[Q41 ? 4 : 1][2];   // K: d[i][0] one scale; V: the scales of four tokens
+struct Pair {
+    uint32_t kw[2], kd[2], km[Q41 ? 2 : 1];
+    uint32_t vw[2], vd[2][2], vm[Q41 ? 2 : 1][2];
 };
 
-// Word i of chunk `c` (16 bytes) of a unit's codes: lane and word index.
+// Where the words' scales are and their fp16 values go.  The values are in the order in which the 32 x 32 x 16 products
+// take them, 1 KiB fragments of 16 bytes a lane: K: fragment (16 channels) lane 32 (g % 2) + token; V: fragment (block,
+// 16-token tile) lane 32 (g % 2) + channel, half g / 2 of its 16 bytes.  V's two words are the block's two tiles.
+struct PairPlace {
+    int code, ks[2], ko[2], vs, vo, token;   // token: V's byte 0 within a tile
+};
 template <int NB>
-__device__ inline void chunk_word(int c, int i, int* lane, int* wi) {
-    constexpr int full = NB / 2;
-    if (NB % 2 == 0 || c < full * 64) {
-        *lane = c & 63;
-        *wi = (c >> 6) * 4 + i;
-    } else {
-        *lane = (c - full * 64) * 2 + (i >> 1);
-        *wi = full * 4 + (i & 1);
+__device__ inline PairPlace pair_place(int p) {   // p: which 8 bytes of the unit's codes
+    const bool tail = NB % 2 && p >= NB / 2 * 128;
+    const int lane = tail ? p - NB / 2 * 128 : (p & 127) >> 1, w0 = tail ? 2 * NB - 2 : (p >> 7) * 4 + (p & 1) * 2;
+    const int g = lane >> 4, x = lane & 15;
+    PairPlace r;
+    r.code = p * 8;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const int tile = (w0 + j) / NB, b = (w0 + j) - tile * NB;
+        r.ks[j] = ((tile * 4 + (x >> 2)) * NB + b) * 8 + (x & 3) * 2;
+        r.ko[j] = (2 * b + (g >> 1)) * 1024 + ((g & 1) * 32 + 16 * tile + x) * 16;
     }
+    r.vs = (g * NB + (w0 >> 1)) * 8;
+    r.vo = w0 * 1024 + ((g & 1) * 32 + x) * 16 + (g >> 1) * 8;
+    r.token = 4 * g;
+    return r;
 }
 
-template <int NB, bool Q41, bool V>
-__device__ inline void load_chunk(const uint8_t* codes, int c, Chunk<Q41>* r) {
-    constexpr int dim = 32 * NB, plane = cache_plane_bytes(dim);
-    r->w = *reinterpret_cast<const u32x4*>(codes + c * 16);
-    const uint8_t* const sc = codes + 16 * dim;
+template <int NB, bool Q41>
+__device__ inline void load_pair(const uint8_t* unit, const PairPlace& at, Pair<Q41>* r) {
+    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), plane = cache_plane_bytes(dim);
+    const u32x2 k = *reinterpret_cast<const u32x2*>(unit + (uint32_t)at.code);
+    const u32x2 v = *reinterpret_cast<const u32x2*>(unit + (uint32_t)(half + at.code));
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        int lane, wi;
-        chunk_word<NB>(c, i, &lane, &wi);
-        if constexpr (V) {
-            const int b = wi >> 1, tile = wi & 1, at = ((tile * 4 + (lane >> 4)) * NB + b) * 8;
-            const u32x2 d = *reinterpret_cast<const u32x2*>(sc + at);
-            r->d[i][0] = d[0];
-            r->d[i][1] = d[1];
-            if constexpr (Q41) {
-                const u32x2 m = *reinterpret_cast<const u32x2*>(sc + plane + at);
-                r->m[i][0] = m[0];
-                r->m[i][1] = m[1];
-            }
-        } else {
-            const int tile = wi / NB, b = wi - tile * NB, t = lane & 15;
-            const int at = (((tile * 4 + (t >> 2)) * NB + b) * 4 + (t & 3)) * 2;
-            r->d[i][0] = *reinterpret_cast<const uint16_t*>(sc + at) * 0x10001u;
-            if constexpr (Q41) r->m[i][0] = *reinterpret_cast<const uint16_t*>(sc + plane + at) * 0x10001u;
+    for (int j = 0; j < 2; j++) {
+        r->kw[j] = k[j];
+        r->vw[j] = v[j];
+        r->kd[j] = *reinterpret_cast<const uint16_t*>(unit + (uint32_t)(16 * dim + at.ks[j]));
+        const u32x2 d = *reinterpret_cast<const u32x2*>(unit + (uint32_t)(half + 16 * dim + at.vs + j * 32 * NB));
+        r->vd[j][0] = d[0];
+        r->vd[j][1] = d[1];
+        if constexpr (Q41) {
+            r->km[j] = *reinterpret_cast<const uint16_t*>(unit + (uint32_t)(16 * dim + plane + at.ks[j]));
+            const u32x2 m = *reinterpret_cast<const u32x2*>(unit + (uint32_t)(half + 16 * dim + plane + at.vs + j * 32 * NB));
+            r->vm[j][0] = m[0];
+            r->vm[j][1] = m[1];
         }
     }
 }
 
-// The chunk's values as fp16 into the operand layouts of the 32 x 32 x 16 products (1 KiB fragments, 16 bytes a lane):
-// K: fragment s (channels 16 s ..), lane 32 (g % 2) + token; V: fragment (block, 16-token tile), lane 32 (g % 2) +
-// channel, half g / 2 of its 16 bytes.  `left`: tokens of the unit that are in the cache (V's others are made zero).
-template <int NB, bool Q41, bool V>
-__device__ inline void store_chunk(const Chunk<Q41>& r, int c, int left, uint32_t f1024, uint8_t* out) {
+// Only `left` (< 32) of the unit's tokens are in the cache: the others become zeros.
+template <bool Q41>
+__device__ inline void clear_pair(const PairPlace& at, int left, Pair<Q41>* r) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        int lane, wi;
-        chunk_word<NB>(c, i, &lane, &wi);
-        const int g = lane >> 4, x = lane & 15;
-        const uint32_t w = r.w[i];
-        if constexpr (V) {
-            const int b = wi >> 1, tile = wi & 1, t = 16 * tile + 4 * g;
-            uint32_t keep[2];
-            keep[0] = (t < left ? 0x0000FFFFu : 0u) | (t + 1 < left ? 0xFFFF0000u : 0u);
-            keep[1] = (t + 2 < left ? 0x0000FFFFu : 0u) | (t + 3 < left ? 0xFFFF0000u : 0u);
-            u32x2 lo, hi;
+    for (int j = 0; j < 2; j++) {
+        const int t = 16 * j + at.token;
+        const uint32_t k0 = (t < left ? 0x0000FFFFu : 0u) | (t + 1 < left ? 0xFFFF0000u : 0u);
+        const uint32_t k1 = (t + 2 < left ? 0x0000FFFFu : 0u) | (t + 3 < left ? 0xFFFF0000u : 0u);
+        r->vd[j][0] &= k0;
+        r->vd[j][1] &= k1;
+        if (left <= 0) r->kd[j] = 0;
+        if constexpr (Q41) {
+            r->vm[j][0] &= k0;
+            r->vm[j][1] &= k1;
+            if (left <= 0) r->km[j] = 0;
+        }
+    }
+}
+
+template <bool Q41>
+__device__ inline void store_pair(const Pair<Q41>& r, const PairPlace& at, uint32_t f1024, uint8_t* k, uint8_t* v) {
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const f16x2 d = as_f16x2(r.d[i][k] & keep[k]);
-                f16x2 m = {};
-                if constexpr (Q41) m = as_f16x2(r.m[i][k] & keep[k]);
-                lo[k] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(w & 0x0F0F0F0Fu, k), d, m));
-                hi[k] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair((w >> 4) & 0x0F0F0F0Fu, k), d, m));
-            }
-            uint8_t* const p = out + (b * 2 + tile) * 1024 + ((g & 1) * 32 + x) * 16 + (g >> 1) * 8;
-            *reinterpret_cast<u32x2*>(p) = lo;
-            *reinterpret_cast<u32x2*>(p + 256) = hi;
-        } else {
-            const int tile = wi / NB, b = wi - tile * NB;
-            const f16x2 d = as_f16x2(r.d[i][0]);
+    for (int j = 0; j < 2; j++) {
+        const f16x2 d = as_f16x2(r.kd[j] * 0x10001u);
+        f16x2 m = {};
+        if constexpr (Q41) m = as_f16x2(r.km[j] * 0x10001u);
+        u32x4 x;
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[i] = __builtin_bit_cast(uint32_t, code_value<Q41>(as_f16x2(nibble_pair(r.kw[j], i, f1024)), d, m));
+        *reinterpret_cast<u32x4*>(k + at.ko[j]) = x;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        const uint32_t wl = r.vw[j] & 0x0F0F0F0Fu, wh = (r.vw[j] >> 4) & 0x0F0F0F0Fu;
+        u32x2 lo, hi;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const f16x2 d = as_f16x2(r.vd[j][i]);
             f16x2 m = {};
-            if constexpr (Q41) m = as_f16x2(r.m[i][0]);
-            u32x4 v;
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                v[k] = __builtin_bit_cast(uint32_t, code_value<Q41>(as_f16x2(nibble_pair(w, k, f1024)), d, m));
-            *reinterpret_cast<u32x4*>(out + (2 * b + (g >> 1)) * 1024 + ((g & 1) * 32 + 16 * tile + x) * 16) = v;
+            if constexpr (Q41) m = as_f16x2(r.vm[j][i]);
+            lo[i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wl, i), d, m));
+            hi[i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wh, i), d, m));
         }
+        *reinterpret_cast<u32x2*>(v + at.vo + j * 1024) = lo;
+        *reinterpret_cast<u32x2*>(v + at.vo + j * 1024 + 256) = hi;
     }
 }
 
-// Per step of KS units: every wave makes its share of the step's keys and values fp16 and puts them in LDS, in the order
-// the products take them; then each wave multiplies them with its 32 columns.  Two LDS buffers, one barrier per step; the
-// next step's codes are on their way meanwhile.
+// Per step of KS units: every wave makes its share of a later step's keys and values fp16 and puts them in LDS, in the
+// order the products take them; and it multiplies this step's with its 32 columns.  A ring of LDS buffers, one barrier per
+// step; the codes of the step after are on their way meanwhile.  A wave's products and its vector arithmetic are
+// independent of each other, so that the matrix unit works beside the vector unit: the scores of unit i + 1 beside the
+// exponentials of unit i, the sums over unit i's values beside the maximum of unit i + 1 and the conversions to fp16.
 template <int NB, bool Q41, int NW, int KS>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_rows(AttnArgs a) {
-    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), unit_lds = 64 * dim;   // fp16 bytes of a unit's K, or V
-    constexpr int chunks = KS * dim;                               // 16-byte chunks of K codes in a step, and of V codes
-    constexpr int threads = NW * 64, rounds = (2 * chunks + threads - 1) / threads, buffer = 2 * KS * unit_lds;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * buffer];
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows(AttnArgs a) {
+    constexpr int dim = 32 * NB, unit_lds = 64 * dim, buffer = 2 * KS * unit_lds;   // fp16 bytes of a unit's K, or V; a step
+    constexpr int threads = NW * 64, pairs = KS * 2 * dim, rounds = (pairs + threads - 1) / threads;
+    constexpr int ahead = KS > 1 ? 2 : 3;   // steps: keys are read a unit before their product, two before their use
+    __shared__ __attribute__((aligned(16))) uint8_t lds[(ahead + 1) * buffer];
     const TileShape ts = tile_shape(NW * 32, a.group);
     const int heads = a.s.heads, tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), hl = lane >> 5;
     // heads vary fastest, so that a head's tiles (which read the same keys and values) tend to the same die; later tiles,
@@ -638,13 +653,72 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
     }
 
     // this wave's 32 columns
-    const int col = wave * 32 + (lane & 31);
-    int row, head;
-    const bool valid = tile_col(a, ts, tile, col, q.n, &row, &head);
-    int lo, hi, lo_most, hi_least, x;
+    int row, head, lo, hi, lo_most, hi_least, x;
+    const bool valid = tile_col(a, ts, tile, wave * 32 + (lane & 31), q.n, &row, &head);
     row_tokens(a, q, valid ? row : first, &lo, &hi);
     row_tokens(a, q, first, &x, &hi_least);
     row_tokens(a, q, end - 1, &lo_most, &x);
+
+    // this thread's pairs of words: unit (id / 2 dim) of the step, 8 bytes (id % 2 dim) of its codes
+    const uint32_t f1024 = held(0x64006400u);
+    int64_t where[KS];                      // the fetched step's units, or -1
+    Pair<Q41> r[rounds];
+    PairPlace place[rounds];
+#pragma unroll
+    for (int i = 0; i < rounds; i++) place[i] = pair_place<NB>((i * threads + tid) % (2 * dim));
+    UnitWalk walk;
+    walk.start(a.s, seq, h, u0);
+    const auto pair_unit = [&](int i) { return uniform((i * threads + wave * 64) / (2 * dim)); };   // (2 dim % 64 == 0)
+    int64_t fetched = u0;                   // unit
+    const auto fetch = [&]() {
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+            where[k] = fetched + k < u1 ? walk.at() : -1;
+            walk.step(1);
+        }
+        fetched += KS;
+#pragma unroll
+        for (int i = 0; i < rounds; i++) {
+            if (i * threads + wave * 64 >= pairs) break;
+            const int64_t p = KS > 1 && pair_unit(i) ? where[KS - 1] : where[0];
+            // (an absent unit's loads are of the pool's first one: cleared below)
+            load_pair<NB, Q41>(a.cache + (p < 0 ? 0 : p), place[i], &r[i]);
+        }
+    };
+    // the fetched step's tokens that are not in the cache are made zeros
+    const auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < rounds; i++) {
+            if (i * threads + wave * 64 >= pairs) break;
+            const int k = pair_unit(i);
+            const int64_t p = KS > 1 && k ? where[KS - 1] : where[0], left = q.tokens - (fetched - KS + k) * kUnit;
+            if (p < 0 || left < kUnit) clear_pair<Q41>(place[i], p < 0 || left < 0 ? 0 : (int)left, &r[i]);
+        }
+    };
+    const auto put = [&](uint8_t* to) {
+#pragma unroll
+        for (int i = 0; i < rounds; i++) {
+            if (rounds * threads > pairs && i * threads + wave * 64 >= pairs) break;
+            const int k = pair_unit(i);
+            store_pair<Q41>(r[i], place[i], f1024, to + k * unit_lds, to + (KS + k) * unit_lds);
+        }
+    };
+
+    // The first `ahead` steps' values, one after the other.
+    uint32_t has = 0;                       // bit i: unit i of this step and the `ahead` steps after it has tokens
+    const auto note = [&](int step) {
+#pragma unroll
+        for (int k = 0; k < KS; k++) has |= (where[k] >= 0 ? 1u : 0u) << (step * KS + k);
+    };
+#pragma unroll
+    for (int i = 0; i < ahead; i++) {
+        fetch();
+        note(i);
+        clear();
+        put(lds + i * buffer);
+    }
+    fetch();
+
     // queries as fp16, scaled by a power of two per column so that the largest is in [2^14, 2^15)
     f16x8 qf[2 * NB];
     float sl2 = a.scale_log2;
@@ -660,9 +734,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
             for (int k = 0; k < 4; k++) big = max(big, max(v[s][k] & 0x7FFFu, (v[s][k] >> 16) & 0x7FFFu));
         }
         big = max(big, (uint32_t)__shfl_xor((int)big, 32, 64));
-        const int k = min(141 - (int)(big >> 7), 100);              // exponent bits of bf16: value < 2^(e - 126)
-        const float up = ldexpf(1.0f, big == 0 ? 0 : k);
-        sl2 *= ldexpf(1.0f, big == 0 ? 0 : -k);
+        const int k = big == 0 ? 0 : min(141 - (int)(big >> 7), 100);   // exponent bits of bf16: value < 2^(e - 126)
+        const float up = ldexpf(1.0f, k);
+        sl2 *= ldexpf(1.0f, -k);
 #pragma unroll
         for (int s = 0; s < 2 * NB; s++) {
             float f[8];
@@ -682,125 +756,136 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
         for (int i = 0; i < 16; i++) o[b][i] = 0.0f;
     float ref = -FLT_MAX, l = 0.0f;
-    const uint32_t f1024 = held(0x64006400u);
-
-    // the step's units: where they are, or -1
-    int64_t where[KS];
-    Chunk<Q41> r[rounds];
-    UnitWalk walk;
-    walk.start(a.s, seq, h, u0);
-    const auto fetch = [&](int u) {
+    constexpr int F = 2 * NB;               // operands of a unit's keys, and of its values
+    f16x8 kf[F], vf[F];
+    f32x16 s;                               // the scores of the unit after the one whose exponentials are taken
+    float e[16], most;
+    const auto read_k = [&](const uint8_t* at) {
 #pragma unroll
-        for (int k = 0; k < KS; k++) {
-            where[k] = u + k < u1 ? walk.at() : -1;
-            walk.step(1);
-        }
-#pragma unroll
-        for (int i = 0; i < rounds; i++) {
-            const int id = i * threads + tid, base = i * threads + wave * 64;   // (chunks is a multiple of 64)
-            if (base >= 2 * chunks) break;
-            const bool v = base >= chunks;
-            const int c = v ? id - chunks : id, k = c / dim;
-            const int64_t p = k ? where[KS - 1] : where[0];
-            if (p < 0) continue;
-            const uint8_t* const codes = a.cache + p;
-            if (v) load_chunk<NB, Q41, true>(codes + half, c - k * dim, &r[i]);
-            else load_chunk<NB, Q41, false>(codes, c - k * dim, &r[i]);
-        }
+        for (int f = 0; f < F; f++) kf[f] = *reinterpret_cast<const f16x8*>(at + f * 1024 + lane * 16);
     };
-    if (u0 < u1) fetch(u0);
-    uint8_t* lk = lds;
-    for (int u = u0; u < u1; u += KS) {
-        uint8_t* const lv = lk + KS * unit_lds;
+    const auto read_v = [&](const uint8_t* at, int c) {   // of the unit's first, second 16 tokens
 #pragma unroll
-        for (int i = 0; i < rounds; i++) {
-            const int id = i * threads + tid, base = i * threads + wave * 64;
-            if (base >= 2 * chunks) break;
-            const bool v = base >= chunks;
-            const int c = v ? id - chunks : id, k = c / dim;
-            const int left = (k ? where[KS - 1] : where[0]) < 0 ? 0 : q.tokens - (u + k) * kUnit;
-            if (left <= 0) r[i] = {};
-            if (v) store_chunk<NB, Q41, true>(r[i], c - k * dim, left, f1024, lv + k * unit_lds);
-            else store_chunk<NB, Q41, false>(r[i], c - k * dim, left, f1024, lk + k * unit_lds);
-        }
-        bool there[KS];
+        for (int b = 0; b < NB; b++) vf[2 * b + c] = *reinterpret_cast<const f16x8*>(at + (2 * b + c) * 1024 + lane * 16);
+    };
+    const auto scores = [&]() {
 #pragma unroll
-        for (int k = 0; k < KS; k++) there[k] = where[k] >= 0;
-        __syncthreads();
-        if (u + KS < u1) fetch(u + KS);
+        for (int i = 0; i < 16; i++) s[i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; k++) {
-            if (!there[k]) continue;
-            f32x16 s;
+        for (int f = 0; f < F; f++) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[f], qf[f], s, 0, 0, 0);
+    };
+    const auto exponents = [&]() {
 #pragma unroll
-            for (int i = 0; i < 16; i++) s[i] = 0.0f;
+        for (int i = 0; i < 16; i++) e[i] = fmaf(s[i], sl2, -ref);
+        most = e[0];
 #pragma unroll
-            for (int f = 0; f < 2 * NB; f++) {
-                const f16x8 kf = *reinterpret_cast<const f16x8*>(lk + k * unit_lds + f * 1024 + lane * 16);
-                s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[f], s, 0, 0, 0);
-            }
-            const int t0 = (u + k) * kUnit;
-            float e[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) e[i] = fmaf(s[i], sl2, -ref);
-            if (t0 < lo_most || t0 + kUnit > hi_least) {
-                asm volatile("");   // (a branch: the compiler would else mask every unit)
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int t = t0 + 8 * (i >> 2) + 4 * hl + (i & 3);
-                    e[i] = t >= lo && t < hi ? e[i] : -INFINITY;
-                }
-            }
-            float most = e[0];
-#pragma unroll
-            for (int i = 1; i < 16; i++) most = fmaxf(most, e[i]);
-            if (__any(most > kRefMost)) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 16; i++) mx = fmaxf(mx, e[i] == -INFINITY ? -INFINITY : s[i] * sl2);
-                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                const float r2 = fmaxf(ref, mx - kRefBelow), alpha = r2 == ref ? 1.0f : exp2_fast(ref - r2);
-#pragma unroll
-                for (int b = 0; b < NB; b++) o[b] *= alpha;
-                l *= alpha;
-                ref = r2;
-#pragma unroll
-                for (int i = 0; i < 16; i++) e[i] = e[i] == -INFINITY ? -INFINITY : fmaf(s[i], sl2, -ref);
-            }
-            float sum = 0.0f;
+        for (int i = 1; i < 16; i++) most = fmaxf(most, e[i]);
+    };
+    // masks, and a new reference, where the unit needs them
+    const auto settle = [&](int u, bool there) {
+        const int t0 = u * kUnit;
+        if (t0 < lo_most || t0 + kUnit > hi_least || !there) {
+            const int lo2 = there ? lo - t0 : kUnit, hi2 = hi - t0;
+            most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                e[i] = exp2_fast(e[i]);
-                sum += e[i];
-            }
-            l += sum;
-#pragma unroll
-            for (int c = 0; c < 2; c++) {
-                const u32x4 p = {pack_f16(e[8 * c], e[8 * c + 1]), pack_f16(e[8 * c + 2], e[8 * c + 3]),
-                                 pack_f16(e[8 * c + 4], e[8 * c + 5]), pack_f16(e[8 * c + 6], e[8 * c + 7])};
-                const f16x8 pf = __builtin_bit_cast(f16x8, p);
-#pragma unroll
-                for (int b = 0; b < NB; b++) {
-                    const f16x8 vf = *reinterpret_cast<const f16x8*>(lv + k * unit_lds + (b * 2 + c) * 1024 + lane * 16);
-                    o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf, o[b], 0, 0, 0);
-                }
+                const int t = 8 * (i >> 2) + 4 * hl + (i & 3);
+                e[i] = t >= lo2 && t < hi2 ? e[i] : -INFINITY;
+                most = fmaxf(most, e[i]);
             }
         }
-        lk = lk == lds ? lds + buffer : lds;
+        if (__any(most > kRefMost)) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; i++) mx = fmaxf(mx, e[i] == -INFINITY ? -INFINITY : s[i] * sl2);
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            const float r2 = fmaxf(ref, mx - kRefBelow), alpha = r2 == ref ? 1.0f : exp2_fast(ref - r2);
+#pragma unroll
+            for (int b = 0; b < NB; b++) o[b] *= alpha;
+            l *= alpha;
+            ref = r2;
+#pragma unroll
+            for (int i = 0; i < 16; i++) e[i] = e[i] == -INFINITY ? -INFINITY : fmaf(s[i], sl2, -ref);
+        }
+    };
+    if (u0 < u1) {
+        __syncthreads();
+        read_k(lds);
+        scores();
+        exponents();
+        settle(u0, has & 1);
+        read_k(lds + (KS > 1 ? unit_lds : buffer));
+        uint8_t *lk = lds, *ln = lds + buffer, *lp = lds + ahead * buffer;   // this step's, the next one's, the one to fill
+        const auto next = [&](uint8_t* at) { return at == lds + ahead * buffer ? lds : at + buffer; };
+        for (int u = u0; u < u1; u += KS) {
+            note(ahead);
+            clear();
+#pragma unroll
+            for (int k = 0; k < KS; k++) {
+                // (behind the last unit the scores are of zeros, and not used)
+                read_v(lk + (KS + k) * unit_lds, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                scores();
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    e[i] = exp2_fast(e[i]);
+                    sum += e[i];
+                }
+                l += sum;
+                f16x8 pf[2];
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+                    pf[c] = __builtin_bit_cast(f16x8, (u32x4){pack_f16(e[8 * c], e[8 * c + 1]), pack_f16(e[8 * c + 2], e[8 * c + 3]),
+                                                              pack_f16(e[8 * c + 4], e[8 * c + 5]), pack_f16(e[8 * c + 6], e[8 * c + 7])});
+                asm volatile("" : "+v"(l));
+#pragma unroll
+                for (int f = 0; f < F; f++) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x402, (40 + F - 1) / F, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                // (the second half of V now: its registers were the probabilities'); keys of the unit after the next
+                read_v(lk + (KS + k) * unit_lds, 1);
+                read_k(KS == 1 ? next(ln) : k == 0 ? ln : ln + unit_lds);
+#pragma unroll
+                for (int f = 0; f < F; f++) {
+                    const int b = f % NB, c = f / NB;
+                    o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[2 * b + c], pf[c], o[b], 0, 0, 0);
+                }
+                if (k == 0) put(lp);
+                exponents();
+                asm volatile("" : "+v"(most));
+#pragma unroll
+                for (int f = 0; f < F; f++) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+                    if (k == 0) __builtin_amdgcn_sched_group_barrier(0x402, (24 + 64 * rounds + F - 1) / F, 1);
+                    else __builtin_amdgcn_sched_group_barrier(0x402, (24 + F - 1) / F, 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                if (k == 0) fetch();
+                settle(u + k + 1, has >> (k + 1) & 1);
+            }
+            has >>= KS;
+            lk = ln;
+            ln = next(ln);
+            lp = next(lp);
+            __syncthreads();
+        }
     }
     l += __shfl_xor(l, 32, 64);
     if (!valid) return;
     if (a.splits > 1) {
         const Partials p(a);
-        const int slot = ((int)before + tile) * heads + h;
-        float* const po = p.sums(slot * a.splits + split, col);
+        const int slot = (((int)before + tile) * heads + h) * a.splits + split, col = wave * 32 + (lane & 31);
+        float* const po = p.sums(slot, col);
 #pragma unroll
         for (int b = 0; b < NB; b++)
 #pragma unroll
             for (int k = 0; k < 4; k++)
                 *reinterpret_cast<f32x4*>(po + 32 * b + 8 * k + 4 * hl) = (f32x4){o[b][4 * k], o[b][4 * k + 1], o[b][4 * k + 2], o[b][4 * k + 3]};
         if (hl == 0) {
-            float* const st = p.stat(slot * a.splits + split, col);
+            float* const st = p.stat(slot, col);
             st[0] = ref;
             st[1] = l;
         }
@@ -910,8 +995,8 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
         const bool wide = c.cols == 256;
         switch (a.dim) {
         case 64: wide ? launch_rows<2, 8, 2>(a, grid, s) : launch_rows<2, 4, 2>(a, grid, s); break;
-        case 96: wide ? launch_rows<3, 8, 2>(a, grid, s) : launch_rows<3, 4, 2>(a, grid, s); break;
-        case 128: wide ? launch_rows<4, 8, 2>(a, grid, s) : launch_rows<4, 4, 2>(a, grid, s); break;
+        case 96: wide ? launch_rows<3, 8, 2>(a, grid, s) : launch_rows<3, 4, 1>(a, grid, s); break;
+        case 128: wide ? launch_rows<4, 8, 2>(a, grid, s) : launch_rows<4, 4, 1>(a, grid, s); break;
         default: launch_rows<8, 4, 1>(a, grid, s); break;
         }
         if (c.splits > 1) hipLaunchKernelGGL(k_attn_join_rows, dim3((unsigned)c.items, std::min(cols, 16)), dim3(256), 0, s, a);

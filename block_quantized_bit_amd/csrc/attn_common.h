@@ -171,6 +171,7 @@ struct UnitWalk {
     int j, k;               // page and unit within it
     int64_t pages, head_units, unit_bytes, per_page;
     int entry;              // of page j
+    int64_t cur;            // byte offset of the unit, or -1
 
     __device__ void start(const Seqs& q, int seq, int head, int unit) {
         upp = q.upp;
@@ -184,6 +185,7 @@ struct UnitWalk {
         k = unit - j * upp;
         entry = seq;
         read();
+        fresh = true;
     }
     __device__ void read() {
         if (table) entry = j < table_ld ? read_const(table, j) : -1;
@@ -191,18 +193,23 @@ struct UnitWalk {
     }
     __device__ void step(int n) {
         k += n;
-        if (k >= upp) {
-            do {
-                k -= upp;
-                j++;
-            } while (k >= upp);
-            read();
+        if (k < upp) {
+            cur = cur < 0 ? cur : cur + n * unit_bytes;
+            return;
         }
+        do {
+            k -= upp;
+            j++;
+        } while (k >= upp);
+        read();
+        fresh = true;
     }
-    // byte offset of the unit, or -1
-    __device__ int64_t at() const {
-        return entry >= 0 && entry < pages ? ((int64_t)entry * per_page + head_units + k) * unit_bytes : -1;
+    __device__ int64_t at() {
+        if (fresh) cur = entry >= 0 && entry < pages ? ((int64_t)entry * per_page + head_units + k) * unit_bytes : -1;
+        fresh = false;
+        return cur;
     }
+    bool fresh;             // cur is to be made from entry
 };
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
