@@ -669,8 +669,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     UnitWalk walk;
     walk.start(a.s, seq, h, u0);
     const auto pair_unit = [&](int i) { return uniform((i * threads + wave * 64) / (2 * dim)); };   // (2 dim % 64 == 0)
-    int64_t fetched = u0;                   // unit
-    const auto fetch = [&]() {
+    int fetched = u0;                       // unit
+    const auto fetch = [&](Pair<Q41>* r, int64_t* where) {
 #pragma unroll
         for (int k = 0; k < KS; k++) {
             where[k] = fetched + k < u1 ? walk.at() : -1;
@@ -685,17 +685,18 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
             load_pair<NB, Q41>(a.cache + (p < 0 ? 0 : p), place[i], &r[i]);
         }
     };
-    // the fetched step's tokens that are not in the cache are made zeros
-    const auto clear = [&]() {
+    // the tokens of step u that are not in the cache are made zeros
+    const auto clear = [&](Pair<Q41>* r, const int64_t* where, int u) {
 #pragma unroll
         for (int i = 0; i < rounds; i++) {
             if (i * threads + wave * 64 >= pairs) break;
             const int k = pair_unit(i);
-            const int64_t p = KS > 1 && k ? where[KS - 1] : where[0], left = q.tokens - (fetched - KS + k) * kUnit;
-            if (p < 0 || left < kUnit) clear_pair<Q41>(place[i], p < 0 || left < 0 ? 0 : (int)left, &r[i]);
+            const int64_t p = KS > 1 && k ? where[KS - 1] : where[0];
+            const int left = p < 0 ? 0 : max(0, q.tokens - (u + k) * kUnit);
+            if (left < kUnit) clear_pair<Q41>(place[i], left, &r[i]);
         }
     };
-    const auto put = [&](uint8_t* to) {
+    const auto put = [&](const Pair<Q41>* r, uint8_t* to) {
 #pragma unroll
         for (int i = 0; i < rounds; i++) {
             if (rounds * threads > pairs && i * threads + wave * 64 >= pairs) break;
@@ -704,35 +705,43 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
         }
     };
 
-    // The first `ahead` steps' values, one after the other.
+    // The first `ahead` steps, all requested before the first is used.
     uint32_t has = 0;                       // bit i: unit i of this step and the `ahead` steps after it has tokens
-    const auto note = [&](int step) {
+    const auto note = [&](const int64_t* where, int step) {
 #pragma unroll
         for (int k = 0; k < KS; k++) has |= (where[k] >= 0 ? 1u : 0u) << (step * KS + k);
     };
+    const uint16_t* const qp = a.q + (int64_t)(q.r0 + row) * a.ldq + (int64_t)(h * a.group + head) * dim + 8 * hl;
+    u32x4 qv[2 * NB];
+    {
+        Pair<Q41> r0[ahead][rounds];
+        int64_t w0[ahead][KS];
 #pragma unroll
-    for (int i = 0; i < ahead; i++) {
-        fetch();
-        note(i);
-        clear();
-        put(lds + i * buffer);
+        for (int i = 0; i < ahead; i++) fetch(r0[i], w0[i]);
+#pragma unroll
+        for (int s = 0; s < 2 * NB; s++) {
+            qv[s] = (u32x4){0, 0, 0, 0};
+            if (valid) qv[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < ahead; i++) {
+            note(w0[i], i);
+            clear(r0[i], w0[i], u0 + i * KS);
+            put(r0[i], lds + i * buffer);
+        }
     }
-    fetch();
+    fetch(r, where);
 
     // queries as fp16, scaled by a power of two per column so that the largest is in [2^14, 2^15)
     f16x8 qf[2 * NB];
     float sl2 = a.scale_log2;
     {
-        const uint16_t* qp = a.q + (int64_t)(q.r0 + row) * a.ldq + (int64_t)(h * a.group + head) * dim + 8 * hl;
-        u32x4 v[2 * NB];
         uint32_t big = 0;
 #pragma unroll
-        for (int s = 0; s < 2 * NB; s++) {
-            v[s] = (u32x4){0, 0, 0, 0};
-            if (valid) v[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+        for (int s = 0; s < 2 * NB; s++)
 #pragma unroll
-            for (int k = 0; k < 4; k++) big = max(big, max(v[s][k] & 0x7FFFu, (v[s][k] >> 16) & 0x7FFFu));
-        }
+            for (int k = 0; k < 4; k++) big = max(big, max(qv[s][k] & 0x7FFFu, (qv[s][k] >> 16) & 0x7FFFu));
         big = max(big, (uint32_t)__shfl_xor((int)big, 32, 64));
         const int k = big == 0 ? 0 : min(141 - (int)(big >> 7), 100);   // exponent bits of bf16: value < 2^(e - 126)
         const float up = ldexpf(1.0f, k);
@@ -742,8 +751,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
             float f[8];
 #pragma unroll
             for (int k2 = 0; k2 < 4; k2++) {
-                f[2 * k2] = __uint_as_float(v[s][k2] << 16) * up;
-                f[2 * k2 + 1] = __uint_as_float(v[s][k2] & 0xFFFF0000u) * up;
+                f[2 * k2] = __uint_as_float(qv[s][k2] << 16) * up;
+                f[2 * k2 + 1] = __uint_as_float(qv[s][k2] & 0xFFFF0000u) * up;
             }
             const u32x4 p = {pack_f16(f[0], f[4]), pack_f16(f[1], f[5]), pack_f16(f[2], f[6]), pack_f16(f[3], f[7])};
             qf[s] = __builtin_bit_cast(f16x8, p);
@@ -818,8 +827,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
         uint8_t *lk = lds, *ln = lds + buffer, *lp = lds + ahead * buffer;   // this step's, the next one's, the one to fill
         const auto next = [&](uint8_t* at) { return at == lds + ahead * buffer ? lds : at + buffer; };
         for (int u = u0; u < u1; u += KS) {
-            note(ahead);
-            clear();
+            note(where, ahead);
+            clear(r, where, u + ahead * KS);
 #pragma unroll
             for (int k = 0; k < KS; k++) {
                 // (behind the last unit the scores are of zeros, and not used)
@@ -853,7 +862,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
                     const int b = f % NB, c = f / NB;
                     o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[2 * b + c], pf[c], o[b], 0, 0, 0);
                 }
-                if (k == 0) put(lp);
+                if (k == 0) put(r, lp);
                 exponents();
                 asm volatile("" : "+v"(most));
 #pragma unroll
@@ -863,7 +872,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
                     else __builtin_amdgcn_sched_group_barrier(0x402, (24 + F - 1) / F, 1);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                if (k == 0) fetch();
+                if (k == 0) fetch(r, where);
                 settle(u + k + 1, has >> (k + 1) & 1);
             }
             has >>= KS;
@@ -924,10 +933,12 @@ namespace {
 
 // Workgroups that a shared-out call has, and the units that each takes at least.
 constexpr int kShareWorkgroups = kJoinParts, kShareLeast = 24;
-// Columns per sequence, on average, from which a call takes tiles of 128 or 256 columns.
-constexpr int kManyCols = 33;
-// Tiles of 128 columns: workgroups that fill the chip twice, and units that a part has at least.
-constexpr int kRowWorkgroups = 512, kRowLeast = 16;
+// Columns per sequence, on average, from which a call takes tiles of 128 or 256 columns: measured in us, tiles of 16 and
+// of 128, 16 sequences of 4096 tokens, 8 x 4 heads of 128: 64 columns 56 and 110, 128 columns 108 and 126; one of 65536
+// tokens, 64 columns 71 and 67, 256 columns 220 and 146.
+constexpr int kManyCols = 129;
+// Tiles of 128 columns: with fewer (tiles x heads) than this their tokens are shared out; units that a part has at least.
+constexpr int kRowItems = 128, kRowLeast = 16;
 
 // How a call runs.
 struct Schedule {
@@ -949,14 +960,14 @@ Schedule schedule(const AttnArgs& a, bool share) {
     if (a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch) {
         items(256);
         if (s.items < 256 || a.dim == 256) items(128);
-        const int64_t most = std::min<int64_t>(kRowWorkgroups / s.items, units / kRowLeast);
-        if (share) s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 64));
+        if (share && s.items <= kRowItems)
+            s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * kRowItems / s.items, units / kRowLeast, 64}));
     } else {
         items(kTokenCols);
-        // Shared out, and joined by a second launch, where a sequence can be long: measured, 8 tiles of 1024 tokens take
-        // 12.9 us whole and 17.0 shared out, of 2048 tokens 22.0 and 17.1; 256 tiles of 2048 24.8 and 30.2, of 4096 42.9
-        // and 42.6 (equal lengths: unequal ones only gain).  Work is counted in 32 bits.
-        if (share && (s.items < 256 ? units >= 48 : units > 128) && s.items * (units + kTileCost) <= 0x7FFFFFFF)
+        // Shared out, and joined by a second launch, where a sequence can be long.  Measured in us, whole and shared out,
+        // 8 heads of 128: 8 tiles of 1024 tokens 11.2 and 17.0, of 2048 tokens 18 and 17.1; 256 tiles of 2048 24.8 and
+        // 30.2, of 4096 42.9 and 42.6 (equal lengths: unequal ones only gain).  Work is counted in 32 bits.
+        if (share && units > (s.items < 256 ? 64 : 96) && s.items * (units + kTileCost) <= 0x7FFFFFFF)
             s.workgroups = kShareWorkgroups;
     }
     return s;
@@ -999,14 +1010,17 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
         case 128: wide ? launch_rows<4, 8, 2>(a, grid, s) : launch_rows<4, 4, 1>(a, grid, s); break;
         default: launch_rows<8, 4, 1>(a, grid, s); break;
         }
-        if (c.splits > 1) hipLaunchKernelGGL(k_attn_join_rows, dim3((unsigned)c.items, std::min(cols, 16)), dim3(256), 0, s, a);
+        if (c.splits > 1) hipLaunchKernelGGL(k_attn_join_rows, dim3((unsigned)c.items, std::min(cols, 64)), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)(c.workgroups ? c.workgroups : c.items));
+    // With at most a tile per compute unit eight waves share a tile's tokens (1024 tokens, 8 tiles of 4 x 128: 13.0 ->
+    // 11.2 us; 80 tiles of 1500 x 64: 13.5 -> 10.7); with more, four (320 tiles of 1500 x 64: 21.0 -> 17.1 us).
+    const bool few = !c.workgroups && c.items <= 256;
     switch (a.dim) {
-    case 64: launch_token<2, 4, 4>(a, grid, s); break;
-    case 96: launch_token<3, 4, 3>(a, grid, s); break;
-    case 128: launch_token<4, 4, 3>(a, grid, s); break;
+    case 64: few ? launch_token<2, 8, 3>(a, grid, s) : launch_token<2, 4, 4>(a, grid, s); break;
+    case 96: few ? launch_token<3, 8, 3>(a, grid, s) : launch_token<3, 4, 3>(a, grid, s); break;
+    case 128: few ? launch_token<4, 8, 3>(a, grid, s) : launch_token<4, 4, 3>(a, grid, s); break;
     default: launch_token<8, 4, 2>(a, grid, s); break;
     }
     if (c.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3(c.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);

@@ -67,6 +67,21 @@ ROWS = [
     (256, 1, 4, 64, [65, 3], [600, 3], 1, 0),
     (256, 2, 2, 32, [90], [123], 1, 40),
     (128, 1, 150, 64, [3], [90], 1, 0),                    # one head's group is wider than any tile
+    (128, 1, 300, 64, [2], [70], 1, 0),
+    # more than 128 columns per sequence
+    (64, 4, 4, 448, [41, 90, 0, 33], [100, 90, 50, 470], 1, 0),
+    (64, 2, 3, 64, [130, 9, 44], [77, 5, 300], 1, 0),      # rows whose token would be negative see nothing
+    (96, 2, 3, 96, [40, 150], [40, 400], 1, 0),
+    (96, 3, 2, 32, [140, 77], [333, 77], 1, 64),
+    (128, 2, 4, 64, [64, 33, 64], [300, 64, 129], 1, 50),
+    (128, 1, 2, 32, [257], [257], 1, 0),
+    (128, 1, 5, 64, [70, 70], [70, 200], 0, 0),
+    (64, 1, 140, 64, [2, 1], [31, 900], 0, 0),
+    (256, 1, 4, 64, [65, 30], [600, 33], 1, 0),
+    (256, 2, 2, 32, [90, 80], [123, 80], 1, 40),
+    (64, 30, 1, 64, [1500, 100], [1500, 164], 1, 300),     # enough tiles for 256 columns each
+    (128, 20, 2, 96, [800, 333], [850, 333], 1, 0),
+    (96, 24, 2, 128, [700], [701], 0, 0),
 ]
 
 
@@ -97,6 +112,8 @@ def test_long_sequences_shared_out(orc, fmt, dim):
     _check(orc, c2, 8, 1, 0, what="long, several rows")
     _check(orc, Case(fmt, dim, 1, 64, [40], [6001], seed=9), 2, 1, 0, what="long, many rows")
     _check(orc, Case(fmt, dim, 1, 64, [40], [6001], seed=10), 2, 1, 1000, what="long, many rows, window")
+    _check(orc, Case(fmt, dim, 1, 64, [100], [3001], seed=19), 2, 1, 0, what="long, more rows")
+    _check(orc, Case(fmt, dim, 1, 64, [100, 1, 90], [2001, 40, 90], seed=20), 3, 1, 500, what="long, more rows, window")
 
 
 def test_results_do_not_change(orc):
@@ -118,7 +135,7 @@ def test_results_do_not_change(orc):
         assert np.array_equal(y.cpu().numpy().view(np.uint16).reshape(8, 128), runs[0][b])
 
 
-@pytest.mark.parametrize("counts", [[1, 1, 1], [33, 1, 8]], ids=["token", "rows"])
+@pytest.mark.parametrize("counts", [[1, 1, 1], [33, 1, 8], [200, 32, 60]], ids=["token", "rows", "many"])
 def test_bad_pages_are_absent(orc, counts):
     c = Case(Q4_1, 64, 2, 32, counts, [200, 32, 70], bad=[(0, 0), (0, 3), (1, 0), (2, 2)], seed=4, one_row=max(counts) == 1)
     _check(orc, c, 2, 1, 0)
@@ -126,7 +143,7 @@ def test_bad_pages_are_absent(orc, counts):
     _check(orc, c, 2, 0, 0)
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 140])
 def test_scores_far_apart(orc, rows):
     """Scores of several hundred in both directions, a first token that outweighs all others, a scale below zero, none."""
     for seed, scale in ((1, 0.5), (2, -0.3), (3, 0.0), (4, 0.09)):
@@ -138,7 +155,7 @@ def test_scores_far_apart(orc, rows):
         _check(orc, c, 1, 1, 0, scale=scale, kv=(k, v), q=q)
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 140])
 def test_small_and_large_values(orc, rows):
     """Values near the smallest a scale can hold, at the limit, and both in one head; queries of any magnitude."""
     for seed, (ks, vs, qs, scale) in enumerate([(1e-4, 1e-4, 1e4, 1.0), (1.0, 1e4, 1.0, 0.1), (2e4, 2e4, 1e-6, 1.0), (1.0, 1e-6, 1e20, 1e-20)]):
@@ -149,7 +166,7 @@ def test_small_and_large_values(orc, rows):
         _check(orc, c, 1, 1, 0, scale=scale, kv=(k, v), q=_q(c, 1, std=qs))
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows", [1, 40, 80])
 def test_nan_stays_in_its_row(orc, rows):
     """A query with a NaN or an infinity makes its own row and head NaN at most."""
     c = Case(Q4_0, 64, 2, 64, [rows, rows], [300, 90], seed=6)
