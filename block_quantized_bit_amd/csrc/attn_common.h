@@ -8,7 +8,7 @@
 
 #include <cfloat>
 
-#include "cache_layout.h"
+#include "cache_device.h"
 #include "wq_device.h"
 #include "wq_launch.h"
 
@@ -21,11 +21,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// The call's int32 arrays are only read and indexed uniformly: as constant memory they are scalar loads.
-typedef const int32_t __attribute__((address_space(4))) * const_i32;
-__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ inline int read_const(const int32_t* p, int64_t i) { return ((const_i32)(uintptr_t)p)[i]; }
 
 // Columns per tile: `rows` rows of the sequence times the group's heads, or one row's `ht` runs of heads.
 struct TileShape {
@@ -106,60 +101,6 @@ struct TileCount {
         int r0, r1;
         seq_rows(a.s, b, &r0, &r1);
         return (uint32_t)tiles_of(ts, r1 - r0);
-    }
-};
-
-// Inclusive prefix sum over the wave.
-__device__ inline uint32_t wave_scan(uint32_t v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = __shfl_up(v, d, 64);
-        v += (threadIdx.x & 63) >= (unsigned)d ? o : 0;
-    }
-    return v;
-}
-
-// Running totals over the sequences of a call: weight(b) is sequence b's share (b per lane).  The first 64 sequences'
-// shares stay in registers, so that a call of at most 64 reads their lengths once for all questions.
-template <class F>
-struct SeqTotals {
-    F weight;
-    int batch;
-    uint32_t w, incl;   // of sequence `lane`
-
-    __device__ SeqTotals(int n, F f) : weight(f), batch(n) {
-        const int lane = threadIdx.x & 63;
-        w = lane < n ? weight(lane) : 0;
-        incl = wave_scan(w);
-    }
-    static __device__ uint32_t last(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
-    __device__ uint32_t total() const {
-        uint32_t run = last(incl);
-        for (int b0 = 64; b0 < batch; b0 += 64) {
-            const int b = b0 + (threadIdx.x & 63);
-            run += last(wave_scan(b < batch ? weight(b) : 0));
-        }
-        return run;
-    }
-    // The sequence whose share contains `target` (below the total), and the total before it; -1 if there is none.
-    __device__ int find(uint32_t target, uint32_t* before) const {
-        uint32_t run = 0, v = w, in = incl;
-        for (int b0 = 0; b0 < batch; b0 += 64) {
-            if (b0 > 0) {
-                const int b = b0 + (threadIdx.x & 63);
-                v = b < batch ? weight(b) : 0;
-                in = wave_scan(v);
-            }
-            const uint32_t sum = last(in);
-            if (target - run < sum) {
-                const int l = __builtin_ctzll(__ballot(in > target - run));
-                *before = run + (uint32_t)__builtin_amdgcn_readlane((int)(in - v), l);
-                return b0 + l;
-            }
-            run += sum;
-        }
-        *before = run;
-        return -1;
     }
 };
 

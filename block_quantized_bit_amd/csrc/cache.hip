@@ -5,7 +5,9 @@
 // q = clamp(rint((x - m) / d), 0, 15), x^ = q d + m), after clamping x to +-32768.
 #include <hip/hip_runtime.h>
 
-#include "cache_layout.h"
+#include <algorithm>
+
+#include "cache_device.h"
 #include "wq_device.h"
 #include "wq_launch.h"
 
@@ -47,13 +49,27 @@ __device__ inline void store8(void* p, int64_t i, const float v[8]) {
     }
 }
 
-// Quantizes a block of 32 held by 4 neighbouring lanes (8 values each, in lane order).  word: the 8 codes, nibble n =
+// Lane ^ 1, lane ^ 2.
+template <int X>
+__device__ inline uint32_t quad_xor(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, X == 1 ? 0xB1 : 0x4E, 0xF, 0xF, true);
+}
+template <int X>
+__device__ inline float quad_xor(float v) { return __uint_as_float(quad_xor<X>(__float_as_uint(v))); }
+
+// Quantizes a block of 32 held by 4 neighbouring lanes (8 values each, in lane order).  Returns the 8 codes, nibble n =
 // value n; d, m: fp16 bits (m only for q4_1).
+//
+// The codes are rint of the correctly rounded quotients t = RN(x / d), in 3 instructions a value in place of a division's
+// 10: with r = RN(1/d), q = RN(x r) is t (1 + a), |a| <= 2^-23, and q + r RN(x - d q) is t within 2^-46 of it.  A tie of the
+// rounding to 24 bits is mid d = x with mid of 25 bits and d of 11: unless it is met exactly, x / d is at least 2^-36 away
+// from it, so the corrected quotient rounds to the same side.  (Where the remainder underflows, |t| is far below 1/2.)
+// d = 0: r = 0 gives the code of 0.
 template <bool Q41>
-__device__ inline void quantize_block(float v[8], uint32_t* word, uint16_t* d, uint16_t* m) {
+__device__ inline uint32_t quantize_block(float v[8], uint16_t* d, uint16_t* m) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = fminf(fmaxf(v[j], -kCacheLimit), kCacheLimit);   // a NaN becomes -32768
-    float base, low;
+    for (int j = 0; j < 8; j++) v[j] = __builtin_amdgcn_fmed3f(v[j], -kCacheLimit, kCacheLimit);   // a NaN becomes the lesser, -32768
+    float low;
     if constexpr (Q41) {
         float lo = v[0], hi = v[0];
 #pragma unroll
@@ -61,156 +77,314 @@ __device__ inline void quantize_block(float v[8], uint32_t* word, uint16_t* d, u
             lo = fminf(lo, v[j]);
             hi = fmaxf(hi, v[j]);
         }
-#pragma unroll
-        for (int s = 1; s <= 2; s <<= 1) {
-            lo = fminf(lo, __shfl_xor(lo, s, 64));
-            hi = fmaxf(hi, __shfl_xor(hi, s, 64));
-        }
+        lo = fminf(lo, quad_xor<1>(lo));
+        hi = fmaxf(hi, quad_xor<1>(hi));
+        lo = fminf(lo, quad_xor<2>(lo));
+        hi = fmaxf(hi, quad_xor<2>(hi));
         *d = f16_sat_bits((hi - lo) / 15.0f);
         *m = f16_sat_bits(lo);
-        base = f16_value(*m);
+        const float mu = f16_value(*m);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] -= mu;
         low = 0.0f;
     } else {
         float big = v[0];                                    // the first of the largest magnitude
 #pragma unroll
         for (int j = 1; j < 8; j++) big = fabsf(v[j]) > fabsf(big) ? v[j] : big;
-#pragma unroll
-        for (int s = 1; s <= 2; s <<= 1) {
-            const float o = __shfl_xor(big, s, 64);
-            const bool other_first = (threadIdx.x & s) != 0;   // the other lane's values come before this one's
-            big = fabsf(o) > fabsf(big) || (other_first && fabsf(o) == fabsf(big)) ? o : big;
-        }
+        const float o1 = quad_xor<1>(big);                   // the other lane's values come first where the bit is set
+        big = fabsf(o1) > fabsf(big) || ((threadIdx.x & 1) && fabsf(o1) == fabsf(big)) ? o1 : big;
+        const float o2 = quad_xor<2>(big);
+        big = fabsf(o2) > fabsf(big) || ((threadIdx.x & 2) && fabsf(o2) == fabsf(big)) ? o2 : big;
         *d = f16_sat_bits(big / -8.0f);
         *m = 0;
-        base = 0.0f;
         low = -8.0f;
     }
-    const float delta = f16_value(*d);
-    uint32_t w = 0;
+    const float delta = f16_value(*d), r = delta != 0.0f ? 1.0f / delta : 0.0f;
+    float c[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        float q = -low;
-        if (delta != 0.0f) q = fminf(fmaxf(rintf((v[j] - base) / delta), low), low + 15.0f) - low;
-        w |= (uint32_t)q << (4 * j);
+        float q = v[j] * r;
+        q = fmaf(fmaf(-q, delta, v[j]), r, q);
+        c[j] = rintf(__builtin_amdgcn_fmed3f(q, low, low + 15.0f));   // (the limits are whole: before or after rint is the same)
     }
-    *word = w;
+    // four codes as one whole number
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+        w[k] = (uint32_t)fmaf(4096.0f, c[4 * k + 3], fmaf(256.0f, c[4 * k + 2], fmaf(16.0f, c[4 * k + 1], c[4 * k] - low * 4369.0f)));
+    return w[0] | (w[1] << 16);
+}
+
+// Four nibbles to the low halves of four bytes, and back.
+__device__ inline uint32_t spread4(uint32_t x) {
+    x = (x | (x << 8)) & 0x00FF00FFu;
+    return (x | (x << 4)) & 0x0F0F0F0Fu;
+}
+__device__ inline uint32_t gather4(uint32_t x) {   // (bytes are below 16)
+    x = (x | (x >> 4)) & 0x00FF00FFu;
+    return (x | (x >> 8)) & 0x0000FFFFu;
+}
+// Rows and columns of a 4 x 4 byte square exchanged.
+__device__ inline void transpose4(uint32_t (&w)[4]) {
+    const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+    const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+    w[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+    w[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+    w[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+    w[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// A thread takes 8 channels of four neighbouring tokens of one head, whose place in a unit is whole words (K), words of
+// one byte per token (V) and 8 bytes of scales: tokens 4 k .. 4 k + 3 of a sequence, as many of them as are the call's.
+struct GroupCount {
+    const Seqs& s;
+    __device__ uint32_t operator()(int b) const {
+        int r0, r1;
+        seq_rows(s, b, &r0, &r1);
+        if (r0 == r1) return 0;
+        const int64_t p0 = (int64_t)s.len[b] - (r1 - r0);
+        return (uint32_t)(((p0 + (r1 - r0) - 1) >> 2) - (p0 >> 2) + 1);
+    }
+};
+struct Group {
+    int seq, h, b, g;     // sequence, head, 32-channel block, 8 channels of it
+    int64_t row;          // of token 0 of the group (the call's rows are row + i, i in [first, end))
+    int first, end;
+    int64_t token;        // of i = 0; may be below 0
+};
+// per_row: threads per group; false: no work for this thread.
+__device__ inline bool thread_group(const Seqs& s, int nb, int per_row, int groups_per_block, Group* q) {
+    const int in_block = groups_per_block > 1 ? threadIdx.x / (unsigned)per_row : 0;
+    const int in = threadIdx.x - in_block * per_row + blockIdx.y * blockDim.x;
+    const uint32_t first = blockIdx.x * groups_per_block;
+    uint32_t before;
+    int seq, r0, r1;
+    if (s.row_start) {
+        const GroupCount count{s};
+        seq = SeqTotals(s.batch, count).find(first, &before);
+        if (seq < 0) return false;
+        if (in >= per_row || in_block >= groups_per_block) return false;
+        uint32_t n = count(seq);
+        while (first + in_block - before >= n) {
+            before += n;
+            if (++seq >= s.batch) return false;
+            n = count(seq);
+        }
+    } else {
+        if (in >= per_row || in_block >= groups_per_block) return false;
+        seq = before = first + in_block;
+        if (seq >= s.batch) return false;
+    }
+    seq_rows(s, seq, &r0, &r1);
+    const int64_t p0 = (int64_t)s.len[seq] - (r1 - r0), t = ((p0 >> 2) + (first + in_block - before)) * 4;
+    q->seq = seq;
+    q->token = t;
+    q->row = r0 + (t - p0);
+    q->first = t < p0 ? (int)(p0 - t) : 0;
+    q->end = t + 4 - p0 > r1 - r0 ? (int)(p0 + (r1 - r0) - t) : 4;
+    const int c8 = nb * 4, h = in / (unsigned)c8, cg = in - h * c8;
+    q->h = h;
+    q->b = cg >> 2;
+    q->g = cg & 3;
+    return true;
 }
 
 }  // namespace
 
-// One thread per 8 channels of one row of one head (4 threads: a block).
-template <bool Q41, bool F32>
-__global__ __launch_bounds__(256) void k_cache_write(Seqs s, int nb, const void* __restrict__ k, int64_t ldk,
+// Bound by instructions, then by memory: 36176 rows of 8 heads of 128 (bf16, q4_1) TODO us.
+template <bool Q41, bool F32, int NB>
+__global__ __launch_bounds__(256) void k_cache_write(Seqs s, int per_row, int groups_per_block, const void* __restrict__ k, int64_t ldk,
                                                      const void* __restrict__ v, int64_t ldv, uint8_t* __restrict__ cache) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int c8 = nb * 4, per_row = s.heads * c8;
-    const int64_t row = c / per_row;
-    if (row >= s.rows) return;
-    const int in_row = (int)(c - row * per_row), h = in_row / c8, cg = in_row - h * c8, b = cg >> 2, g = cg & 3;
-    const int seq = seq_of_row(s, (int)row);
-    if (seq < 0) return;
-    int r0, r1;
-    seq_rows(s, seq, &r0, &r1);
-    const int64_t t = (int64_t)s.len[seq] - r1 + row;   // its position
-    if (t < 0 || t >= (int64_t)s.table_ld * s.page) return;
-    const int64_t at = seq_unit(s, seq, h, (int)t);
+    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim);
+    Group q;
+    if (!thread_group(s, NB, per_row, groups_per_block, &q)) return;
+    const int64_t cap = (int64_t)s.table_ld * s.page;
+    const int first = max(q.first, q.token < 0 ? (int)min((int64_t)4, -q.token) : 0);
+    if (first >= q.end || q.token >= cap) return;           // (cap is a multiple of 4)
+    const int64_t at = seq_unit(s, q.seq, q.h, (int)(q.token < 0 ? 0 : q.token));
+    const int col = q.h * dim + q.b * 32 + q.g * 8;
+    float x[4][8], y[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        // (a row that is not the call's is read as its neighbour that is)
+        const int64_t row = q.row + max(first, min(i, q.end - 1));
+        load8<F32>(k, row * ldk + col, x[i]);
+        load8<F32>(v, row * ldv + col, y[i]);
+    }
+    uint32_t kw[4], vw[4];
+    uint16_t kd[4], km[4], vd[4], vm[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) kw[i] = quantize_block<Q41>(x[i], &kd[i], &km[i]);
+#pragma unroll
+    for (int i = 0; i < 4; i++) vw[i] = quantize_block<Q41>(y[i], &vd[i], &vm[i]);
     if (at < 0) return;
-    const int u = (int)(t % s.page) % kUnit, dim = nb * 32;
+    const int u = (int)(q.token % s.page) % kUnit;          // of token 0: a multiple of 4 (below 0 only before the first)
+    const int u0 = q.token < 0 ? 0 : u;
     uint8_t* const kb = cache + at;
-    uint8_t* const vb = kb + cache_half_bytes(Q41, dim);
-    float x[8];
-    uint32_t word;
-    uint16_t d, m;
-    load8<F32>(k, row * ldk + h * dim + cg * 8, x);
-    quantize_block<Q41>(x, &word, &d, &m);
-    *reinterpret_cast<uint32_t*>(kb + cache_k_word(nb, u, b, g)) = word;
-    uint16_t* sc = reinterpret_cast<uint16_t*>(kb + 16 * dim) + cache_scale(nb, u, b);
-    if (g == 0) {
-        sc[0] = d;
-        if constexpr (Q41) sc[dim] = m;
-    }
-    load8<F32>(v, row * ldv + h * dim + cg * 8, x);
-    quantize_block<Q41>(x, &word, &d, &m);
-    // channels 8 g + n: the low nibble of channel's byte for g < 2, the high one of channel - 16's for g >= 2
-    const uint32_t other = __shfl_xor(word, 2, 64);
-    const uint32_t lo = g < 2 ? word : other, hi = g < 2 ? other : word;
-    // this lane writes the bytes of channels 8 (g & 1) + 4 (g >> 1) + 0..3
+    uint8_t* const vb = kb + half;
+    // V: channels 8 g + n of this lane's codes are the low nibbles of the bytes for g < 2, and the high ones of the lane
+    // g ^ 2's channels: this lane writes the bytes of channels 8 (g & 1) + 4 (g >> 1) + 0..3
+    uint32_t vt[4];
 #pragma unroll
-    for (int n = 0; n < 4; n++) {
-        const int e = 4 * (g >> 1) + n;
-        vb[cache_v_byte(nb, u, b, 8 * (g & 1) + e)] = (uint8_t)(((lo >> (4 * e)) & 15u) | (((hi >> (4 * e)) & 15u) << 4));
+    for (int i = 0; i < 4; i++) {
+        const uint32_t other = quad_xor<2>(vw[i]);
+        const uint32_t lo = q.g < 2 ? vw[i] & 0xFFFFu : other >> 16, hi = q.g < 2 ? other & 0xFFFFu : vw[i] >> 16;
+        vt[i] = spread4(lo) | (spread4(hi) << 4);
     }
-    sc = reinterpret_cast<uint16_t*>(vb + 16 * dim) + cache_scale(nb, u, b);
-    if (g == 0) {
-        sc[0] = d;
-        if constexpr (Q41) sc[dim] = m;
-    }
-}
-
-// One thread per 8 channels of one row of one head.
-template <bool Q41, bool F32>
-__global__ __launch_bounds__(256) void k_cache_read(Seqs s, int nb, const uint8_t* __restrict__ cache, void* __restrict__ k,
-                                                    int64_t ldk, void* __restrict__ v, int64_t ldv) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int c8 = nb * 4, per_row = s.heads * c8;
-    const int64_t row = c / per_row;
-    if (row >= s.rows) return;
-    const int in_row = (int)(c - row * per_row), h = in_row / c8, cg = in_row - h * c8, b = cg >> 2, g = cg & 3;
-    const int seq = seq_of_row(s, (int)row);
-    if (seq < 0) return;
-    int r0, r1;
-    seq_rows(s, seq, &r0, &r1);
-    const int64_t t = (int64_t)s.len[seq] - r1 + row;
-    const int dim = nb * 32;
-    const int64_t at = t < 0 || t >= (int64_t)s.table_ld * s.page ? -1 : seq_unit(s, seq, h, (int)t);
-    float x[8], y[8];
-    if (at < 0) {
+    const int c0 = 8 * (q.g & 1) + 4 * (q.g >> 1);
+    uint16_t* const ks = reinterpret_cast<uint16_t*>(kb + 16 * dim) + cache_scale(NB, u0, q.b);
+    uint16_t* const vs = reinterpret_cast<uint16_t*>(vb + 16 * dim) + cache_scale(NB, u0, q.b);
+    if (first == 0 && q.end == 4) {
+        transpose4(vt);
 #pragma unroll
-        for (int n = 0; n < 8; n++) x[n] = y[n] = 0.0f;
-    } else {
-        const int u = (int)(t % s.page) % kUnit;
-        const uint8_t* const kb = cache + at;
-        const uint8_t* const vb = kb + cache_half_bytes(Q41, dim);
-        const uint16_t* ks = reinterpret_cast<const uint16_t*>(kb + 16 * dim) + cache_scale(nb, u, b);
-        const uint16_t* vs = reinterpret_cast<const uint16_t*>(vb + 16 * dim) + cache_scale(nb, u, b);
-        const float kd = f16_value(ks[0]), vd = f16_value(vs[0]);
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(kb + cache_k_word(nb, u, b, g));
-#pragma unroll
-        for (int n = 0; n < 8; n++) {
-            const uint32_t kq = (word >> (4 * n)) & 15u;
-            const uint32_t vq = (vb[cache_v_byte(nb, u, b, 8 * (g & 1) + n)] >> (g < 2 ? 0 : 4)) & 15u;
+        for (int i = 0; i < 4; i++) {
+            *reinterpret_cast<uint32_t*>(kb + cache_k_word(NB, u0 + i, q.b, q.g)) = kw[i];
+            *reinterpret_cast<uint32_t*>(vb + cache_v_byte(NB, u0, q.b, c0 + i)) = vt[i];
+        }
+        if (q.g == 0) {
+            typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<u16x4*>(ks) = (u16x4){kd[0], kd[1], kd[2], kd[3]};
+            *reinterpret_cast<u16x4*>(vs) = (u16x4){vd[0], vd[1], vd[2], vd[3]};
             if constexpr (Q41) {
-                x[n] = (float)kq * kd + f16_value(ks[dim]);
-                y[n] = (float)vq * vd + f16_value(vs[dim]);
-            } else {
-                x[n] = ((float)kq - 8.0f) * kd;
-                y[n] = ((float)vq - 8.0f) * vd;
+                *reinterpret_cast<u16x4*>(ks + dim) = (u16x4){km[0], km[1], km[2], km[3]};
+                *reinterpret_cast<u16x4*>(vs + dim) = (u16x4){vm[0], vm[1], vm[2], vm[3]};
+            }
+        }
+        return;
+    }
+    // some of the four are not the call's: only the others' bytes
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (i < first || i >= q.end) continue;
+        *reinterpret_cast<uint32_t*>(kb + cache_k_word(NB, u0 + i, q.b, q.g)) = kw[i];
+#pragma unroll
+        for (int n = 0; n < 4; n++) vb[cache_v_byte(NB, u0 + i, q.b, c0 + n)] = (uint8_t)(vt[i] >> (8 * n));
+        if (q.g == 0) {
+            ks[i] = kd[i];
+            vs[i] = vd[i];
+            if constexpr (Q41) {
+                ks[dim + i] = km[i];
+                vs[dim + i] = vm[i];
             }
         }
     }
-    store8<F32>(k, row * ldk + h * dim + cg * 8, x);
-    store8<F32>(v, row * ldv + h * dim + cg * 8, y);
+}
+
+// Bound by memory: 36176 rows of 8 heads of 128 (q4_1 to bf16) TODO us.
+template <bool Q41, bool F32, int NB>
+__global__ __launch_bounds__(256) void k_cache_read(Seqs s, int per_row, int groups_per_block, const uint8_t* __restrict__ cache,
+                                                    void* __restrict__ k, int64_t ldk, void* __restrict__ v, int64_t ldv) {
+    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim);
+    typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+    Group q;
+    if (!thread_group(s, NB, per_row, groups_per_block, &q)) return;
+    const int64_t cap = (int64_t)s.table_ld * s.page;
+    const int64_t at = q.token <= -4 || q.token >= cap ? -1 : seq_unit(s, q.seq, q.h, (int)(q.token < 0 ? 0 : q.token));
+    const int c0 = 8 * (q.g & 1) + 4 * (q.g >> 1);
+    uint32_t kw[4] = {}, vt[4] = {};
+    u16x4 kd = {}, km = {}, vd = {}, vm = {};
+    if (at >= 0) {
+        const int u0 = q.token < 0 ? 0 : (int)(q.token % s.page) % kUnit;
+        const uint8_t* const kb = cache + at;
+        const uint8_t* const vb = kb + half;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            kw[i] = *reinterpret_cast<const uint32_t*>(kb + cache_k_word(NB, u0 + i, q.b, q.g));
+            vt[i] = *reinterpret_cast<const uint32_t*>(vb + cache_v_byte(NB, u0, q.b, c0 + i));
+        }
+        const uint16_t* const ks = reinterpret_cast<const uint16_t*>(kb + 16 * dim) + cache_scale(NB, u0, q.b);
+        const uint16_t* const vs = reinterpret_cast<const uint16_t*>(vb + 16 * dim) + cache_scale(NB, u0, q.b);
+        kd = *reinterpret_cast<const u16x4*>(ks);
+        vd = *reinterpret_cast<const u16x4*>(vs);
+        if constexpr (Q41) {
+            km = *reinterpret_cast<const u16x4*>(ks + dim);
+            vm = *reinterpret_cast<const u16x4*>(vs + dim);
+        }
+    }
+    transpose4(vt);   // now row i's bytes of channels c0 .. c0 + 3
+    const int col = q.h * dim + q.b * 32 + q.g * 8;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        // to this lane's 8 channels: four nibbles of its own bytes and four of lane g ^ 2's
+        const uint32_t lo = gather4(vt[i] & 0x0F0F0F0Fu), hi = gather4((vt[i] >> 4) & 0x0F0F0F0Fu);
+        const uint32_t own = q.g < 2 ? lo : hi, give = q.g < 2 ? hi : lo, got = quad_xor<2>(give);
+        const uint32_t vw = q.g < 2 ? own | (got << 16) : got | (own << 16);
+        if (i < q.first || i >= q.end) continue;
+        const bool none = at < 0 || q.token + i < 0;
+        float x[8], y[8];
+#pragma unroll
+        for (int n = 0; n < 8; n++) {
+            const float kq = (float)((kw[i] >> (4 * n)) & 15u), vq = (float)((vw >> (4 * n)) & 15u);
+            if constexpr (Q41) {
+                x[n] = kq * f16_value(kd[i]) + f16_value(km[i]);
+                y[n] = vq * f16_value(vd[i]) + f16_value(vm[i]);
+            } else {
+                x[n] = (kq - 8.0f) * f16_value(kd[i]);
+                y[n] = (vq - 8.0f) * f16_value(vd[i]);
+            }
+            if (none) x[n] = y[n] = 0.0f;
+        }
+        store8<F32>(k, (q.row + i) * ldk + col, x);
+        store8<F32>(v, (q.row + i) * ldv + col, y);
+    }
 }
 
 namespace {
-unsigned chunk_blocks(const Seqs& s, int nb) { return (unsigned)(((int64_t)s.rows * s.heads * nb * 4 + 255) / 256); }
+
+// Threads per group, groups per workgroup, the launch.
+struct Launch {
+    int per_row, groups;
+    dim3 grid, block;
+};
+Launch group_launch(const Seqs& s, int nb) {
+    Launch l;
+    l.per_row = s.heads * nb * 4;
+    l.groups = std::max(1, 256 / l.per_row);
+    const int threads = std::min(256, (l.per_row * l.groups + 63) / 64 * 64);
+    // groups of four tokens: n rows touch at most n / 4 + 2
+    const int64_t n = s.row_start ? (int64_t)s.rows / 4 + 2 * (int64_t)std::min(s.rows, s.batch) : s.batch;
+    l.grid = dim3((unsigned)((n + l.groups - 1) / l.groups), (unsigned)((l.per_row + threads - 1) / threads));
+    if (l.per_row <= threads) l.grid.y = 1;
+    l.block = dim3((unsigned)threads);
+    return l;
+}
+
+template <int NB>
+void write_nb(const Seqs& q, bool q41, bool f32, const void* k, int64_t ldk, const void* v, int64_t ldv, uint8_t* cache, hipStream_t s) {
+    const Launch l = group_launch(q, NB);
+    auto f = q41 ? (f32 ? k_cache_write<true, true, NB> : k_cache_write<true, false, NB>)
+                 : (f32 ? k_cache_write<false, true, NB> : k_cache_write<false, false, NB>);
+    hipLaunchKernelGGL(f, l.grid, l.block, 0, s, q, l.per_row, l.groups, k, ldk, v, ldv, cache);
+}
+template <int NB>
+void read_nb(const Seqs& q, bool q41, bool f32, const uint8_t* cache, void* k, int64_t ldk, void* v, int64_t ldv, hipStream_t s) {
+    const Launch l = group_launch(q, NB);
+    auto f = q41 ? (f32 ? k_cache_read<true, true, NB> : k_cache_read<true, false, NB>)
+                 : (f32 ? k_cache_read<false, true, NB> : k_cache_read<false, false, NB>);
+    hipLaunchKernelGGL(f, l.grid, l.block, 0, s, q, l.per_row, l.groups, cache, k, ldk, v, ldv);
+}
+
 }  // namespace
 
 hipError_t launch_cache_write(const Seqs& q, bool q41, int dim, bool f32, const void* k, int64_t ldk, const void* v, int64_t ldv,
                               uint8_t* cache, hipStream_t s) {
-    const int nb = dim / 32;
-    auto f = q41 ? (f32 ? k_cache_write<true, true> : k_cache_write<true, false>)
-                 : (f32 ? k_cache_write<false, true> : k_cache_write<false, false>);
-    hipLaunchKernelGGL(f, dim3(chunk_blocks(q, nb)), dim3(256), 0, s, q, nb, k, ldk, v, ldv, cache);
+    switch (dim) {
+    case 64: write_nb<2>(q, q41, f32, k, ldk, v, ldv, cache, s); break;
+    case 96: write_nb<3>(q, q41, f32, k, ldk, v, ldv, cache, s); break;
+    case 128: write_nb<4>(q, q41, f32, k, ldk, v, ldv, cache, s); break;
+    default: write_nb<8>(q, q41, f32, k, ldk, v, ldv, cache, s); break;
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_cache_read(const Seqs& q, bool q41, int dim, bool f32, const uint8_t* cache, void* k, int64_t ldk, void* v,
                              int64_t ldv, hipStream_t s) {
-    const int nb = dim / 32;
-    auto f = q41 ? (f32 ? k_cache_read<true, true> : k_cache_read<true, false>)
-                 : (f32 ? k_cache_read<false, true> : k_cache_read<false, false>);
-    hipLaunchKernelGGL(f, dim3(chunk_blocks(q, nb)), dim3(256), 0, s, q, nb, cache, k, ldk, v, ldv);
+    switch (dim) {
+    case 64: read_nb<2>(q, q41, f32, cache, k, ldk, v, ldv, s); break;
+    case 96: read_nb<3>(q, q41, f32, cache, k, ldk, v, ldv, s); break;
+    case 128: read_nb<4>(q, q41, f32, cache, k, ldk, v, ldv, s); break;
+    default: read_nb<8>(q, q41, f32, cache, k, ldk, v, ldv, s); break;
+    }
     return hipGetLastError();
 }
 

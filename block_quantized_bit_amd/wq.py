@@ -96,7 +96,42 @@ def seqs(batch: int, rows: int, len, table=None, row_start=None, table_ld: int |
         table_ld = table.shape[1]
     s = wq_seqs(int(batch), int(rows), _ptr(row_start), _ptr(len), _ptr(table), int(table_ld or 0), 0)
     s.tensors = (row_start, len, table)
+    s.device = _device("seqs", *s.tensors)
     return s
+
+
+def _device(where: str, *args):
+    """The device index that the tensors among the arguments share (None if there are none)."""
+    dev = None
+    for t in args:
+        if t is None or isinstance(t, int):
+            continue
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{where}: tensors on devices {dev} and {d}")
+    return dev
+
+
+def _call_on(where: str, s: wq_seqs, tensors, stream, check: bool, fn, *args) -> int:
+    """fn(*args, stream) with the tensors' device current: a launch goes to the current device, and the default stream
+    is that device's."""
+    dev = _device(where, *tensors)
+    own = getattr(s, "device", None)
+    if own is not None:
+        if dev is not None and dev != own:
+            raise ValueError(f"{where}: tensors on device {dev}, sequences on {own}")
+        dev = own
+    if dev is not None:
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        if dev != _torch.cuda.current_device():
+            with _torch.cuda.device(dev):
+                return _check(fn(*args, _stream(stream)), where, check)
+    return _check(fn(*args, _stream(stream)), where, check)
 
 
 _lib = None
@@ -163,10 +198,16 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_torch = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())   # of torch.cuda.current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -265,15 +306,13 @@ def wq_cache_size(d: wq_cache_desc) -> int:
 
 
 def wq_cache_write(d: wq_cache_desc, s: wq_seqs, k, ldk: int, v, ldv: int, xdt: int, cache, stream=None, check=True) -> int:
-    st = lib().wq_cache_write(ctypes.byref(d), ctypes.byref(s), _ptr(k), int(ldk), _ptr(v), int(ldv), int(xdt), _ptr(cache),
-                              _stream(stream))
-    return _check(st, "wq_cache_write", check)
+    return _call_on("wq_cache_write", s, (k, v, cache), stream, check, lib().wq_cache_write, ctypes.byref(d), ctypes.byref(s),
+                    _ptr(k), ldk, _ptr(v), ldv, xdt, _ptr(cache))
 
 
 def wq_cache_read(d: wq_cache_desc, s: wq_seqs, cache, k, ldk: int, v, ldv: int, ydt: int, stream=None, check=True) -> int:
-    st = lib().wq_cache_read(ctypes.byref(d), ctypes.byref(s), _ptr(cache), _ptr(k), int(ldk), _ptr(v), int(ldv), int(ydt),
-                             _stream(stream))
-    return _check(st, "wq_cache_read", check)
+    return _call_on("wq_cache_read", s, (cache, k, v), stream, check, lib().wq_cache_read, ctypes.byref(d), ctypes.byref(s),
+                    _ptr(cache), _ptr(k), ldk, _ptr(v), ldv, ydt)
 
 
 def wq_attn_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int) -> int:
@@ -285,6 +324,5 @@ def wq_attn_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int) -> int:
 
 def wq_attn(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scale: float, causal, window: int, y, ldy: int,
             ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
-    st = lib().wq_attn(ctypes.byref(d), ctypes.byref(s), int(q_heads), _ptr(q), int(ldq), _ptr(cache), float(scale),
-                       int(causal), int(window), _ptr(y), int(ldy), _ptr(ws), int(ws_bytes), _stream(stream))
-    return _check(st, "wq_attn", check)
+    return _call_on("wq_attn", s, (q, cache, y, ws), stream, check, lib().wq_attn, ctypes.byref(d), ctypes.byref(s), q_heads,
+                    _ptr(q), ldq, _ptr(cache), scale, int(causal), window, _ptr(y), ldy, _ptr(ws), ws_bytes)
