@@ -16,6 +16,7 @@ namespace wq {
 namespace {
 
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 template <bool F32>
@@ -202,71 +203,66 @@ __global__ __launch_bounds__(256) void k_cache_write(Seqs s, int per_row, int gr
     const int first = max(q.first, q.token < 0 ? (int)min((int64_t)4, -q.token) : 0);
     if (first >= q.end || q.token >= cap) return;           // (cap is a multiple of 4)
     const int64_t at = seq_unit(s, q.seq, q.h, (int)(q.token < 0 ? 0 : q.token));
-    const int col = q.h * dim + q.b * 32 + q.g * 8;
-    float x[4][8], y[4][8];
+    const bool is_v = blockIdx.z;
+    const void* const src = is_v ? v : k;
+    const int64_t ld = is_v ? ldv : ldk;
+    float x[4][8];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         // (a row that is not the call's is read as its neighbour that is)
         const int64_t row = q.row + max(first, min(i, q.end - 1));
-        load8<F32>(k, row * ldk + col, x[i]);
-        load8<F32>(v, row * ldv + col, y[i]);
+        load8<F32>(src, row * ld + q.h * dim + q.b * 32 + q.g * 8, x[i]);
     }
-    uint32_t kw[4], vw[4];
-    uint16_t kd[4], km[4], vd[4], vm[4];
+    uint32_t w[4];
+    uint16_t d[4], m[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) kw[i] = quantize_block<Q41>(x[i], &kd[i], &km[i]);
-#pragma unroll
-    for (int i = 0; i < 4; i++) vw[i] = quantize_block<Q41>(y[i], &vd[i], &vm[i]);
+    for (int i = 0; i < 4; i++) w[i] = quantize_block<Q41>(x[i], &d[i], &m[i]);
     if (at < 0) return;
-    const int u = (int)(q.token % s.page) % kUnit;          // of token 0: a multiple of 4 (below 0 only before the first)
-    const int u0 = q.token < 0 ? 0 : u;
-    uint8_t* const kb = cache + at;
-    uint8_t* const vb = kb + half;
-    // V: channels 8 g + n of this lane's codes are the low nibbles of the bytes for g < 2, and the high ones of the lane
-    // g ^ 2's channels: this lane writes the bytes of channels 8 (g & 1) + 4 (g >> 1) + 0..3
-    uint32_t vt[4];
+    // token 0's place in its unit (a multiple of 4; a group that begins before the sequence ends before token 1)
+    const int u0 = q.token < 0 ? 0 : (int)(q.token % s.page) % kUnit;
+    uint8_t* const to = cache + at + (is_v ? half : 0);
+    uint16_t* const sc = reinterpret_cast<uint16_t*>(to + 16 * dim) + cache_scale(NB, u0, q.b);
+    const bool whole = first == 0 && q.end == 4;
+    if (q.g == 0) {
+        if (whole) {
+            *reinterpret_cast<u16x4*>(sc) = (u16x4){d[0], d[1], d[2], d[3]};
+            if constexpr (Q41) *reinterpret_cast<u16x4*>(sc + dim) = (u16x4){m[0], m[1], m[2], m[3]};
+        } else {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const uint32_t other = quad_xor<2>(vw[i]);
-        const uint32_t lo = q.g < 2 ? vw[i] & 0xFFFFu : other >> 16, hi = q.g < 2 ? other & 0xFFFFu : vw[i] >> 16;
-        vt[i] = spread4(lo) | (spread4(hi) << 4);
-    }
-    const int c0 = 8 * (q.g & 1) + 4 * (q.g >> 1);
-    uint16_t* const ks = reinterpret_cast<uint16_t*>(kb + 16 * dim) + cache_scale(NB, u0, q.b);
-    uint16_t* const vs = reinterpret_cast<uint16_t*>(vb + 16 * dim) + cache_scale(NB, u0, q.b);
-    if (first == 0 && q.end == 4) {
-        transpose4(vt);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            *reinterpret_cast<uint32_t*>(kb + cache_k_word(NB, u0 + i, q.b, q.g)) = kw[i];
-            *reinterpret_cast<uint32_t*>(vb + cache_v_byte(NB, u0, q.b, c0 + i)) = vt[i];
-        }
-        if (q.g == 0) {
-            typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<u16x4*>(ks) = (u16x4){kd[0], kd[1], kd[2], kd[3]};
-            *reinterpret_cast<u16x4*>(vs) = (u16x4){vd[0], vd[1], vd[2], vd[3]};
-            if constexpr (Q41) {
-                *reinterpret_cast<u16x4*>(ks + dim) = (u16x4){km[0], km[1], km[2], km[3]};
-                *reinterpret_cast<u16x4*>(vs + dim) = (u16x4){vm[0], vm[1], vm[2], vm[3]};
+            for (int i = 0; i < 4; i++) {
+                if (i < first || i >= q.end) continue;
+                sc[i] = d[i];
+                if constexpr (Q41) sc[dim + i] = m[i];
             }
         }
+    }
+    if (!is_v) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (i >= first && i < q.end) *reinterpret_cast<uint32_t*>(to + cache_k_word(NB, u0 + i, q.b, q.g)) = w[i];
+        return;
+    }
+    // V: channels 8 g + n of this lane's codes are the low nibbles of the bytes for g < 2, and the high ones of the lane
+    // g ^ 2's channels: this lane writes the bytes of channels 8 (g & 1) + 4 (g >> 1) + 0..3
+    const int c0 = 8 * (q.g & 1) + 4 * (q.g >> 1);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t other = quad_xor<2>(w[i]);
+        const uint32_t lo = q.g < 2 ? w[i] & 0xFFFFu : other >> 16, hi = q.g < 2 ? other & 0xFFFFu : w[i] >> 16;
+        w[i] = spread4(lo) | (spread4(hi) << 4);
+    }
+    if (whole) {
+        transpose4(w);
+#pragma unroll
+        for (int i = 0; i < 4; i++) *reinterpret_cast<uint32_t*>(to + cache_v_byte(NB, u0, q.b, c0 + i)) = w[i];
         return;
     }
     // some of the four are not the call's: only the others' bytes
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         if (i < first || i >= q.end) continue;
-        *reinterpret_cast<uint32_t*>(kb + cache_k_word(NB, u0 + i, q.b, q.g)) = kw[i];
 #pragma unroll
-        for (int n = 0; n < 4; n++) vb[cache_v_byte(NB, u0 + i, q.b, c0 + n)] = (uint8_t)(vt[i] >> (8 * n));
-        if (q.g == 0) {
-            ks[i] = kd[i];
-            vs[i] = vd[i];
-            if constexpr (Q41) {
-                ks[dim + i] = km[i];
-                vs[dim + i] = vm[i];
-            }
-        }
+        for (int n = 0; n < 4; n++) to[cache_v_byte(NB, u0 + i, q.b, c0 + n)] = (uint8_t)(w[i] >> (8 * n));
     }
 }
 
@@ -275,57 +271,49 @@ template <bool Q41, bool F32, int NB>
 __global__ __launch_bounds__(256) void k_cache_read(Seqs s, int per_row, int groups_per_block, const uint8_t* __restrict__ cache,
                                                     void* __restrict__ k, int64_t ldk, void* __restrict__ v, int64_t ldv) {
     constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim);
-    typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
     Group q;
     if (!thread_group(s, NB, per_row, groups_per_block, &q)) return;
     const int64_t cap = (int64_t)s.table_ld * s.page;
     const int64_t at = q.token <= -4 || q.token >= cap ? -1 : seq_unit(s, q.seq, q.h, (int)(q.token < 0 ? 0 : q.token));
+    const bool is_v = blockIdx.z;
     const int c0 = 8 * (q.g & 1) + 4 * (q.g >> 1);
-    uint32_t kw[4] = {}, vt[4] = {};
-    u16x4 kd = {}, km = {}, vd = {}, vm = {};
+    uint32_t w[4] = {};
+    u16x4 d = {}, m = {};
     if (at >= 0) {
         const int u0 = q.token < 0 ? 0 : (int)(q.token % s.page) % kUnit;
-        const uint8_t* const kb = cache + at;
-        const uint8_t* const vb = kb + half;
+        const uint8_t* const from = cache + at + (is_v ? half : 0);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            w[i] = *reinterpret_cast<const uint32_t*>(from + (is_v ? cache_v_byte(NB, u0, q.b, c0 + i) : cache_k_word(NB, u0 + i, q.b, q.g)));
+        const uint16_t* const sc = reinterpret_cast<const uint16_t*>(from + 16 * dim) + cache_scale(NB, u0, q.b);
+        d = *reinterpret_cast<const u16x4*>(sc);
+        if constexpr (Q41) m = *reinterpret_cast<const u16x4*>(sc + dim);
+    }
+    if (is_v) {
+        transpose4(w);   // now row i's bytes of channels c0 .. c0 + 3
+        // to this lane's 8 channels: four nibbles of its own bytes and four of lane g ^ 2's
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            kw[i] = *reinterpret_cast<const uint32_t*>(kb + cache_k_word(NB, u0 + i, q.b, q.g));
-            vt[i] = *reinterpret_cast<const uint32_t*>(vb + cache_v_byte(NB, u0, q.b, c0 + i));
-        }
-        const uint16_t* const ks = reinterpret_cast<const uint16_t*>(kb + 16 * dim) + cache_scale(NB, u0, q.b);
-        const uint16_t* const vs = reinterpret_cast<const uint16_t*>(vb + 16 * dim) + cache_scale(NB, u0, q.b);
-        kd = *reinterpret_cast<const u16x4*>(ks);
-        vd = *reinterpret_cast<const u16x4*>(vs);
-        if constexpr (Q41) {
-            km = *reinterpret_cast<const u16x4*>(ks + dim);
-            vm = *reinterpret_cast<const u16x4*>(vs + dim);
+            const uint32_t lo = gather4(w[i] & 0x0F0F0F0Fu), hi = gather4((w[i] >> 4) & 0x0F0F0F0Fu);
+            const uint32_t own = q.g < 2 ? lo : hi, got = quad_xor<2>(q.g < 2 ? hi : lo);
+            w[i] = q.g < 2 ? own | (got << 16) : got | (own << 16);
         }
     }
-    transpose4(vt);   // now row i's bytes of channels c0 .. c0 + 3
-    const int col = q.h * dim + q.b * 32 + q.g * 8;
+    void* const dst = is_v ? v : k;
+    const int64_t ld = is_v ? ldv : ldk;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        // to this lane's 8 channels: four nibbles of its own bytes and four of lane g ^ 2's
-        const uint32_t lo = gather4(vt[i] & 0x0F0F0F0Fu), hi = gather4((vt[i] >> 4) & 0x0F0F0F0Fu);
-        const uint32_t own = q.g < 2 ? lo : hi, give = q.g < 2 ? hi : lo, got = quad_xor<2>(give);
-        const uint32_t vw = q.g < 2 ? own | (got << 16) : got | (own << 16);
         if (i < q.first || i >= q.end) continue;
         const bool none = at < 0 || q.token + i < 0;
-        float x[8], y[8];
+        float x[8];
 #pragma unroll
         for (int n = 0; n < 8; n++) {
-            const float kq = (float)((kw[i] >> (4 * n)) & 15u), vq = (float)((vw >> (4 * n)) & 15u);
-            if constexpr (Q41) {
-                x[n] = kq * f16_value(kd[i]) + f16_value(km[i]);
-                y[n] = vq * f16_value(vd[i]) + f16_value(vm[i]);
-            } else {
-                x[n] = (kq - 8.0f) * f16_value(kd[i]);
-                y[n] = (vq - 8.0f) * f16_value(vd[i]);
-            }
-            if (none) x[n] = y[n] = 0.0f;
+            const float c = (float)((w[i] >> (4 * n)) & 15u);
+            if constexpr (Q41) x[n] = c * f16_value(d[i]) + f16_value(m[i]);
+            else x[n] = (c - 8.0f) * f16_value(d[i]);
+            if (none) x[n] = 0.0f;
         }
-        store8<F32>(k, (q.row + i) * ldk + col, x);
-        store8<F32>(v, (q.row + i) * ldv + col, y);
+        store8<F32>(dst, (q.row + i) * ld + q.h * dim + q.b * 32 + q.g * 8, x);
     }
 }
 
@@ -343,8 +331,7 @@ Launch group_launch(const Seqs& s, int nb) {
     const int threads = std::min(256, (l.per_row * l.groups + 63) / 64 * 64);
     // groups of four tokens: n rows touch at most n / 4 + 2
     const int64_t n = s.row_start ? (int64_t)s.rows / 4 + 2 * (int64_t)std::min(s.rows, s.batch) : s.batch;
-    l.grid = dim3((unsigned)((n + l.groups - 1) / l.groups), (unsigned)((l.per_row + threads - 1) / threads));
-    if (l.per_row <= threads) l.grid.y = 1;
+    l.grid = dim3((unsigned)((n + l.groups - 1) / l.groups), (unsigned)((l.per_row + threads - 1) / threads), 2);   // z: K, V
     l.block = dim3((unsigned)threads);
     return l;
 }
