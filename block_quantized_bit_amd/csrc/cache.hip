@@ -139,12 +139,13 @@ __device__ inline void transpose4(uint32_t (&w)[4]) {
 // one byte per token (V) and 8 bytes of scales: tokens 4 k .. 4 k + 3 of a sequence, as many of them as are the call's.
 struct GroupCount {
     const Seqs& s;
+    int log2;             // tokens per group: 4, or 32 for whole units
     __device__ uint32_t operator()(int b) const {
         int r0, r1;
         seq_rows(s, b, &r0, &r1);
         if (r0 == r1) return 0;
         const int64_t p0 = (int64_t)s.len[b] - (r1 - r0);
-        return (uint32_t)(((p0 + (r1 - r0) - 1) >> 2) - (p0 >> 2) + 1);
+        return (uint32_t)(((p0 + (r1 - r0) - 1) >> log2) - (p0 >> log2) + 1);
     }
 };
 struct Group {
@@ -161,7 +162,7 @@ __device__ inline bool thread_group(const Seqs& s, int nb, int per_row, int grou
     uint32_t before;
     int seq, r0, r1;
     if (s.row_start) {
-        const GroupCount count{s};
+        const GroupCount count{s, 2};
         seq = SeqTotals(s.batch, count).find(first, &before);
         if (seq < 0) return false;
         if (in >= per_row || in_block >= groups_per_block) return false;
@@ -192,78 +193,124 @@ __device__ inline bool thread_group(const Seqs& s, int nb, int per_row, int grou
 
 }  // namespace
 
-// Bound by instructions, then by memory: 36176 rows of 8 heads of 128 (bf16, q4_1) TODO us.
-template <bool Q41, bool F32, int NB>
-__global__ __launch_bounds__(256) void k_cache_write(Seqs s, int per_row, int groups_per_block, const void* __restrict__ k, int64_t ldk,
-                                                     const void* __restrict__ v, int64_t ldv, uint8_t* __restrict__ cache) {
-    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim);
-    Group q;
-    if (!thread_group(s, NB, per_row, groups_per_block, &q)) return;
-    const int64_t cap = (int64_t)s.table_ld * s.page;
-    const int first = max(q.first, q.token < 0 ? (int)min((int64_t)4, -q.token) : 0);
-    if (first >= q.end || q.token >= cap) return;           // (cap is a multiple of 4)
-    const int64_t at = seq_unit(s, q.seq, q.h, (int)(q.token < 0 ? 0 : q.token));
-    const bool is_v = blockIdx.z;
-    const void* const src = is_v ? v : k;
-    const int64_t ld = is_v ? ldv : ldk;
-    float x[4][8];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        // (a row that is not the call's is read as its neighbour that is)
-        const int64_t row = q.row + max(first, min(i, q.end - 1));
-        load8<F32>(src, row * ld + q.h * dim + q.b * 32 + q.g * 8, x[i]);
-    }
+// 8 channels of the group's tokens [first, end): codes and scales.  A row that is not the call's is read as its neighbour
+// that is.
+struct GroupCodes {
     uint32_t w[4];
     uint16_t d[4], m[4];
+};
+template <bool Q41, bool F32>
+__device__ inline GroupCodes quantize_group(const void* src, int64_t ld, int64_t row, int col, int first, int end) {
+    float x[4][8];
 #pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = quantize_block<Q41>(x[i], &d[i], &m[i]);
-    if (at < 0) return;
-    // token 0's place in its unit (a multiple of 4; a group that begins before the sequence ends before token 1)
-    const int u0 = q.token < 0 ? 0 : (int)(q.token % s.page) % kUnit;
-    uint8_t* const to = cache + at + (is_v ? half : 0);
-    uint16_t* const sc = reinterpret_cast<uint16_t*>(to + 16 * dim) + cache_scale(NB, u0, q.b);
-    const bool whole = first == 0 && q.end == 4;
-    if (q.g == 0) {
-        if (whole) {
-            *reinterpret_cast<u16x4*>(sc) = (u16x4){d[0], d[1], d[2], d[3]};
-            if constexpr (Q41) *reinterpret_cast<u16x4*>(sc + dim) = (u16x4){m[0], m[1], m[2], m[3]};
-        } else {
+    for (int i = 0; i < 4; i++) load8<F32>(src, (row + max(first, min(i, end - 1))) * ld + col, x[i]);
+    GroupCodes c;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (i < first || i >= q.end) continue;
-                sc[i] = d[i];
-                if constexpr (Q41) sc[dim + i] = m[i];
-            }
-        }
-    }
-    if (!is_v) {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (i >= first && i < q.end) *reinterpret_cast<uint32_t*>(to + cache_k_word(NB, u0 + i, q.b, q.g)) = w[i];
-        return;
-    }
-    // V: channels 8 g + n of this lane's codes are the low nibbles of the bytes for g < 2, and the high ones of the lane
-    // g ^ 2's channels: this lane writes the bytes of channels 8 (g & 1) + 4 (g >> 1) + 0..3
-    const int c0 = 8 * (q.g & 1) + 4 * (q.g >> 1);
+    for (int i = 0; i < 4; i++) c.w[i] = quantize_block<Q41>(x[i], &c.d[i], &c.m[i]);
+    return c;
+}
+// V's bytes: channels 8 g + n of a lane's codes are the low nibbles of the bytes for g < 2, and the high ones of the lane
+// g ^ 2's channels: a lane makes the bytes of channels 8 (g & 1) + 4 (g >> 1) + 0..3, one token each.
+__device__ inline int v_first(int g) { return 8 * (g & 1) + 4 * (g >> 1); }
+__device__ inline void codes_to_bytes(int g, uint32_t (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const uint32_t other = quad_xor<2>(w[i]);
-        const uint32_t lo = q.g < 2 ? w[i] & 0xFFFFu : other >> 16, hi = q.g < 2 ? other & 0xFFFFu : w[i] >> 16;
+        const uint32_t lo = g < 2 ? w[i] & 0xFFFFu : other >> 16, hi = g < 2 ? other & 0xFFFFu : w[i] >> 16;
         w[i] = spread4(lo) | (spread4(hi) << 4);
     }
-    if (whole) {
-        transpose4(w);
-#pragma unroll
-        for (int i = 0; i < 4; i++) *reinterpret_cast<uint32_t*>(to + cache_v_byte(NB, u0, q.b, c0 + i)) = w[i];
-        return;
+}
+// All four tokens, from place u0 (a multiple of 4) of the unit's K or V part at `to` (memory or LDS).
+template <bool Q41, int NB>
+__device__ inline void store_whole(GroupCodes& c, bool is_v, int u0, int b, int g, uint8_t* to) {
+    constexpr int dim = 32 * NB;
+    if (g == 0) {
+        uint16_t* const sc = reinterpret_cast<uint16_t*>(to + 16 * dim) + cache_scale(NB, u0, b);
+        *reinterpret_cast<u16x4*>(sc) = (u16x4){c.d[0], c.d[1], c.d[2], c.d[3]};
+        if constexpr (Q41) *reinterpret_cast<u16x4*>(sc + dim) = (u16x4){c.m[0], c.m[1], c.m[2], c.m[3]};
     }
-    // some of the four are not the call's: only the others' bytes
+    if (is_v) {
+        codes_to_bytes(g, c.w);
+        transpose4(c.w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        *reinterpret_cast<uint32_t*>(to + (is_v ? cache_v_byte(NB, u0, b, v_first(g) + i) : cache_k_word(NB, u0 + i, b, g))) = c.w[i];
+}
+// The tokens [first, end) of the four, and no byte of the others.
+template <bool Q41, int NB>
+__device__ inline void store_some(GroupCodes& c, bool is_v, int u0, int b, int g, int first, int end, uint8_t* to) {
+    constexpr int dim = 32 * NB;
+    uint16_t* const sc = reinterpret_cast<uint16_t*>(to + 16 * dim) + cache_scale(NB, u0, b);
+    if (is_v) codes_to_bytes(g, c.w);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        if (i < first || i >= q.end) continue;
+        if (i < first || i >= end) continue;
+        if (g == 0) {
+            sc[i] = c.d[i];
+            if constexpr (Q41) sc[dim + i] = c.m[i];
+        }
+        if (is_v) {
 #pragma unroll
-        for (int n = 0; n < 4; n++) to[cache_v_byte(NB, u0 + i, q.b, c0 + n)] = (uint8_t)(w[i] >> (8 * n));
+            for (int n = 0; n < 4; n++) to[cache_v_byte(NB, u0 + i, b, v_first(g) + n)] = (uint8_t)(c.w[i] >> (8 * n));
+        } else {
+            *reinterpret_cast<uint32_t*>(to + cache_k_word(NB, u0 + i, b, g)) = c.w[i];
+        }
     }
+}
+
+// Few rows per sequence: bound by the way to memory and back (lengths, pages, rows): one row of 20 heads of 64 3.6 us.
+template <bool Q41, bool F32, int NB>
+__global__ __launch_bounds__(256) void k_cache_write(Seqs s, int per_row, int groups_per_block, const void* __restrict__ k, int64_t ldk,
+                                                     const void* __restrict__ v, int64_t ldv, uint8_t* __restrict__ cache) {
+    constexpr int dim = 32 * NB;
+    Group q;
+    if (!thread_group(s, NB, per_row, groups_per_block, &q)) return;
+    const int first = max(q.first, q.token < 0 ? (int)min((int64_t)4, -q.token) : 0);
+    if (first >= q.end || q.token >= (int64_t)s.table_ld * s.page) return;   // (the capacity is a multiple of 4)
+    const int token = q.token < 0 ? 0 : (int)q.token;
+    const int64_t at = seq_unit(s, q.seq, q.h, token);
+    if (at < 0) return;
+    const bool is_v = blockIdx.z;
+    GroupCodes c = quantize_group<Q41, F32>(is_v ? v : k, is_v ? ldv : ldk, q.row, q.h * dim + q.b * 32 + q.g * 8, first, q.end);
+    uint8_t* const to = cache + at + (is_v ? cache_half_bytes(Q41, dim) : 0);
+    const int u0 = token % s.page % kUnit;   // (below 0: only tokens of a group that ends before the first one)
+    if (first == 0 && q.end == 4) store_whole<Q41, NB>(c, is_v, u0, q.b, q.g, to);
+    else store_some<Q41, NB>(c, is_v, u0, q.b, q.g, first, q.end, to);
+}
+
+// Many rows per sequence: a workgroup makes one unit's K, or V, of one head.  In the unit's order a lane's results are
+// 4-byte pieces 16 bytes apart, so a whole unit is put together in LDS and written in 16-byte pieces side by side.
+template <bool Q41, bool F32, int NB>
+__global__ __launch_bounds__(NB == 3 ? 128 : 32 * NB) void k_cache_write_units(Seqs s, const void* __restrict__ k, int64_t ldk,
+                                                                               const void* __restrict__ v, int64_t ldv,
+                                                                               uint8_t* __restrict__ cache) {
+    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), threads = NB == 3 ? 128 : 32 * NB;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[half];
+    uint32_t before;
+    const int seq = SeqTotals(s.batch, GroupCount{s, 5}).find(blockIdx.x, &before);
+    if (seq < 0) return;
+    int r0, r1;
+    seq_rows(s, seq, &r0, &r1);
+    const int64_t p0 = (int64_t)s.len[seq] - (r1 - r0), t0 = ((p0 >> 5) + (blockIdx.x - before)) * kUnit;   // the unit's token 0
+    if (t0 < 0 || t0 >= (int64_t)s.table_ld * s.page) return;   // (units before the first token, past the last page)
+    const int h = blockIdx.y;
+    const int64_t at = seq_unit(s, seq, h, (int)t0);
+    if (at < 0) return;
+    const int gi = threadIdx.x / (4 * NB), cg = threadIdx.x - gi * (4 * NB), b = cg >> 2, g = cg & 3;
+    const int64_t t = t0 + 4 * gi, lo = p0 > 0 ? p0 : 0, hi = p0 + (r1 - r0);
+    const int first = t < lo ? (int)min((int64_t)4, lo - t) : 0, end = t + 4 > hi ? (int)max((int64_t)0, hi - t) : 4;
+    const bool is_v = blockIdx.z, whole = t0 >= lo && t0 + kUnit <= hi;
+    uint8_t* const to = cache + at + (is_v ? half : 0);
+    if (gi < 8 && first < end) {
+        GroupCodes c = quantize_group<Q41, F32>(is_v ? v : k, is_v ? ldv : ldk, r0 + (t - p0), h * dim + b * 32 + g * 8, first, end);
+        if (whole) store_whole<Q41, NB>(c, is_v, 4 * gi, b, g, lds);
+        else store_some<Q41, NB>(c, is_v, 4 * gi, b, g, first, end, to);
+    }
+    if (!whole) return;
+    __syncthreads();
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    for (int i = threadIdx.x; i < half / 16; i += threads) reinterpret_cast<u32x4*>(to)[i] = reinterpret_cast<const u32x4*>(lds)[i];
 }
 
 // Bound by memory: 36176 rows of 8 heads of 128 (q4_1 to bf16) TODO us.
@@ -319,6 +366,9 @@ __global__ __launch_bounds__(256) void k_cache_read(Seqs s, int per_row, int gro
 
 namespace {
 
+// Rows per sequence, on average, from which whole units are written.
+constexpr int64_t kManyRows = 16;
+
 // Threads per group, groups per workgroup, the launch.
 struct Launch {
     int per_row, groups;
@@ -338,6 +388,14 @@ Launch group_launch(const Seqs& s, int nb) {
 
 template <int NB>
 void write_nb(const Seqs& q, bool q41, bool f32, const void* k, int64_t ldk, const void* v, int64_t ldv, uint8_t* cache, hipStream_t s) {
+    if (q.row_start && (int64_t)q.rows >= kManyRows * (int64_t)q.batch) {
+        // units of 32 tokens: n rows touch at most n / 32 + 2
+        const dim3 grid((unsigned)((int64_t)q.rows / kUnit + 2 * (int64_t)std::min(q.rows, q.batch)), (unsigned)q.heads, 2);
+        auto f = q41 ? (f32 ? k_cache_write_units<true, true, NB> : k_cache_write_units<true, false, NB>)
+                     : (f32 ? k_cache_write_units<false, true, NB> : k_cache_write_units<false, false, NB>);
+        hipLaunchKernelGGL(f, grid, dim3(NB == 3 ? 128 : 32 * NB), 0, s, q, k, ldk, v, ldv, cache);
+        return;
+    }
     const Launch l = group_launch(q, NB);
     auto f = q41 ? (f32 ? k_cache_write<true, true, NB> : k_cache_write<true, false, NB>)
                  : (f32 ? k_cache_write<false, true, NB> : k_cache_write<false, false, NB>);
