@@ -55,18 +55,11 @@ __device__ inline SeqInfo seq_info(const AttnArgs& a, int b) {   // b per lane
 
 // The same for a uniform b, through scalar loads.
 __device__ inline SeqInfo seq_info_uniform(const AttnArgs& a, int b) {
-    const Seqs& s = a.s;
+    const SeqRows r = seq_rows_uniform(a.s, b);
+    const int len = r.len, cap = a.s.table_ld * a.s.page;
     SeqInfo q;
-    int r0 = b, r1 = b + 1;
-    if (s.row_start) {
-        r0 = read_const(s.row_start, b);
-        r1 = read_const(s.row_start, b + 1);
-        r0 = r0 < 0 ? 0 : r0 > s.rows ? s.rows : r0;
-        r1 = r1 < r0 ? r0 : r1 > s.rows ? s.rows : r1;
-    }
-    const int len = read_const(s.len, b), cap = s.table_ld * s.page;
-    q.r0 = r0;
-    q.n = r1 - r0;
+    q.r0 = r.r0;
+    q.n = r.r1 - r.r0;
     q.tokens = len < 0 ? 0 : len < cap ? len : cap;
     q.pos0 = (int64_t)len - q.n;
     return q;

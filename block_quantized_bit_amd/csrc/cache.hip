@@ -61,11 +61,16 @@ __device__ inline float quad_xor(float v) { return __uint_as_float(quad_xor<X>(_
 // Quantizes a block of 32 held by 4 neighbouring lanes (8 values each, in lane order).  Returns the 8 codes, nibble n =
 // value n; d, m: fp16 bits (m only for q4_1).
 //
-// The codes are rint of the correctly rounded quotients t = RN(x / d), in 3 instructions a value in place of a division's
-// 10: with r = RN(1/d), q = RN(x r) is t (1 + a), |a| <= 2^-23, and q + r RN(x - d q) is t within 2^-46 of it.  A tie of the
-// rounding to 24 bits is mid d = x with mid of 25 bits and d of 11: unless it is met exactly, x / d is at least 2^-36 away
-// from it, so the corrected quotient rounds to the same side.  (Where the remainder underflows, |t| is far below 1/2.)
-// d = 0: r = 0 gives the code of 0.
+// The codes are rint of the correctly rounded quotients RN(x / d), in 3 instructions a value in place of a division's 10
+// (and d itself likewise from (max - min) / 15): with r = 1/d to 1 ulp, q = RN(x r) is (x / d)(1 + a), |a| < 2^-21, and
+// q + r RN(x - d q) is x / d to 2^-44 before its rounding.  A tie of the rounding to 24 bits is mid d = x with mid of 25
+// bits and d of at most 11: unless it is met exactly, x / d is at least 2^-36 away from it, so the corrected quotient
+// rounds to the same side.  (Where the remainder underflows, the quotient is far below 1/2.)  d = 0: r = 0 gives the code
+// of 0.
+__device__ inline float corrected_quotient(float x, float d, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, d, x), r, q);
+}
 template <bool Q41>
 __device__ inline uint32_t quantize_block(float v[8], uint16_t* d, uint16_t* m) {
 #pragma unroll
@@ -82,7 +87,7 @@ __device__ inline uint32_t quantize_block(float v[8], uint16_t* d, uint16_t* m) 
         hi = fmaxf(hi, quad_xor<1>(hi));
         lo = fminf(lo, quad_xor<2>(lo));
         hi = fmaxf(hi, quad_xor<2>(hi));
-        *d = f16_sat_bits((hi - lo) / 15.0f);
+        *d = f16_sat_bits(corrected_quotient(hi - lo, 15.0f, 1.0f / 15.0f));
         *m = f16_sat_bits(lo);
         const float mu = f16_value(*m);
 #pragma unroll
@@ -96,16 +101,15 @@ __device__ inline uint32_t quantize_block(float v[8], uint16_t* d, uint16_t* m) 
         big = fabsf(o1) > fabsf(big) || ((threadIdx.x & 1) && fabsf(o1) == fabsf(big)) ? o1 : big;
         const float o2 = quad_xor<2>(big);
         big = fabsf(o2) > fabsf(big) || ((threadIdx.x & 2) && fabsf(o2) == fabsf(big)) ? o2 : big;
-        *d = f16_sat_bits(big / -8.0f);
+        *d = f16_sat_bits(big * -0.125f);
         *m = 0;
         low = -8.0f;
     }
-    const float delta = f16_value(*d), r = delta != 0.0f ? 1.0f / delta : 0.0f;
+    const float delta = f16_value(*d), r = delta != 0.0f ? __builtin_amdgcn_rcpf(delta) : 0.0f;
     float c[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        float q = v[j] * r;
-        q = fmaf(fmaf(-q, delta, v[j]), r, q);
+        const float q = corrected_quotient(v[j], delta, r);
         c[j] = rintf(__builtin_amdgcn_fmed3f(q, low, low + 15.0f));   // (the limits are whole: before or after rint is the same)
     }
     // four codes as one whole number
@@ -279,38 +283,46 @@ __global__ __launch_bounds__(256) void k_cache_write(Seqs s, int per_row, int gr
     else store_some<Q41, NB>(c, is_v, u0, q.b, q.g, first, q.end, to);
 }
 
-// Many rows per sequence: a workgroup makes one unit's K, or V, of one head.  In the unit's order a lane's results are
+// Many rows per sequence: a workgroup makes one unit of one head.  In the unit's order a lane's results are
 // 4-byte pieces 16 bytes apart, so a whole unit is put together in LDS and written in 16-byte pieces side by side.
 template <bool Q41, bool F32, int NB>
 __global__ __launch_bounds__(NB == 3 ? 128 : 32 * NB) void k_cache_write_units(Seqs s, const void* __restrict__ k, int64_t ldk,
                                                                                const void* __restrict__ v, int64_t ldv,
                                                                                uint8_t* __restrict__ cache) {
     constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), threads = NB == 3 ? 128 : 32 * NB;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[half];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * half];
     uint32_t before;
     const int seq = SeqTotals(s.batch, GroupCount{s, 5}).find(blockIdx.x, &before);
     if (seq < 0) return;
-    int r0, r1;
-    seq_rows(s, seq, &r0, &r1);
-    const int64_t p0 = (int64_t)s.len[seq] - (r1 - r0), t0 = ((p0 >> 5) + (blockIdx.x - before)) * kUnit;   // the unit's token 0
+    const SeqRows r = seq_rows_uniform(s, seq);
+    const int r0 = r.r0, r1 = r.r1;
+    const int64_t p0 = (int64_t)r.len - (r1 - r0), t0 = ((p0 >> 5) + (blockIdx.x - before)) * kUnit;   // the unit's token 0
     if (t0 < 0 || t0 >= (int64_t)s.table_ld * s.page) return;   // (units before the first token, past the last page)
     const int h = blockIdx.y;
-    const int64_t at = seq_unit(s, seq, h, (int)t0);
-    if (at < 0) return;
     const int gi = threadIdx.x / (4 * NB), cg = threadIdx.x - gi * (4 * NB), b = cg >> 2, g = cg & 3;
     const int64_t t = t0 + 4 * gi, lo = p0 > 0 ? p0 : 0, hi = p0 + (r1 - r0);
     const int first = t < lo ? (int)min((int64_t)4, lo - t) : 0, end = t + 4 > hi ? (int)max((int64_t)0, hi - t) : 4;
-    const bool is_v = blockIdx.z, whole = t0 >= lo && t0 + kUnit <= hi;
-    uint8_t* const to = cache + at + (is_v ? half : 0);
+    const bool whole = t0 >= lo && t0 + kUnit <= hi;
+    const int64_t at = seq_unit_uniform(s, seq, h, (int)t0);
+    if (at < 0) return;
+    uint8_t* const to = cache + at;
     if (gi < 8 && first < end) {
-        GroupCodes c = quantize_group<Q41, F32>(is_v ? v : k, is_v ? ldv : ldk, r0 + (t - p0), h * dim + b * 32 + g * 8, first, end);
-        if (whole) store_whole<Q41, NB>(c, is_v, 4 * gi, b, g, lds);
-        else store_some<Q41, NB>(c, is_v, 4 * gi, b, g, first, end, to);
+        const int64_t row = r0 + (t - p0);
+        const int col = h * dim + b * 32 + g * 8;
+        GroupCodes ck = quantize_group<Q41, F32>(k, ldk, row, col, first, end);
+        GroupCodes cv = quantize_group<Q41, F32>(v, ldv, row, col, first, end);
+        if (whole) {
+            store_whole<Q41, NB>(ck, false, 4 * gi, b, g, lds);
+            store_whole<Q41, NB>(cv, true, 4 * gi, b, g, lds + half);
+        } else {
+            store_some<Q41, NB>(ck, false, 4 * gi, b, g, first, end, to);
+            store_some<Q41, NB>(cv, true, 4 * gi, b, g, first, end, to + half);
+        }
     }
     if (!whole) return;
     __syncthreads();
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    for (int i = threadIdx.x; i < half / 16; i += threads) reinterpret_cast<u32x4*>(to)[i] = reinterpret_cast<const u32x4*>(lds)[i];
+    for (int i = threadIdx.x; i < 2 * half / 16; i += threads) reinterpret_cast<u32x4*>(to)[i] = reinterpret_cast<const u32x4*>(lds)[i];
 }
 
 // Bound by memory: 36176 rows of 8 heads of 128 (q4_1 to bf16) TODO us.
@@ -390,7 +402,7 @@ template <int NB>
 void write_nb(const Seqs& q, bool q41, bool f32, const void* k, int64_t ldk, const void* v, int64_t ldv, uint8_t* cache, hipStream_t s) {
     if (q.row_start && (int64_t)q.rows >= kManyRows * (int64_t)q.batch) {
         // units of 32 tokens: n rows touch at most n / 32 + 2
-        const dim3 grid((unsigned)((int64_t)q.rows / kUnit + 2 * (int64_t)std::min(q.rows, q.batch)), (unsigned)q.heads, 2);
+        const dim3 grid((unsigned)((int64_t)q.rows / kUnit + 2 * (int64_t)std::min(q.rows, q.batch)), (unsigned)q.heads);
         auto f = q41 ? (f32 ? k_cache_write_units<true, true, NB> : k_cache_write_units<true, false, NB>)
                      : (f32 ? k_cache_write_units<false, true, NB> : k_cache_write_units<false, false, NB>);
         hipLaunchKernelGGL(f, grid, dim3(NB == 3 ? 128 : 32 * NB), 0, s, q, k, ldk, v, ldv, cache);

@@ -13,6 +13,27 @@ typedef const int32_t __attribute__((address_space(4))) * const_i32;
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ inline int read_const(const int32_t* p, int64_t i) { return ((const_i32)(uintptr_t)p)[i]; }
 
+// seq_rows, the length and seq_unit for a uniform sequence, through scalar loads.
+struct SeqRows {
+    int r0, r1, len;
+};
+__device__ inline SeqRows seq_rows_uniform(const Seqs& s, int b) {
+    SeqRows r = {b, b + 1, read_const(s.len, b)};
+    if (s.row_start) {
+        const int a = read_const(s.row_start, b), e = read_const(s.row_start, b + 1);
+        r.r0 = a < 0 ? 0 : a > s.rows ? s.rows : a;
+        r.r1 = e < r.r0 ? r.r0 : e > s.rows ? s.rows : e;
+    }
+    return r;
+}
+__device__ inline int64_t seq_unit_uniform(const Seqs& s, int b, int h, int t) {
+    const int j = t / s.page;
+    if (j >= s.table_ld) return -1;
+    const int64_t p = s.table ? (int64_t)read_const(s.table, (int64_t)b * s.table_ld + j) : (int64_t)b;
+    if (p < 0 || p >= s.pages) return -1;
+    return ((p * s.heads + h) * s.upp + (t - j * s.page) / kUnit) * s.unit_bytes;
+}
+
 // Inclusive prefix sum over the wave: lanes 1, 2, 4, 8 below within rows of 16, then the rows' totals.
 template <int CTRL, int ROWS>
 __device__ inline uint32_t add_dpp(uint32_t v) {
