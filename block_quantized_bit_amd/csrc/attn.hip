@@ -271,11 +271,10 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
     int put = 0, get = 0;   // byte offsets of the slots to fill and to read next
     const auto next = [](int at) { return at + bytes == D * bytes ? 0 : at + bytes; };
     const auto request = [&](int i) {
-        const int64_t at = walk.at();
-        walk.step(NW);
-        request_unit<bytes>(a.cache + (at < 0 ? 0 : at), uniform(ring_at + put));
+        request_unit<bytes>(walk.at(a.cache), uniform(ring_at + put));
         put = next(put);
-        absent = at < 0 ? absent | 1u << (i & 31) : absent & ~(1u << (i & 31));
+        absent = walk.there ? absent & ~(1u << (i & 31)) : absent | 1u << (i & 31);
+        walk.step(NW);
     };
 #pragma unroll
     for (int i = 0; i < D - 1; i++)
@@ -527,43 +526,47 @@ struct Pair {
 // take them, 1 KiB fragments of 16 bytes a lane: K: fragment (16 channels) lane 32 (g % 2) + token; V: fragment (block,
 // 16-token tile) lane 32 (g % 2) + channel, half g / 2 of its 16 bytes.  V's two words are the block's two tiles.
 struct PairPlace {
-    int code, ks[2], ko[2], vs, vo, token;   // token: V's byte 0 within a tile
+    uint32_t kc, vc, ks[2], vs;              // byte offsets in the unit: words, scales
+    int ko[2], vo, token;                    // token: V's byte 0 within a tile
 };
-template <int NB>
+template <int NB, bool Q41>
 __device__ inline PairPlace pair_place(int p) {   // p: which 8 bytes of the unit's codes
+    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim);
     const bool tail = NB % 2 && p >= NB / 2 * 128;
     const int lane = tail ? p - NB / 2 * 128 : (p & 127) >> 1, w0 = tail ? 2 * NB - 2 : (p >> 7) * 4 + (p & 1) * 2;
     const int g = lane >> 4, x = lane & 15;
     PairPlace r;
-    r.code = p * 8;
+    r.kc = p * 8;
+    r.vc = half + p * 8;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         const int tile = (w0 + j) / NB, b = (w0 + j) - tile * NB;
-        r.ks[j] = ((tile * 4 + (x >> 2)) * NB + b) * 8 + (x & 3) * 2;
+        r.ks[j] = 16 * dim + ((tile * 4 + (x >> 2)) * NB + b) * 8 + (x & 3) * 2;
         r.ko[j] = (2 * b + (g >> 1)) * 1024 + ((g & 1) * 32 + 16 * tile + x) * 16;
     }
-    r.vs = (g * NB + (w0 >> 1)) * 8;
+    r.vs = half + 16 * dim + (g * NB + (w0 >> 1)) * 8;
     r.vo = w0 * 1024 + ((g & 1) * 32 + x) * 16 + (g >> 1) * 8;
     r.token = 4 * g;
     return r;
 }
 
 template <int NB, bool Q41>
-__device__ inline void load_pair(const uint8_t* unit, const PairPlace& at, Pair<Q41>* r) {
-    constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), plane = cache_plane_bytes(dim);
-    const u32x2 k = *reinterpret_cast<const u32x2*>(unit + (uint32_t)at.code);
-    const u32x2 v = *reinterpret_cast<const u32x2*>(unit + (uint32_t)(half + at.code));
+__device__ inline void load_pair(global_bytes unit, const PairPlace& at, Pair<Q41>* r) {
+    constexpr int plane = cache_plane_bytes(32 * NB);
+    // (a uniform address and a 32-bit offset per lane each)
+    const u32x2 k = load_at<u32x2>(unit, at.kc);
+    const u32x2 v = load_at<u32x2>(unit, at.vc);
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         r->kw[j] = k[j];
         r->vw[j] = v[j];
-        r->kd[j] = *reinterpret_cast<const uint16_t*>(unit + (uint32_t)(16 * dim + at.ks[j]));
-        const u32x2 d = *reinterpret_cast<const u32x2*>(unit + (uint32_t)(half + 16 * dim + at.vs + j * 32 * NB));
+        r->kd[j] = load_at<uint16_t>(unit, at.ks[j]);
+        const u32x2 d = load_at<u32x2>(unit + j * 32 * NB, at.vs);
         r->vd[j][0] = d[0];
         r->vd[j][1] = d[1];
         if constexpr (Q41) {
-            r->km[j] = *reinterpret_cast<const uint16_t*>(unit + (uint32_t)(16 * dim + plane + at.ks[j]));
-            const u32x2 m = *reinterpret_cast<const u32x2*>(unit + (uint32_t)(half + 16 * dim + plane + at.vs + j * 32 * NB));
+            r->km[j] = load_at<uint16_t>(unit + plane, at.ks[j]);
+            const u32x2 m = load_at<u32x2>(unit + (plane + j * 32 * NB), at.vs);
             r->vm[j][0] = m[0];
             r->vm[j][1] = m[1];
         }
@@ -634,20 +637,22 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     // heads vary fastest, so that a head's tiles (which read the same keys and values) tend to the same die; later tiles,
     // which see more, come first
     int at = blockIdx.x;
-    const int h = at % heads;
-    at /= heads;
-    const int split = at % a.splits;
-    at /= a.splits;
+    const int h = uniform(at % heads);
+    at = uniform(at / heads);
+    const int split = uniform(at % a.splits);
+    at = uniform(at / a.splits);
     uint32_t before;
     const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
     if (seq < 0) return;
     const SeqInfo q = seq_info_uniform(a, seq);
-    const int tile = tiles_of(ts, q.n) - 1 - (at - (int)before);
-    const int first = ts.ht == 1 ? tile * ts.rows : tile / ts.ht, end = min(first + ts.rows, q.n);
+    const int tile = uniform(tiles_of(ts, q.n) - 1 - (at - (int)before));
+    const int first = uniform(ts.ht == 1 ? tile * ts.rows : tile / ts.ht), end = min(first + ts.rows, q.n);
     int u0, u1;
     row_units(a, q, first, end, &u0, &u1);
+    u0 = uniform(u0);
+    u1 = uniform(u1);
     if (a.splits > 1) {
-        const int per = ((u1 - u0 + a.splits - 1) / a.splits + KS - 1) / KS * KS;
+        const int per = uniform(((u1 - u0 + a.splits - 1) / a.splits + KS - 1) / KS * KS);
         u0 += split * per;
         u1 = min(u1, u0 + per);
     }
@@ -661,38 +666,39 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
 
     // this thread's pairs of words: unit (id / 2 dim) of the step, 8 bytes (id % 2 dim) of its codes
     const uint32_t f1024 = held(0x64006400u);
-    int64_t where[KS];                      // the fetched step's units, or -1
-    Pair<Q41> r[rounds];
+    Pair<Q41> r[rounds];                    // the fetched step's
     PairPlace place[rounds];
 #pragma unroll
-    for (int i = 0; i < rounds; i++) place[i] = pair_place<NB>((i * threads + tid) % (2 * dim));
+    for (int i = 0; i < rounds; i++) place[i] = pair_place<NB, Q41>((i * threads + tid) % (2 * dim));
     UnitWalk walk;
     walk.start(a.s, seq, h, u0);
     const auto pair_unit = [&](int i) { return uniform((i * threads + wave * 64) / (2 * dim)); };   // (2 dim % 64 == 0)
     int fetched = u0;                       // unit
-    const auto fetch = [&](Pair<Q41>* r, int64_t* where) {
+    // requests a step's words; returns which of its units have tokens (a bit each)
+    const auto fetch = [&](Pair<Q41>* r) {
+        uint32_t has = 0;
+        global_bytes unit[KS];
 #pragma unroll
         for (int k = 0; k < KS; k++) {
-            where[k] = fetched + k < u1 ? walk.at() : -1;
+            const bool there = fetched + k < u1 && walk.there;
+            has |= (there ? 1u : 0u) << k;
+            unit[k] = scalar_address(there ? walk.at(a.cache) : a.cache);   // (an absent unit's loads are of the pool's first one: cleared below)
             walk.step(1);
         }
         fetched += KS;
 #pragma unroll
         for (int i = 0; i < rounds; i++) {
-            if (i * threads + wave * 64 >= pairs) break;
-            const int64_t p = KS > 1 && pair_unit(i) ? where[KS - 1] : where[0];
-            // (an absent unit's loads are of the pool's first one: cleared below)
-            load_pair<NB, Q41>(a.cache + (p < 0 ? 0 : p), place[i], &r[i]);
+            if (rounds * threads > pairs && i * threads + wave * 64 >= pairs) break;
+            load_pair<NB, Q41>(KS > 1 && pair_unit(i) ? unit[KS - 1] : unit[0], place[i], &r[i]);
         }
+        return has;
     };
     // the tokens of step u that are not in the cache are made zeros
-    const auto clear = [&](Pair<Q41>* r, const int64_t* where, int u) {
+    const auto clear = [&](Pair<Q41>* r, uint32_t has, int u) {
+        if (has == (1u << KS) - 1 && (u + KS) * kUnit <= q.tokens) return;
 #pragma unroll
         for (int i = 0; i < rounds; i++) {
-            if (i * threads + wave * 64 >= pairs) break;
-            const int k = pair_unit(i);
-            const int64_t p = KS > 1 && k ? where[KS - 1] : where[0];
-            const int left = p < 0 ? 0 : max(0, q.tokens - (u + k) * kUnit);
+            const int k = pair_unit(i), left = has >> k & 1 ? q.tokens - (u + k) * kUnit : 0;
             if (left < kUnit) clear_pair<Q41>(place[i], left, &r[i]);
         }
     };
@@ -706,18 +712,14 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     };
 
     // The first `ahead` steps, all requested before the first is used.
-    uint32_t has = 0;                       // bit i: unit i of this step and the `ahead` steps after it has tokens
-    const auto note = [&](const int64_t* where, int step) {
-#pragma unroll
-        for (int k = 0; k < KS; k++) has |= (where[k] >= 0 ? 1u : 0u) << (step * KS + k);
-    };
+    uint32_t has = 0, got;                  // units with tokens: of this step and the `ahead` - 1 after it; of the fetched one
     const uint16_t* const qp = a.q + (int64_t)(q.r0 + row) * a.ldq + (int64_t)(h * a.group + head) * dim + 8 * hl;
     u32x4 qv[2 * NB];
     {
         Pair<Q41> r0[ahead][rounds];
-        int64_t w0[ahead][KS];
+        uint32_t h0[ahead];
 #pragma unroll
-        for (int i = 0; i < ahead; i++) fetch(r0[i], w0[i]);
+        for (int i = 0; i < ahead; i++) h0[i] = fetch(r0[i]);
 #pragma unroll
         for (int s = 0; s < 2 * NB; s++) {
             qv[s] = (u32x4){0, 0, 0, 0};
@@ -726,12 +728,12 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < ahead; i++) {
-            note(w0[i], i);
-            clear(r0[i], w0[i], u0 + i * KS);
+            has |= h0[i] << (i * KS);
+            clear(r0[i], h0[i], u0 + i * KS);
             put(r0[i], lds + i * buffer);
         }
     }
-    fetch(r, where);
+    got = fetch(r);
 
     // queries as fp16, scaled by a power of two per column so that the largest is in [2^14, 2^15)
     f16x8 qf[2 * NB];
@@ -827,8 +829,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
         uint8_t *lk = lds, *ln = lds + buffer, *lp = lds + ahead * buffer;   // this step's, the next one's, the one to fill
         const auto next = [&](uint8_t* at) { return at == lds + ahead * buffer ? lds : at + buffer; };
         for (int u = u0; u < u1; u += KS) {
-            note(where, ahead);
-            clear(r, where, u + ahead * KS);
+            has |= got << (ahead * KS);
+            clear(r, got, u + ahead * KS);
 #pragma unroll
             for (int k = 0; k < KS; k++) {
                 // (behind the last unit the scores are of zeros, and not used)
@@ -872,7 +874,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
                     else __builtin_amdgcn_sched_group_barrier(0x402, (24 + F - 1) / F, 1);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                if (k == 0) fetch(r, where);
+                if (k == 0) got = fetch(r);
                 settle(u + k + 1, has >> (k + 1) & 1);
             }
             has >>= KS;
@@ -958,8 +960,11 @@ Schedule schedule(const AttnArgs& a, bool share) {
     const int64_t units = ((int64_t)a.s.table_ld * a.s.page) / kUnit;   // of the longest sequence there can be
     s.splits = 1;
     if (a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch) {
+        // Twice as many columns share a conversion to fp16, with one workgroup per compute unit instead of two: in us, 256
+        // and 128 columns, 2048 rows of 8 x 4 heads of 128 over 18432 tokens 596 and 719, two prompts of 2048 rows 108 and
+        // 122, but 8 prompts of 700 rows, 12 heads of 96, 51 and 45, 4 of 1500, 20 heads of 64, 80 and 75.
         items(256);
-        if (s.items < 256 || a.dim == 256) items(128);
+        if (s.items < 256 || units < 64 || a.dim == 256) items(128);
         if (share && s.items <= kRowItems)
             s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * kRowItems / s.items, units / kRowLeast, 64}));
     } else {

@@ -97,54 +97,71 @@ struct TileCount {
     }
 };
 
-// Where the units of one head of one sequence are, unit by unit.  The table entry of the next unit is requested a step
-// before it is used.
+// Where the units of one head of one sequence are, unit by unit.  The wave holds 64 table entries, one a lane: an entry
+// read when it is needed would be a scalar load, whose wait is also one for every LDS read that is on its way.
 struct UnitWalk {
     const int32_t* table;   // this sequence's row, or null
-    int upp, table_ld;
+    int upp, table_ld, seq, pages;
     int j, k;               // page and unit within it
-    int64_t pages, head_units, unit_bytes, per_page;
-    int entry;              // of page j
-    int64_t cur;            // byte offset of the unit, or -1
+    int j0, entries;        // entries (per lane): of page j0 + lane
+    int per_page, head_units, unit_bytes;
+    int64_t cur;            // byte offset of the unit (the pool's first one's where it is absent)
+    int there;              // whether it has a page
 
-    __device__ void start(const Seqs& q, int seq, int head, int unit) {
+    __device__ void start(const Seqs& q, int sequence, int head, int unit) {
         upp = q.upp;
         table_ld = q.table_ld;
-        table = q.table ? q.table + (int64_t)seq * q.table_ld : nullptr;
-        pages = q.pages;
-        unit_bytes = q.unit_bytes;
-        per_page = (int64_t)q.heads * q.upp;
-        head_units = (int64_t)head * q.upp;
-        j = unit / upp;
+        table = q.table ? q.table + (int64_t)sequence * q.table_ld : nullptr;
+        seq = sequence;
+        pages = (int)q.pages;
+        unit_bytes = (int)q.unit_bytes;
+        per_page = q.heads * q.upp;     // below 2^16 2^19, and below 2^46 / unit bytes / pages: see the page limits
+        head_units = head * q.upp;
+        j = uniform(unit / upp);   // (a quotient is made by the vector unit, and would keep what follows from it there)
         k = unit - j * upp;
-        entry = seq;
-        read();
-        fresh = true;
+        hold();
+        place();
     }
-    __device__ void read() {
-        if (table) entry = j < table_ld ? read_const(table, j) : -1;
-        else if (j > 0) entry = -1;
+    __device__ void hold() {
+        j0 = j;
+        const int at = j + (threadIdx.x & 63);
+        entries = -1;
+        if (at < table_ld) entries = table ? table[at] : seq;
+        asm volatile("" : "+v"(entries));   // waited for here, and not wherever an entry is used
+    }
+    __device__ void place() {
+        const int entry = __builtin_amdgcn_readlane(entries, j - j0);
+        there = (unsigned)entry < (unsigned)pages;
+        cur = there ? ((int64_t)entry * per_page + (head_units + k)) * unit_bytes : 0;
     }
     __device__ void step(int n) {
         k += n;
         if (k < upp) {
-            cur = cur < 0 ? cur : cur + n * unit_bytes;
+            cur += there ? n * unit_bytes : 0;
             return;
         }
         do {
             k -= upp;
             j++;
         } while (k >= upp);
-        read();
-        fresh = true;
+        if (j - j0 >= 64) hold();
+        place();
     }
-    __device__ int64_t at() {
-        if (fresh) cur = entry >= 0 && entry < pages ? ((int64_t)entry * per_page + head_units + k) * unit_bytes : -1;
-        fresh = false;
-        return cur;
-    }
-    bool fresh;             // cur is to be made from entry
+    // The unit's address.
+    __device__ const uint8_t* at(const uint8_t* cache) const { return cache + cur; }
 };
+// An address in scalar registers whose origin the compiler does not see: it would else add the lanes' offsets to the
+// part that does not change, and hold 64-bit sums of them in vector registers.
+typedef const uint8_t __attribute__((address_space(1))) * global_bytes;
+__device__ inline global_bytes scalar_address(const uint8_t* p) {
+    uint64_t v = (uint64_t)(uintptr_t)p;
+    asm("" : "+s"(v));
+    return (global_bytes)v;
+}
+template <class T>
+__device__ inline T load_at(global_bytes p, uint32_t offset) {
+    return *(const T __attribute__((address_space(1)))*)(p + offset);
+}
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 

@@ -128,9 +128,12 @@ def _call_on(where: str, s: wq_seqs, tensors, stream, check: bool, fn, *args) ->
         if _torch is None:
             import torch
             _torch = torch
-        if dev != _torch.cuda.current_device():
+        if dev != _torch._C._cuda_getDevice():
             with _torch.cuda.device(dev):
                 return _check(fn(*args, _stream(stream)), where, check)
+        if stream is None:
+            return _check(fn(*args, _torch._C._cuda_getCurrentRawStream(dev)), where, check)
+    return _check(fn(*args, _stream(stream)), where, check)
     return _check(fn(*args, _stream(stream)), where, check)
 
 
