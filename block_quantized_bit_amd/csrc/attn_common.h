@@ -115,7 +115,7 @@ struct UnitWalk {
         seq = sequence;
         pages = (int)q.pages;
         unit_bytes = (int)q.unit_bytes;
-        per_page = q.heads * q.upp;     // below 2^16 2^19, and below 2^46 / unit bytes / pages: see the page limits
+        per_page = q.heads * q.upp;     // (below 2^31: a cache is at most 2^41 bytes)
         head_units = head * q.upp;
         j = uniform(unit / upp);   // (a quotient is made by the vector unit, and would keep what follows from it there)
         k = unit - j * upp;

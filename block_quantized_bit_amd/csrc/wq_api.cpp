@@ -191,7 +191,7 @@ wq_status check_cache(const wq_cache_desc* d, wq::Seqs* q, bool* q41) {
     q->pages = d->pages;
     q->unit_bytes = wq::cache_unit_bytes(*q41, d->head_dim);
     const int64_t page_bytes = q->unit_bytes * q->upp * d->kv_heads;   // < 2^14 2^19 2^16
-    if (d->pages > (int64_t(1) << 46) / page_bytes) return WQ_ERR_SHAPE;
+    if (d->pages > (int64_t(1) << 41) / page_bytes) return WQ_ERR_SHAPE;   // (so that a page's units fit 32 bits)
     return WQ_OK;
 }
 
@@ -512,7 +512,7 @@ wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, con
     if ((st = check_rows(y, ldy, width)) != WQ_OK) return st;
     if (!cache) return WQ_ERR_INVALID_ARG;
     if (!aligned(cache, 16)) return WQ_ERR_ALIGNMENT;
-    if (!std::isfinite(scale)) return WQ_ERR_INVALID_ARG;
+    if (!std::isfinite(scale * 1.44269504088896340736f)) return WQ_ERR_INVALID_ARG;
     if (causal != 0 && causal != 1) return WQ_ERR_INVALID_ARG;
     if (window < 0 || (window > 0 && !causal)) return WQ_ERR_INVALID_ARG;
     if (a.s.rows == 0 || a.s.batch == 0) return WQ_OK;

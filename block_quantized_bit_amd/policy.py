@@ -23,6 +23,7 @@ from dataclasses import dataclass, field
 from . import wq
 
 D_MODEL, FFN, ENC_LAYERS, DEC_LAYERS = 1280, 5120, 32, 4
+HEADS, HEAD_DIM = 20, 64
 VOCAB, DEC_POSITIONS, ENC_POSITIONS = 51866, 448, 1500
 
 # Bits per weight of each format as packed by libwq (codes + scales; NF4+DQ's group scales and
@@ -197,4 +198,30 @@ def _merge_once_per_utterance(calls: list[Call]) -> list[Call]:
             continue
         m = out[at[key]]
         out[at[key]] = Call(m.names + c.names, m.fmt, m.n + c.n, m.k, m.split_n + c.split_n, m.rows, merged=True)
+    return out
+
+
+@dataclass(frozen=True)
+class DecoderCache:
+    """A decoder layer's key/value cache of `sequences` utterances, one page each (no page table): the self-attention's
+    grows by the decoded tokens, the cross-attention's is written once with the encoder's frames."""
+    layer: int
+    kind: str          # "self" | "cross"
+    desc: wq.wq_cache_desc
+    causal: bool       # as wq_attn takes it
+
+
+def decoder_caches(fmt: str, sequences: int) -> list[DecoderCache]:
+    """The caches of the decoder's layers in a 4-bit cache format (q4_0 or q4_1), in layer order, self before cross.  A
+    page is the positions or frames rounded up to whole units of 32 tokens."""
+    f = _check(fmt)
+    if f not in ("q4_0", "q4_1"):
+        raise ValueError(f"a cache is q4_0 or q4_1, not {fmt!r}")
+    if sequences < 1:
+        raise ValueError(f"{sequences} sequences")
+    out = []
+    for l in range(DEC_LAYERS):
+        for kind, tokens in (("self", DEC_POSITIONS), ("cross", ENC_POSITIONS)):
+            page = -(-tokens // 32) * 32
+            out.append(DecoderCache(l, kind, wq.cache_desc(f, HEAD_DIM, HEADS, page, sequences), kind == "self"))
     return out

@@ -276,7 +276,7 @@ wq_status wq_matmul_w4a4(const wq_desc* d, int64_t m, const void* xcodes, const 
  *   head_dim : 64, 96, 128 or 256 (else WQ_ERR_UNSUPPORTED)
  *   kv_heads : 1 .. 65535
  *   page     : tokens per page, a multiple of 32, at most 2^24
- *   pages    : 1 .. 2^31 - 1; the whole cache is at most 2^46 bytes */
+ *   pages    : 1 .. 2^31 - 1; the whole cache is at most 2^41 bytes */
 typedef struct {
     int32_t format;
     int32_t head_dim;
@@ -347,7 +347,7 @@ wq_status wq_attn_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32
  *             i / (q_heads / kv_heads)
  *   q       : bf16 [rows, q_heads * head_dim], 16-byte aligned, ldq % 8 == 0,
  *             q_heads * head_dim <= ldq <= 2^31 - 1
- *   scale   : finite factor of the scores
+ *   scale   : finite factor of the scores, at most 2^127 in magnitude
  *   causal  : 1: the row at token p sees the tokens 0 .. p; 0: every row sees all len[b]
  *             tokens (cross-attention: the rows are then no tokens of the cache)
  *   window  : with causal, > 0: the row sees only its last `window` tokens (itself among

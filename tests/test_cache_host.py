@@ -6,7 +6,7 @@ import subprocess
 import numpy as np
 import pytest
 
-from block_quantized_bit_amd import build, wq
+from block_quantized_bit_amd import build, policy, wq
 
 FAKE = 1 << 20
 Q4_0, Q4_1 = wq.WQ_Q4_0, wq.WQ_Q4_1
@@ -36,7 +36,7 @@ BAD_DESCS = [(dict(format=0), 1), (dict(format=9), 1), (dict(format=wq.WQ_NF4), 
              (dict(head_dim=32), 2), (dict(head_dim=80), 2), (dict(head_dim=512), 2), (dict(kv_heads=0), 3),
              (dict(kv_heads=65536), 3), (dict(page=0), 3), (dict(page=16), 3), (dict(page=33), 3), (dict(page=-32), 3),
              (dict(page=(1 << 24) + 32), 3), (dict(pages=0), 3), (dict(pages=1 << 31), 3),
-             (dict(pages=(1 << 31) - 1, page=4096), 3), (dict(reserved=1), 1)]
+             (dict(pages=(1 << 31) - 1, page=4096), 3), (dict(kv_heads=8192, page=1 << 24, pages=1), 3), (dict(reserved=1), 1)]
 BAD_SEQS = [(dict(batch=-1), 3), (dict(batch=(1 << 20) + 1, row_start=FAKE), 3), (dict(rows=-1), 3), (dict(rows=3), 3),
             (dict(len=None), 1), (dict(len=FAKE + 2), 4), (dict(table=FAKE + 1), 4), (dict(row_start=FAKE + 3), 4),
             (dict(table_ld=0), 1), (dict(table_ld=-1), 1), (dict(table=None), 1), (dict(table_ld=1 << 25), 3),
@@ -90,7 +90,7 @@ def test_attention_refusals():
     assert at(q=None) == 1 and at(y=None) == 1 and at(cache=None) == 1
     assert at(q=FAKE + 2) == 4 and at(y=FAKE + 8) == 4 and at(cache=FAKE + 8) == 4
     assert at(ldq=4088) == 1 and at(ldy=4100) == 1 and at(ldq=1 << 31) == 1
-    assert at(scale=float("nan")) == 1 and at(scale=float("inf")) == 1
+    assert at(scale=float("nan")) == 1 and at(scale=float("inf")) == 1 and at(scale=-3e38) == 1
     assert at(causal=2) == 1 and at(causal=-1) == 1
     assert at(window=-1) == 1 and at(causal=0, window=5) == 1
     assert at(ws=FAKE + 8, wsb=1 << 40) == 4
@@ -126,6 +126,43 @@ def test_binding_refuses_other_tensors():
         wq.seqs(4, 4, FAKE, table=torch.zeros((3, 5), dtype=torch.int32))
     with pytest.raises(ValueError, match="contiguous"):
         wq.seqs(4, 4, FAKE, table=torch.zeros((5, 4), dtype=torch.int32).t())
+
+
+class _Tensor:
+    """A stand-in for a device tensor: an address on a device."""
+    is_cuda, dtype = True, "torch.int32"
+
+    def __init__(self, device):
+        self.device_index = device
+
+    def get_device(self):
+        return self.device_index
+
+    def data_ptr(self):
+        return FAKE
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 100
+
+    def dim(self):
+        return 2
+
+    shape = (4, 10)
+
+
+def test_binding_refuses_tensors_of_two_devices():
+    with pytest.raises(ValueError, match="devices 0 and 1"):
+        wq.seqs(4, 4, _Tensor(0), _Tensor(1))
+    s = wq.seqs(4, 0, _Tensor(1), _Tensor(1), _Tensor(1))
+    assert s.device == 1
+    for a, b in ((0, 0), (1, 0)):
+        with pytest.raises(ValueError, match="device"):
+            wq.wq_cache_write(_desc(), s, _Tensor(a), 1024, _Tensor(b), 1024, wq.WQ_BF16, _Tensor(a), stream=0)
+        with pytest.raises(ValueError, match="device"):
+            wq.wq_attn(_desc(), s, 32, _Tensor(a), 4096, _Tensor(b), 0.1, 1, 0, _Tensor(b), 4096, stream=0)
 
 
 @pytest.fixture(scope="module")
@@ -231,3 +268,20 @@ def test_bad_pages_and_lengths(layout):
     assert layout.unit(None, 1, 64, 5, 4, 1000, 4, 0, 5) == -1
     big = layout.unit(_p(_i32(2**31 - 2)), 1, 64, 5, 2**31 - 1, 9216, 0, 4, 63)   # far past 32 bits
     assert big == (((2**31 - 2) * 5 + 4) * 2 + 1) * 9216
+
+
+def test_decoder_caches():
+    """One self- and one cross-attention cache per decoder layer, pages of whole units that hold the positions and frames."""
+    for fmt, bits in (("q4_0", 9), ("Q4_1", 10)):
+        caches = policy.decoder_caches(fmt, 3)
+        assert [(c.layer, c.kind) for c in caches] == [(l, k) for l in range(4) for k in ("self", "cross")]
+        for c in caches:
+            tokens = 448 if c.kind == "self" else 1504
+            assert (c.desc.page, c.desc.pages, c.causal) == (tokens, 3, c.kind == "self")
+            assert c.desc.kv_heads * c.desc.head_dim == policy.D_MODEL
+            assert wq.wq_cache_size(c.desc) == 3 * tokens * 1280 * bits // 8
+    for bad in ("nf4", "q8_0", "bf16"):
+        with pytest.raises(ValueError, match="q4_0 or q4_1"):
+            policy.decoder_caches(bad, 1)
+    with pytest.raises(ValueError):
+        policy.decoder_caches("q4_0", 0)

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_quantized_bit_amd import wq
+from block_quantized_bit_amd import policy, wq
 from block_quantized_bit_amd.inputs import bf16_bits_to_f32, f32_to_bf16_bits
 
 from cache_helpers import Q4_0, Q4_1, Case, attend, check_attn, run_attn
@@ -308,6 +308,70 @@ def test_another_stream_and_graph_replays(orc):
     assert c.lens == full
 
 
+@pytest.mark.parametrize("counts,lens", [([1, 1], [3000, 900]), ([40, 3], [2600, 3]), ([150, 2], [2600, 900])],
+                         ids=["shared out", "rows", "many rows"])
+def test_graph_replays_of_split_calls(orc, counts, lens):
+    """Calls that take a workspace and a second launch, captured and replayed with other lengths and a workspace that holds
+    the last replay's parts: every replay equals the eager call."""
+    c = Case(Q4_0, 128, 1, 64, counts, lens, seed=30, one_row=max(counts) == 1)
+    k, v = c.random_kv()
+    c.fill(k, v)
+    hq = 2
+    q = _q(c, hq)
+    Q = dev_bf16(q.reshape(c.rows, -1))
+    Y = torch.empty_like(Q)
+    n = wq.wq_attn_workspace_size(c.desc, c.seqs, hq)
+    assert n > 0
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)          # NaN in every float
+
+    def step():
+        wq.wq_attn(c.desc, c.seqs, hq, Q, hq * 128, c.cache, 0.1, 1, 0, Y, hq * 128, ws, n)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for cut in (0, 1, 700, 32, 0):
+        c.d_len.copy_(torch.tensor([max(t - cut, 0) for t in lens], dtype=torch.int32))
+        Y.fill_(0x7FC0)
+        g.replay()
+        torch.cuda.synchronize()
+        got = Y.clone()
+        ws.fill_(0xFF)
+        Y.fill_(0x7FC0)
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got, Y), f"lengths cut by {cut}"
+    c.lens = lens
+    ref, ab, A = attend(c, orc, k, v, bf16_bits_to_f32(q), hq, 0.1, 1, 0)
+    check_attn(bf16_bits_to_f32(Y.cpu().numpy().view(np.uint16)).reshape(ref.shape), ref, ab, A, "last replay")
+
+
+def test_calls_on_two_streams(orc):
+    """Two calls at the same time on two streams, each with its workspace, on one cache."""
+    c = Case(Q4_1, 64, 4, 64, [1, 1, 1], [5000, 77, 2500], seed=31, one_row=True)
+    k, v = c.random_kv()
+    c.fill(k, v)
+    qs = [_q(c, 2) for _ in range(2)]
+    want = [run_attn(c, q, 2, 0.125, 1, 0)[1] for q in qs]
+    n = wq.wq_attn_workspace_size(c.desc, c.seqs, 8)
+    assert n > 0
+    Q = [dev_bf16(q.reshape(3, -1)) for q in qs]
+    Y = [torch.zeros_like(x) for x in Q]
+    W = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            wq.wq_attn(c.desc, c.seqs, 8, Q[i], 512, c.cache, 0.125, 1, 0, Y[i], 512, W[i], n, stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert np.array_equal(Y[i].cpu().numpy().view(np.uint16).reshape(want[i].shape), want[i])
+
+
 @pytest.mark.parametrize("fmt", ["q4_0", "q4_1"])
 def test_a_decoder_layer(orc, fmt):
     """The fused projection's K and V rows into the cache, attention over it, the output projection: a prompt of 5 tokens,
@@ -320,6 +384,8 @@ def test_a_decoder_layer(orc, fmt):
     do, co, so = gpu_quantize(wq.WQ_Q4_0, wo)
     wo_hat = orc.quantize(wq.WQ_Q4_0, wo)["w_hat"]
     c = Case(Q4_0 if fmt == "q4_0" else Q4_1, dim, heads, 448, [1], [12], paged=False, seed=1)
+    planned = policy.decoder_caches(fmt, 1)[0].desc
+    assert bytes(planned) == bytes(c.desc)                       # the model's own self-attention cache
     lens = torch.zeros(1, dtype=torch.int32, device=DEV)
     keys, values = [], []
     for first, n in [(0, 5)] + [(i, 1) for i in range(5, 12)]:
