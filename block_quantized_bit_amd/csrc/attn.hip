@@ -109,7 +109,10 @@ __device__ inline void unit_step(const uint8_t* unit, const bf16x8 (&qf)[NB], co
             u32x4 u;
 #pragma unroll
             for (int i = 0; i < 4; i++) u[i] = nibble_pair(w, i, bf128);
-            const f32x4 c = {c0[b], c0[b], c0[b], c0[b]};
+            // (wide heads: four copies of each start would be held in registers across the loop)
+            float start = c0[b];
+            if (NB > 4) asm("" : "+v"(start));
+            const f32x4 c = {start, start, start, start};
             const f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, u), qf[b], c, 0, 0, 0);
             const f16x2 d01 = as_f16x2(kd[b][0]), d23 = as_f16x2(kd[b][1]);
             s[0] = fmaf((float)d01[0], p[0], s[0]);
@@ -971,8 +974,8 @@ Schedule schedule(const AttnArgs& a, bool share) {
         items(kTokenCols);
         // Shared out, and joined by a second launch, where a sequence can be long.  Measured in us, whole and shared out,
         // 8 heads of 128: 8 tiles of 1024 tokens 11.2 and 17.0, of 2048 tokens 18 and 17.1; 256 tiles of 2048 24.8 and
-        // 30.2, of 4096 42.9 and 42.6 (equal lengths: unequal ones only gain).  Work is counted in 32 bits.
-        if (share && units > (s.items < 256 ? 64 : 96) && s.items * (units + kTileCost) <= 0x7FFFFFFF)
+        // 30.2, of 4096 42.9 and 42.6, 288 tiles of 4096 42.9 and 48.9 (equal lengths: unequal ones only gain).  Work is counted in 32 bits.
+        if (share && units > (s.items < 256 ? 64 : 128) && s.items * (units + kTileCost) <= 0x7FFFFFFF)
             s.workgroups = kShareWorkgroups;
     }
     return s;
