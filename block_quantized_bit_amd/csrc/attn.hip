@@ -1,4 +1,9 @@
 // attn.hip -- attention over the 4-bit cache: y = sum_t softmax_t(scale q . k^_t) v^_t over the tokens a row sees.
+//
+// One pass over the tokens: with x_t the scores times log2(e), a column holds a reference ref, l = sum 2^(x_t - ref) and
+// o = sum 2^(x_t - ref) v^_t in fp32; where a score passes ref by too much, o and l are scaled to a new one.  Parts of a
+// column (waves, workgroups) are joined by y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  Nothing of the size
+// rows x tokens is written, and keys and values are read packed.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -11,6 +16,15 @@ namespace wq {
 // Few columns per sequence (single tokens, drafted tokens): tiles of 16 columns, every wave its own units.
 // ---------------------------------------------------------------------------------------------------------------
 
+// What bounds it: with one row per sequence a group's heads share every unit that is read, at 2 x 16 columns of products
+// per 4.5 or 5 bits, so a call with enough tokens is bound by memory, and a short one by the way to memory and back
+// (lengths, pages, units, one after the other).  Measured (a copy runs at 5.1 TB/s on the card): 32 sequences
+// of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0 (1.16 GB) 228 us with the join, 5.1 TB/s; one of 131077 tokens, 8 x 8
+// heads (151 MB) 42 us; 16 of 1500 tokens, 20 heads of 64 (35 MB) 16 us; one of 224 tokens 5.8 us; 16 x 5 rows that see 4096
+// tokens, 2 x 8 heads of 256, q4_1 (43 MB) 47 us, where three tiles take each unit and their conversions bound it.
+// 16 columns, since a group's heads of one token are seldom more; with 32 columns a wave spills, and was slower in all of
+// these.
+//
 // Each wave keeps a ring of units in LDS, filled by loads that go there directly (no registers), so that several units
 // per wave are on their way while one is computed on.  The unit is contiguous in the cache and keeps its layout.
 template <int NB, bool Q41>
@@ -371,8 +385,9 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
 }
 
 // Sequences shared out evenly: workgroup i takes units [i share, (i + 1) share) of the call's work, whatever the lengths
-// are; a tile that more than one workgroup has a part of is joined by k_attn_join.  With `splits` 0 every workgroup has
-// one whole tile.
+// are; a tile that more than one workgroup has a part of is joined by k_attn_join_token.  With `workgroups` 0 every
+// workgroup has one whole tile.  (61 sequences of 1 to 8191 tokens, 8 x 4 heads of 128, q4_1: 74 us and 8 for the join,
+// 3.9 TB/s; 102 us where what beginning a tile costs is not counted.)
 template <int NB, bool Q41, int NW, int D>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_token(AttnArgs a) {
     constexpr int ring_bytes = NW * D * UnitRing<NB, Q41>::bytes, join_bytes = NW * 16 * (32 * NB + 4 + 2) * 4;
@@ -419,7 +434,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
                 const int slot = 2 * blockIdx.x + (s0 > 0 ? 0 : 1);
                 po = p.sums(slot, 0);
                 pm = p.stat(slot, 0);
-                if (s0 == 0) open = {(int)((w + span - 1) / sh.share - blockIdx.x) + 1, tile, h, q.r0, q.n};
+                // (the rows' starts are the caller's: whatever they hold, the parts are workgroups)
+                if (s0 == 0) open = {(int)(min((w + span - 1) / sh.share, gridDim.x - 1) - blockIdx.x) + 1, tile, h, q.r0, q.n};
             }
             token_segment<NB, Q41, NW, D>(a, ts, q, seq, tile, h, u0 + max(0, s0 - kTileCost), u0 + max(0, s1 - kTileCost), po, pm, lds);
             w += s1 - s0;
@@ -431,7 +447,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
 }
 
 // Joins the parts of a tile's column: y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  Every thread sums four
-// channels of some of the parts; their sums meet in LDS, in order.
+// channels of some of the parts; their sums meet in LDS, in order.  Bound by the way to memory: 5.6 us for 64 columns of 64
+// parts of 128 channels, 8.2 us for 512 open tiles.
 constexpr int kJoinParts = 512;
 struct JoinLds {
     float f[kJoinParts], red[4], sum[1024];
@@ -629,6 +646,12 @@ __device__ inline void store_pair(const Pair<Q41>& r, const PairPlace& at, uint3
 // step; the codes of the step after are on their way meanwhile.  A wave's products and its vector arithmetic are
 // independent of each other, so that the matrix unit works beside the vector unit: the scores of unit i + 1 beside the
 // exponentials of unit i, the sums over unit i's values beside the maximum of unit i + 1 and the conversions to fp16.
+//
+// Bound by the vector unit beside the matrix unit: 2048 rows of 8 x 4 heads of 128 over 18432 tokens (584 GFLOP) 612 us,
+// 955 TFLOP/s, where a large fp16 matrix product reaches 1405.  The products alone take 418 us; the conversions and
+// their loads the rest, which is why 256 columns share each of them.  64 columns per wave would halve them again, but the
+// accumulators then leave no registers (spills, and moves to and from the accumulation registers every step: slower); a ring
+// of 4 buffers, or two units per step with 128 columns of heads of 128, gained nothing.
 template <int NB, bool Q41, int NW, int KS>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows(AttnArgs a) {
     constexpr int dim = 32 * NB, unit_lds = 64 * dim, buffer = 2 * KS * unit_lds;   // fp16 bytes of a unit's K, or V; a step
@@ -644,6 +667,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     at = uniform(at / heads);
     const int split = uniform(at % a.splits);
     at = uniform(at / a.splits);
+    const int item = at * heads + h;        // of the parts' places: below the grid's bound whatever row_start holds
     uint32_t before;
     const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
     if (seq < 0) return;
@@ -891,7 +915,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     if (!valid) return;
     if (a.splits > 1) {
         const Partials p(a);
-        const int slot = (((int)before + tile) * heads + h) * a.splits + split, col = wave * 32 + (lane & 31);
+        const int slot = item * a.splits + split, col = wave * 32 + (lane & 31);
         float* const po = p.sums(slot, col);
 #pragma unroll
         for (int b = 0; b < NB; b++)
@@ -924,7 +948,7 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
     const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
     if (seq < 0) return;
     const SeqInfo q = seq_info_uniform(a, seq);
-    const int tile = at - before;
+    const int tile = tiles_of(ts, q.n) - 1 - (at - (int)before);
     const Partials p(a);
     const auto slot = [&](int i) { return (int)blockIdx.x * a.splits + i; };
     for (int col = blockIdx.y; col < a.tile_cols; col += gridDim.y) {
@@ -993,6 +1017,12 @@ void launch_rows(const AttnArgs& a, dim3 grid, hipStream_t s) {
 }
 
 }  // namespace
+
+// A launch has fewer than 2^32 threads.
+bool attn_fits(const AttnArgs& a) {
+    const Schedule s = schedule(a, true);
+    return s.items * s.splits < (int64_t(1) << 23);
+}
 
 size_t attn_workspace_bytes(const AttnArgs& a) {
     const Schedule s = schedule(a, true);

@@ -244,6 +244,7 @@ wq_status check_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, 
     a->q_heads = q_heads;
     a->group = q_heads / d->kv_heads;
     a->dim = d->head_dim;
+    if (a->s.rows > 0 && a->s.batch > 0 && !wq::attn_fits(*a)) return WQ_ERR_SHAPE;
     return WQ_OK;
 }
 

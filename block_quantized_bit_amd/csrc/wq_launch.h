@@ -95,6 +95,7 @@ struct AttnArgs {
     int32_t slots;         // partial results that the workspace holds
     bool q41, causal;
 };
+bool attn_fits(const AttnArgs& a);
 size_t attn_workspace_bytes(const AttnArgs& a);
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 

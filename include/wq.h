@@ -354,6 +354,9 @@ wq_status wq_attn_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32
  *             them); 0: no limit
  *   y       : bf16 [rows, q_heads * head_dim], as q with ldy; must not overlap q
  *   ws      : workspace (16-byte aligned, see wq_attn_workspace_size) or NULL
+ * rows * q_heads is at most 2^31 - 1, and the call has fewer than 2^23 tiles (else
+ * WQ_ERR_SHAPE): a tile is one key/value head with 16 pairs (128 or 256 in calls with more
+ * than 128 per sequence) of a row and a query head of one sequence.
  * A row that sees no token gets zeros.  Scores, the softmax's maximum and sum and the
  * sums over tokens are fp32; probabilities, values and (in calls with many rows) keys are
  * rounded to fp16 for the matrix products.  Per element |y - y_ref| <=

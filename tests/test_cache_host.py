@@ -111,6 +111,18 @@ def test_workspace_refusal():
         assert _status(wq.wq_attn, d, s, 32, FAKE, 4096, FAKE, 0.1, 1, 0, FAKE, 4096, FAKE, need - 1, 0) == 6
 
 
+def test_more_tiles_than_a_launch_has():
+    size = lambda d, s, hq: _status(wq.wq_attn_workspace_size, d, s, hq)  # noqa: E731
+    d = _desc(head_dim=64, kv_heads=128)                  # one tile per sequence and head
+    for batch, want in (((1 << 16) - 1, 0), (1 << 16, 3)):
+        s = _seqs(batch=batch, rows=batch)
+        assert size(d, s, 128) == want and size(d, s, 128 * 16) == want
+        if want:
+            assert _status(wq.wq_attn, d, s, 128, FAKE, 8192, FAKE, 0.1, 1, 0, FAKE, 8192, None, 0, 0) == 3
+    s = _seqs(batch=1 << 15, rows=1 << 15)
+    assert size(d, s, 128 * 16) == 0 and size(d, s, 128 * 17) == 3   # two tiles
+
+
 def test_binding_refuses_other_tensors():
     import torch
     n = torch.zeros(4, dtype=torch.int32)

@@ -183,6 +183,23 @@ def test_nan_stays_in_its_row(orc, rows):
     assert np.array_equal(got[keep], clean[keep])
 
 
+def test_rows_claimed_twice_stay_in_the_workspace(orc):
+    """Starts that do not ascend, so that two sequences claim the same rows: the outputs are not specified, but the parts
+    of a split call stay inside the workspace and the rows that no sequence has are left as they were."""
+    c = Case(Q4_0, 64, 1, 64, [160, 0, 160], [2000, 0, 1900], seed=33, pad_rows=5)
+    c.fill(*c.random_kv())
+    c.d_start.copy_(torch.tensor([0, 160, 0, 160], dtype=torch.int32))
+    s = wq.seqs(3, 165, c.d_len, c.d_table, row_start=c.d_start)
+    need = wq.wq_attn_workspace_size(c.desc, s, 4)
+    assert need > 0
+    ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
+    q = torch.ones((165, 256), dtype=torch.bfloat16, device=DEV)
+    y = torch.full((165, 256), 0x7BAD, dtype=torch.int16, device=DEV)
+    wq.wq_attn(c.desc, s, 4, q, 256, c.cache, 0.125, 1, 0, y, 256, ws, need)
+    torch.cuda.synchronize()
+    assert bool((ws[need:] == 0x5A).all()) and bool((y[160:] == 0x7BAD).all())
+
+
 def test_shared_pages(orc):
     """Two sequences that share their first pages read the same keys and values."""
     c = Case(Q4_0, 128, 2, 32, [1, 1], [96, 96], seed=12, one_row=True)
