@@ -165,11 +165,11 @@ __device__ inline T load_at(global_bytes p, uint32_t offset) {
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// (w & mask) | bits in one instruction: with both as literals the compiler spends two (an instruction takes one literal).
+// (w & mask) | bits, in one instruction where neither is a literal to the compiler (an instruction takes one).  Not as
+// written assembly: the compiler counts no waiting states between a matrix instruction and that.
 __device__ inline uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
-    uint32_t r;
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(bits));
-    return r;
+    asm("" : "+s"(mask));
+    return (w & mask) | bits;
 }
 // A constant in a register.
 __device__ inline uint32_t held(uint32_t c) {

@@ -116,6 +116,17 @@ def test_long_sequences_shared_out(orc, fmt, dim):
     _check(orc, Case(fmt, dim, 1, 64, [100, 1, 90], [2001, 40, 90], seed=20), 3, 1, 500, what="long, more rows, window")
 
 
+@pytest.mark.parametrize("fmt,dim", [(Q4_0, 64), (Q4_1, 96), (Q4_0, 128), (Q4_1, 256)])
+def test_one_long_sequence_among_many(orc, fmt, dim):
+    """Tiles of one, a few and many parts in one call."""
+    lens = [20011, 5003, 1, 0, 2999, 1300] + [7 * i % 331 for i in range(64)]
+    say("one long", fmt, dim)
+    c = Case(fmt, dim, 1, 256, [1] * len(lens), lens, seed=21, one_row=True, pad_rows=1)
+    _check(orc, c, 5, 1, 0, what="one long")
+    c = Case(fmt, dim, 1, 256, [2, 1, 1, 0, 3, 1] + [1] * 64, lens, seed=22)
+    _check(orc, c, 3, 1, 2500, what="one long, window")
+
+
 def test_results_do_not_change(orc):
     """The same call gives the same bits, with any workspace content, and neighbours in the batch do not matter to
     rows of a call without a workspace."""
