@@ -19,9 +19,9 @@ namespace wq {
 // What bounds it: with one row per sequence a group's heads share every unit that is read, at 2 x 16 columns of products
 // per 4.5 or 5 bits, so a call with enough tokens is bound by memory, and a short one by the way to memory and back
 // (lengths, pages, units, one after the other).  Measured (a copy runs at 5.1 TB/s on the card): 32 sequences
-// of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0 (1.16 GB) 228 us with the join, 5.1 TB/s; one of 131077 tokens, 8 x 8
+// of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0 (1.16 GB) 226 us with the join, 5.1 TB/s; one of 131077 tokens, 8 x 8
 // heads (151 MB) 42 us; 16 of 1500 tokens, 20 heads of 64 (35 MB) 16 us; one of 224 tokens 5.8 us; 16 x 5 rows that see 4096
-// tokens, 2 x 8 heads of 256, q4_1 (43 MB) 47 us, where three tiles take each unit and their conversions bound it.
+// tokens, 2 x 8 heads of 256, q4_1 (43 MB) 44 us, where three tiles take each unit and their conversions bound it.
 // 16 columns, since a group's heads of one token are seldom more; with 32 columns a wave spills, and was slower in all of
 // these.
 //
@@ -388,8 +388,8 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
 
 // Sequences shared out evenly: workgroup i takes units [i share, (i + 1) share) of the call's work, whatever the lengths
 // are; a tile that more than one workgroup has a part of is joined by k_attn_join_token.  With `workgroups` 0 every
-// workgroup has one whole tile.  (61 sequences of 1 to 8191 tokens, 8 x 4 heads of 128, q4_1: 74 us and 8 for the join,
-// 3.9 TB/s; 102 us where what beginning a tile costs is not counted.)
+// workgroup has one whole tile.  (61 sequences of 1 to 8191 tokens, 8 x 4 heads of 128, q4_1: 74 us and 5 for the join,
+// 4.1 TB/s; 102 us where what beginning a tile costs is not counted.)
 template <int NB, bool Q41, int NW, int D>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_token(AttnArgs a) {
     constexpr int ring_bytes = NW * D * UnitRing<NB, Q41>::bytes, join_bytes = NW * 16 * (32 * NB + 4 + 2) * 4;
@@ -449,8 +449,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
 }
 
 // Joins the parts of a tile's column: y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  Every thread sums four
-// channels of some of the parts; their sums meet in LDS, in order.  Bound by the way to memory: 5.6 us for 64 columns of 64
-// parts of 128 channels, 8.2 us for 512 open tiles.
+// channels of some of the parts; their sums meet in LDS, in order.  Bound by the way to memory: 5.5 us for 64 columns of 64
+// parts of 128 channels.
 constexpr int kJoinParts = 512;
 struct JoinLds {
     float f[kJoinParts], red[4], sum[1024];
@@ -465,7 +465,7 @@ __device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, 
     for (int k = 0; k < ahead; k++) {
         const int i = gr + k * groups;
         early[k] = (f32x4){0, 0, 0, 0};
-        if (gr < groups && i < n) early[k] = *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
+        if (gr < groups && i < n) early[k] = p.read(slot(i), col, 4 * c);
     }
 #pragma unroll
     for (int k = 0; k < 2; k++) {
@@ -473,7 +473,7 @@ __device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, 
         m0[k] = -FLT_MAX;
         l0[k] = 0.0f;
         if (i < n) {
-            const float* st = p.stat(slot(i), col);
+            const f32x2 st = p.read_stat(slot(i), col);
             m0[k] = st[0];
             l0[k] = st[1];
         }
@@ -503,7 +503,7 @@ __device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, 
         for (int k = 0; k < ahead; k++)
             if (gr + k * groups < n) o += lds.f[gr + k * groups] * early[k];
 #pragma unroll 4
-        for (int i = gr + ahead * groups; i < n; i += groups) o += lds.f[i] * *reinterpret_cast<const f32x4*>(p.sums(slot(i), col) + 4 * c);
+        for (int i = gr + ahead * groups; i < n; i += groups) o += lds.f[i] * p.read(slot(i), col, 4 * c);
         *reinterpret_cast<f32x4*>(lds.sum + tid * 4) = o;
     }
     __syncthreads();
@@ -515,7 +515,55 @@ __device__ inline void join_column(const AttnArgs& a, const Partials& p, int n, 
     }
 }
 
-// Workgroup i: the tile, if there is one, that workgroup i of k_attn_token began and did not end.
+// The same by a wave, for few parts: no barriers, and a workgroup has four columns at a time (488 tiles of 4 columns, at most
+// three parts each: 5.1 us, by workgroups 8.4).
+constexpr int kWaveParts = 16;
+__device__ inline void join_column_wave(const AttnArgs& a, const Partials& p, int n, int col, uint16_t* y, int slot0) {
+    const int lane = threadIdx.x & 63, quads = a.dim / 4, groups = 64 / quads, gr = lane / quads, c = lane - gr * quads;
+    const auto slot = [&](int i) { return slot0 + 2 * i + (i == 0); };
+    const auto part = [&](int i) {
+        return gr < groups && i < n ? p.read(slot(i), col, 4 * c) : (f32x4){0, 0, 0, 0};
+    };
+    constexpr int ahead = 8;                  // parts requested before their factors are known
+    f32x4 early[ahead];
+#pragma unroll
+    for (int k = 0; k < ahead; k++) early[k] = part(gr + k * groups);
+    float m0 = -FLT_MAX, l = 0.0f;
+    if (lane < n) {
+        const f32x2 st = p.read_stat(slot(lane), col);
+        m0 = st[0];
+        l = st[1];
+    }
+    float ref = m0;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) ref = fmaxf(ref, __shfl_xor(ref, d, 64));
+    const float f = exp2_fast(m0 - ref);
+    l *= f;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) l += __shfl_xor(l, d, 64);
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < ahead; k++) {
+        const float fk = __shfl(f, (gr + k * groups) & 63, 64);
+        if (gr + k * groups < n) o += fk * early[k];
+    }
+    for (int i0 = ahead * groups; i0 < n; i0 += groups) {
+        const float fk = __shfl(f, (gr + i0) & 63, 64);
+        if (gr + i0 < n) o += fk * part(gr + i0);
+    }
+    f32x4 sum = o;
+    for (int k = 1; k < groups; k++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) sum[i] += __shfl(o[i], (lane + k * quads) & 63, 64);
+    if (lane < quads) {
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        *reinterpret_cast<u32x2*>(y + 4 * c) = (u32x2){pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv)};
+    }
+}
+
+// Workgroup i: the tile, if there is one, that workgroup i of k_attn_token began and did not end.  WAVES: tiles of few parts
+// by waves.  (A kernel of its own: with both ways in it, eight tiles of 64 parts took 6.5 us in place of 5.7.)
+template <bool WAVES>
 __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) JoinLds lds;
     const TileShape ts = tile_shape(kTokenCols, a.group);
@@ -525,10 +573,13 @@ __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
     const Partials p(a);
     // the first part is the one that starts the tile, the others start their workgroups
     const auto slot = [](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0); };
-    for (int col = blockIdx.y; col < kTokenCols; col += gridDim.y) {
+    const bool few = WAVES && t.parts <= kWaveParts;
+    for (int col = few ? blockIdx.y * 4 + uniform(threadIdx.x >> 6) : blockIdx.y; col < kTokenCols; col += (few ? 4 : 1) * gridDim.y) {
         int row, head;
         if (!tile_col(a, ts, t.tile, col, t.n, &row, &head)) break;   // columns without a query are the last ones
-        join_column(a, p, t.parts, col, a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim, slot, lds);
+        uint16_t* const y = a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim;
+        if (few) join_column_wave(a, p, t.parts, col, y, 2 * (int)blockIdx.x);
+        else join_column(a, p, t.parts, col, y, slot, lds);
     }
 }
 
@@ -1063,7 +1114,11 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     case 128: few ? launch_token<4, 8, 3>(a, grid, s) : launch_token<4, 4, 3>(a, grid, s); break;
     default: launch_token<8, 4, 2>(a, grid, s); break;
     }
-    if (c.workgroups) hipLaunchKernelGGL(k_attn_join_token, dim3(c.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);
+    // (with few tiles each has many parts, and a workgroup takes one column at a time, not four)
+    if (c.workgroups) {
+        if (c.items * 8 >= c.workgroups) hipLaunchKernelGGL(k_attn_join_token<true>, dim3(c.workgroups - 1, (cols + 3) / 4), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL(k_attn_join_token<false>, dim3(c.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);
+    }
     return hipGetLastError();
 }
 

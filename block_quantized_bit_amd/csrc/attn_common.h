@@ -17,6 +17,7 @@ namespace wq {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -215,6 +216,13 @@ struct Partials {
         : o(reinterpret_cast<float*>(a.ws)), ml(o + (int64_t)a.slots * a.tile_cols * a.dim), dim(a.dim), cols(a.tile_cols) {}
     __device__ float* sums(int slot, int col) const { return o + ((int64_t)slot * cols + col) * dim; }
     __device__ float* stat(int slot, int col) const { return ml + ((int64_t)slot * cols + col) * 2; }
+    // (at most 1024 slots of 16 columns, or 256 of 128, of 256 channels: offsets fit 32 bits)
+    __device__ f32x4 read(int slot, int col, int ch) const {
+        return load_at<f32x4>((global_bytes)(uintptr_t)o, (uint32_t)(((slot * cols + col) * dim + ch) * 4));
+    }
+    __device__ f32x2 read_stat(int slot, int col) const {
+        return load_at<f32x2>((global_bytes)(uintptr_t)ml, (uint32_t)((slot * cols + col) * 8));
+    }
 };
 __host__ __device__ inline int64_t partial_bytes(int slots, int cols, int dim) { return (int64_t)slots * cols * (dim + 2) * 4; }
 
