@@ -116,7 +116,8 @@ def test_long_sequences_shared_out(orc, fmt, dim):
     _check(orc, Case(fmt, dim, 1, 64, [100, 1, 90], [2001, 40, 90], seed=20), 3, 1, 500, what="long, more rows, window")
 
 
-@pytest.mark.parametrize("fmt,dim", [(Q4_0, 64), (Q4_1, 96), (Q4_0, 128), (Q4_1, 256)])
+@pytest.mark.parametrize("fmt", FMT, ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
 def test_one_long_sequence_among_many(orc, fmt, dim):
     """Tiles of one, a few and many parts in one call."""
     lens = [20011, 5003, 1, 0, 2999, 1300] + [7 * i % 331 for i in range(64)]
@@ -125,6 +126,26 @@ def test_one_long_sequence_among_many(orc, fmt, dim):
     _check(orc, c, 5, 1, 0, what="one long")
     c = Case(fmt, dim, 1, 256, [2, 1, 1, 0, 3, 1] + [1] * 64, lens, seed=22)
     _check(orc, c, 3, 1, 2500, what="one long, window")
+
+
+@pytest.mark.parametrize("fmt", FMT, ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_more_tiles_than_compute_units(orc, fmt, dim):
+    lens = [37 * i % 401 for i in range(150)]
+    say("many tiles", fmt, dim)
+    c = Case(fmt, dim, 2, 96, [1] * len(lens), lens, seed=23, one_row=True, pad_rows=2)
+    _check(orc, c, 3, 1, 0, ws=("asked",), what="many tiles")
+
+
+@pytest.mark.parametrize("fmt", FMT, ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_many_rows_split(orc, fmt, dim):
+    """Tiles of 128 columns whose tokens are shared out: the last part ends anywhere in a unit."""
+    for tokens in (3001, 2990):
+        say("rows split", fmt, dim, tokens)
+        c = Case(fmt, dim, 1, 64, [70, 3], [tokens, 50], seed=24)
+        assert wq.wq_attn_workspace_size(c.desc, c.seqs, 4) > 0
+        _check(orc, c, 4, 1, 0, ws=("asked",), what="rows split")
 
 
 def test_results_do_not_change(orc):
