@@ -369,14 +369,16 @@ __global__ __launch_bounds__(256) void k_cache_read(Seqs s, int per_row, int gro
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         if (i < q.first || i >= q.end) continue;
+        // no token: codes and scales that give +0
         const bool none = at < 0 || q.token + i < 0;
+        const uint32_t codes = none ? 0x88888888u : w[i], lo = codes & 0x0F0F0F0Fu, hi = (codes >> 4) & 0x0F0F0F0Fu;
+        const float delta = none ? 0.0f : f16_value(d[i]), mu = none ? 0.0f : f16_value(m[i]);
         float x[8];
 #pragma unroll
         for (int n = 0; n < 8; n++) {
-            const float c = (float)((w[i] >> (4 * n)) & 15u);
-            if constexpr (Q41) x[n] = c * f16_value(d[i]) + f16_value(m[i]);
-            else x[n] = (c - 8.0f) * f16_value(d[i]);
-            if (none) x[n] = 0.0f;
+            const float c = (float)(((n & 1 ? hi : lo) >> (8 * (n >> 1))) & 0xFFu);
+            if constexpr (Q41) x[n] = fmaf(c, delta, mu);   // (c d is exact: one rounding either way)
+            else x[n] = (c - 8.0f) * delta;
         }
         store8<F32>(dst, (q.row + i) * ld + q.h * dim + q.b * 32 + q.g * 8, x);
     }
