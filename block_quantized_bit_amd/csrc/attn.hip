@@ -102,11 +102,14 @@ struct ColState {
     float ref, l;        // l: this lane's tokens only
 };
 
-// K codes are multiplied as the bf16 integers 128 + q, exact, with the sum's start at -(128 + 8) sum q (q4_0; -128 sum q
-// for q4_1), so that a block's product is the exact-code sum in fp32, and its fp16 scale is applied after it.
+// What K is multiplied as: q4_0's codes less 8, which fp16 holds exactly, with a block's scale applied to its product in fp32;
+// q4_1's values d q + m, rounded to fp16 once.  Either way a product's terms are the keys' own, so its fp32 error follows
+// sum |q k^|.  (Terms that only cancel, codes from 128 on against a start of -136 sum q, or m sum q beside q4_1's codes, leave
+// errors of the size of the block's scale times sum |q|: a key of 32768 beside a query of nearly zero moved scores of 0.6 by
+// 0.1.  They were no faster: 32 sequences of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0, 223-227 us that way, 227-228 us.)
 template <int NB, bool Q41, bool MASKED>
-__device__ inline void unit_step(const uint8_t* unit, const bf16x8 (&qf)[NB], const float (&c0)[NB], float sl2, int t0, int lo,
-                                 int hi, int tokens, uint32_t bf128, ColState<NB>* st) {
+__device__ inline void unit_step(const uint8_t* unit, const f16x8 (&qf)[NB], float sl2, int t0, int lo, int hi, int tokens,
+                                 uint32_t f1024, f16x2 s16, ColState<NB>* st) {
     using R = UnitRing<NB, Q41>;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     float x[8];
@@ -115,33 +118,34 @@ __device__ inline void unit_step(const uint8_t* unit, const bf16x8 (&qf)[NB], co
 #pragma unroll
     for (int tile = 0; tile < 2; tile++) {
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t kd[NB][2], km[NB][2];
         if (NB > 4 && tile) asm volatile("" ::: "memory");
-        read_scales<NB, NB>(unit + 16 * R::dim, g, tile, 0, kd);
-        if constexpr (Q41) read_scales<NB, NB>(unit + 16 * R::dim + R::plane, g, tile, 0, km);
+        if constexpr (Q41) {
+            // (the lane's words are one token's: 4 (r / 4) + r % 4 of the tile)
+            const uint8_t* const sc = unit + 16 * R::dim + ((tile * 4 + ((lane & 15) >> 2)) * NB) * 8 + (lane & 3) * 2;
 #pragma unroll
-        for (int b = 0; b < NB; b++) {
-            const uint32_t w = kw[tile * NB + b];
-            u32x4 u;
+            for (int b = 0; b < NB; b++) {
+                const _Float16 d1 = *reinterpret_cast<const _Float16*>(sc + b * 8), m1 = *reinterpret_cast<const _Float16*>(sc + b * 8 + R::plane);
+                const f16x2 d = {d1, d1}, m = {m1, m1};
+                u32x4 u;
 #pragma unroll
-            for (int i = 0; i < 4; i++) u[i] = nibble_pair(w, i, bf128);
-            // (wide heads: four copies of each start would be held in registers across the loop)
-            float start = c0[b];
-            if (NB > 4) asm("" : "+v"(start));
-            const f32x4 c = {start, start, start, start};
-            const f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, u), qf[b], c, 0, 0, 0);
-            const f16x2 d01 = as_f16x2(kd[b][0]), d23 = as_f16x2(kd[b][1]);
-            s[0] = fmaf((float)d01[0], p[0], s[0]);
-            s[1] = fmaf((float)d01[1], p[1], s[1]);
-            s[2] = fmaf((float)d23[0], p[2], s[2]);
-            s[3] = fmaf((float)d23[1], p[3], s[3]);
-            if constexpr (Q41) {
-                const f16x2 m01 = as_f16x2(km[b][0]), m23 = as_f16x2(km[b][1]);
-                const float sx = c0[b] * -0.0078125f;   // sum q over the block
-                s[0] = fmaf((float)m01[0], sx, s[0]);
-                s[1] = fmaf((float)m01[1], sx, s[1]);
-                s[2] = fmaf((float)m23[0], sx, s[2]);
-                s[3] = fmaf((float)m23[1], sx, s[3]);
+                for (int i = 0; i < 4; i++)
+                    u[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(code_pair<0>(kw[tile * NB + b], i, f1024, s16), d, m));
+                s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, u), qf[b], s, 0, 0, 0);
+            }
+        } else {
+            uint32_t kd[NB][2];
+            read_scales<NB, NB>(unit + 16 * R::dim, g, tile, 0, kd);
+#pragma unroll
+            for (int b = 0; b < NB; b++) {
+                u32x4 u;
+#pragma unroll
+                for (int i = 0; i < 4; i++) u[i] = __builtin_bit_cast(uint32_t, code_pair<8>(kw[tile * NB + b], i, f1024, s16));
+                const f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, u), qf[b], (f32x4){0, 0, 0, 0}, 0, 0, 0);
+                const f16x2 d01 = as_f16x2(kd[b][0]), d23 = as_f16x2(kd[b][1]);
+                s[0] = fmaf((float)d01[0], p[0], s[0]);
+                s[1] = fmaf((float)d01[1], p[1], s[1]);
+                s[2] = fmaf((float)d23[0], p[2], s[2]);
+                s[3] = fmaf((float)d23[1], p[3], s[3]);
             }
         }
 #pragma unroll
@@ -198,15 +202,20 @@ __device__ inline void unit_step(const uint8_t* unit, const bf16x8 (&qf)[NB], co
             u32x4 vlo, vhi;
 #pragma unroll
             for (int tile = 0; tile < 2; tile++) {
-                const uint32_t w = vw[2 * b + tile], wl = w & 0x0F0F0F0Fu, wh = (w >> 4) & 0x0F0F0F0Fu;
+                const uint32_t w = vw[2 * b + tile], wl = w & 0x0F0F0F0Fu, wh = w & 0xF0F0F0F0u;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     const uint32_t in = MASKED ? keep[2 * tile + i] : ~0u;
                     const f16x2 d = as_f16x2(vd[tile][b][i] & in);
-                    f16x2 m = {};
-                    if constexpr (Q41) m = as_f16x2(vm[tile][b][i] & in);
-                    vlo[2 * tile + i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wl, i), d, m));
-                    vhi[2 * tile + i] = __builtin_bit_cast(uint32_t, code_value<Q41>(byte_pair(wh, i), d, m));
+                    const f16x2 cl = byte_pair(wl, i) - (_Float16)(Q41 ? 1024.0f : 1032.0f), ch = sixteenth<Q41 ? 0 : 8>(byte_pair(wh, i), s16);
+                    f16x2 lo2 = cl * d, hi2 = ch * d;
+                    if constexpr (Q41) {
+                        const f16x2 m = as_f16x2(vm[tile][b][i] & in);
+                        lo2 = __builtin_elementwise_fma(cl, d, m);
+                        hi2 = __builtin_elementwise_fma(ch, d, m);
+                    }
+                    vlo[2 * tile + i] = __builtin_bit_cast(uint32_t, lo2);
+                    vhi[2 * tile + i] = __builtin_bit_cast(uint32_t, hi2);
                 }
             }
             f32x4* const o = st->o + 2 * (b0 + b);
@@ -298,29 +307,26 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
 #pragma unroll
     for (int i = 0; i < D - 1; i++)
         if (i < n) request(i);
-    bf16x8 qf[NB];
+    u32x4 qv[NB];
     const uint16_t* qp = a.q + (int64_t)(q.r0 + row) * a.ldq + (int64_t)(h * a.group + head) * dim + 8 * g;
 #pragma unroll
     for (int b = 0; b < NB; b++) {
-        u32x4 v = {};
-        if (valid) v = *reinterpret_cast<const u32x4*>(qp + 32 * b);
-        // to the order of a K word's nibble pairs: 0, 4, 1, 5, 2, 6, 3, 7
-        u32x4 w;
-        w[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);
-        w[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);
-        w[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);
-        w[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
-        qf[b] = __builtin_bit_cast(bf16x8, w);
+        qv[b] = (u32x4){0, 0, 0, 0};
+        if (valid) qv[b] = *reinterpret_cast<const u32x4*>(qp + 32 * b);
     }
-    float c0[NB];
-    {
-        const uint32_t minus = Q41 ? 0xC300C300u : 0xC308C308u;   // bf16 -128, -136
-        const bf16x8 k = __builtin_bit_cast(bf16x8, (u32x4){minus, minus, minus, minus});
+    uint32_t big = 0;
 #pragma unroll
-        for (int b = 0; b < NB; b++) c0[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, qf[b], (f32x4){0, 0, 0, 0}, 0, 0, 0)[0];
-    }
+    for (int b = 0; b < NB; b++) big = max(big, largest_bf16(qv[b]));
+    big = max(big, (uint32_t)__shfl_xor((int)big, 16, 64));
+    big = max(big, (uint32_t)__shfl_xor((int)big, 32, 64));
+    const int up = query_shift(big);
+    const float sl2 = ldexpf(a.scale_log2, -up);
+    f16x8 qf[NB];
+#pragma unroll
+    for (int b = 0; b < NB; b++) qf[b] = query_f16(qv[b], up);
 
-    const uint32_t bf128 = held(0x43004300u);
+    const uint32_t f1024 = held(0x64006400u);
+    const f16x2 s16 = as_f16x2(held(0x2C002C00u));   // 1/16
     ColState<NB> st;
 #pragma unroll
     for (int i = 0; i < 2 * NB; i++) st.o[i] = (f32x4){0, 0, 0, 0};
@@ -338,8 +344,8 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
         const int t0 = (ua + wave + NW * i) * kUnit;
         const bool masked = t0 < lo_most || t0 + kUnit > hi_least;
         if (!(absent >> (i & 31) & 1)) {
-            if (masked) unit_step<NB, Q41, true>(ring + get, qf, c0, a.scale_log2, t0, lo, hi, q.tokens, bf128, &st);
-            else unit_step<NB, Q41, false>(ring + get, qf, c0, a.scale_log2, t0, lo, hi, q.tokens, bf128, &st);
+            if (masked) unit_step<NB, Q41, true>(ring + get, qf, sl2, t0, lo, hi, q.tokens, f1024, s16, &st);
+            else unit_step<NB, Q41, false>(ring + get, qf, sl2, t0, lo, hi, q.tokens, f1024, s16, &st);
         }
         get = next(get);
     }

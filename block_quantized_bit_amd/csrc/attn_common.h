@@ -14,7 +14,6 @@
 
 namespace wq {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -166,6 +165,8 @@ __device__ inline T load_at(global_bytes p, uint32_t offset) {
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+__device__ inline f16x2 as_f16x2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+
 // (w & mask) | bits, in one instruction where neither is a literal to the compiler (an instruction takes one).  Not as
 // written assembly: the compiler counts no waiting states between a matrix instruction and that.
 __device__ inline uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
@@ -179,11 +180,24 @@ __device__ inline uint32_t held(uint32_t c) {
     return r;
 }
 // The codes of a word, two to a register, nibbles i and i + 4, under the bits of a number whose last place is 1
-// (fp16 1024: 0x64006400, bf16 128: 0x43004300).
+// (fp16 1024: 0x64006400).
 __device__ inline uint32_t nibble_pair(uint32_t w, int i, uint32_t bits) { return and_or(w >> (4 * i), 0x000F000Fu, bits); }
 // V words (masked to one nibble per byte): bytes 0, 1 or 2, 3.
 __device__ inline f16x2 byte_pair(uint32_t w, int hi) {
     return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w, hi ? 0x04030402u : 0x04010400u));
+}
+// 1024 + 16 q -> q - OFF, exactly: a code where it lies, four bits up, costs no shift.  s16: 1/16.
+template <int OFF>
+__device__ inline f16x2 sixteenth(f16x2 u, f16x2 s16) {
+    const _Float16 c = -(_Float16)(64 + OFF);
+    return __builtin_elementwise_fma(u, s16, (f16x2){c, c});
+}
+// Nibbles i and i + 4 of a word, less OFF.
+template <int OFF>
+__device__ inline f16x2 code_pair(uint32_t w, int i, uint32_t f1024, f16x2 s16) {
+    if (i >= 2) w >>= 8;
+    if (i & 1) return sixteenth<OFF>(as_f16x2(and_or(w, 0x00F000F0u, f1024)), s16);
+    return as_f16x2(and_or(w, 0x000F000Fu, f1024)) - (_Float16)(1024 + OFF);
 }
 // 1024 + q -> the value: (q - 8) d, or q d + m with one rounding.  Both subtractions are exact.
 template <bool Q41>
@@ -196,11 +210,31 @@ __device__ inline f16x2 code_value(f16x2 u, f16x2 d, f16x2 m) {
         return c * d;
     }
 }
-__device__ inline f16x2 as_f16x2(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
 __device__ inline uint32_t pack_f16(float a, float b) { return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b}); }
 __device__ inline uint32_t pack_bf16(float a, float b) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// Queries as fp16: a row's values times 2^query_shift, which puts the largest into [2^14, 2^15) (subnormal bf16 numbers get as
+// far as 2^141 takes them, and all of them are exact then).  The others keep all their bits down to 2^-14, and are off by
+// 2^-39 of the largest at most below that.  The factor is taken back in the scale of the scores.
+__device__ inline uint32_t largest_bf16(u32x4 v) {   // bits, without the sign
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) big = max(big, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+    return big;
+}
+__device__ inline int query_shift(uint32_t big) { return 141 - (int)(big >> 7); }   // exponent bits of bf16: value < 2^(e - 126)
+// In the order of a K word's nibble pairs: 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ inline f16x8 query_f16(u32x4 v, int up) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[2 * i] = ldexpf(__uint_as_float(v[i] << 16), up);
+        f[2 * i + 1] = ldexpf(__uint_as_float(v[i] & 0xFFFF0000u), up);
+    }
+    return __builtin_bit_cast(f16x8, (u32x4){pack_f16(f[0], f[4]), pack_f16(f[1], f[5]), pack_f16(f[2], f[6]), pack_f16(f[3], f[7])});
 }
 
 // Probabilities are held as 2^(x - ref): at most 2^15, the top of fp16, and 2^7 when ref is set, so that ref moves

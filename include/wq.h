@@ -358,10 +358,13 @@ wq_status wq_attn_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32
  * WQ_ERR_SHAPE): a tile is one key/value head with 16 pairs (128 or 256 in calls with more
  * than 128 per sequence) of a row and a query head of one sequence.
  * A row that sees no token gets zeros.  Scores, the softmax's maximum and sum and the
- * sums over tokens are fp32; probabilities, values and (in calls with many rows) keys are
- * rounded to fp16 for the matrix products.  Per element |y - y_ref| <=
- * (2^-9 + 2^-9 A) * sum_t (p_t + 2^-23) |v^_t| plus the final bf16 rounding, where A is the row's
- * largest |scale| * sum_c |q_c k^_tc| and y_ref is exact for the values in the cache. */
+ * sums over tokens are fp32; probabilities, values and (q4_1, and in calls with many rows)
+ * keys are rounded to fp16 for the matrix products, and so are queries, after a power of two that
+ * puts a row's largest near the top of fp16.  Per element |y - y_ref| <=
+ * (2^-9 + 2^-9 A + 2^-38 Q) * sum_t (p_t + 2^-23) |v^_t| plus the final bf16 rounding, where A is
+ * the largest |scale| * sum_c |q_c k^_tc| of the row and head, Q its |scale| * max_c |q_c| times the
+ * largest sum_c |k^_tc|, and y_ref is exact for the values in the cache, as long as |scale| * max_c |q_c|
+ * is at most 2^100 (beyond that, and where a query is no finite number, the row and head may be NaN). */
 wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq, const void* cache,
                   float scale, int32_t causal, int32_t window, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes,
                   void* stream);
