@@ -821,31 +821,15 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     }
     got = fetch(r);
 
-    // queries as fp16, scaled by a power of two per column so that the largest is in [2^14, 2^15)
+    uint32_t big = 0;
+#pragma unroll
+    for (int s = 0; s < 2 * NB; s++) big = max(big, largest_bf16(qv[s]));
+    big = max(big, (uint32_t)__shfl_xor((int)big, 32, 64));
+    const int up = query_shift(big);
+    const float sl2 = ldexpf(a.scale_log2, -up);
     f16x8 qf[2 * NB];
-    float sl2 = a.scale_log2;
-    {
-        uint32_t big = 0;
 #pragma unroll
-        for (int s = 0; s < 2 * NB; s++)
-#pragma unroll
-            for (int k = 0; k < 4; k++) big = max(big, max(qv[s][k] & 0x7FFFu, (qv[s][k] >> 16) & 0x7FFFu));
-        big = max(big, (uint32_t)__shfl_xor((int)big, 32, 64));
-        const int k = big == 0 ? 0 : min(141 - (int)(big >> 7), 100);   // exponent bits of bf16: value < 2^(e - 126)
-        const float up = ldexpf(1.0f, k);
-        sl2 *= ldexpf(1.0f, -k);
-#pragma unroll
-        for (int s = 0; s < 2 * NB; s++) {
-            float f[8];
-#pragma unroll
-            for (int k2 = 0; k2 < 4; k2++) {
-                f[2 * k2] = __uint_as_float(qv[s][k2] << 16) * up;
-                f[2 * k2 + 1] = __uint_as_float(qv[s][k2] & 0xFFFF0000u) * up;
-            }
-            const u32x4 p = {pack_f16(f[0], f[4]), pack_f16(f[1], f[5]), pack_f16(f[2], f[6]), pack_f16(f[3], f[7])};
-            qf[s] = __builtin_bit_cast(f16x8, p);
-        }
-    }
+    for (int s = 0; s < 2 * NB; s++) qf[s] = query_f16(qv[s], up);
 
     f32x16 o[NB];
 #pragma unroll

@@ -95,3 +95,9 @@ def _magnitude(orc, fmt, rows, tokens, qs, scale):
 @RANGE
 def test_queries_of_any_magnitude(orc, fmt, rows, tokens, qs, scale):
     _magnitude(orc, fmt, rows, tokens, qs, scale)
+
+
+@FMT
+@RANGE
+def test_many_rows_of_queries_of_any_magnitude(orc, fmt, qs, scale):
+    _magnitude(orc, fmt, 140, 70, qs, scale)
