@@ -111,11 +111,12 @@ int64_t floor_div(int64_t a, int64_t b) {   // b > 0
 // byte range [base_i + r*ld_i*es, base_i + r*ld_i*es + w_i*es).  Row r1 of A meets row r2
 // of B iff b + r2*lb < a_hi and b + r2*lb + wb > a_lo, an interval of r2 that is solved
 // in closed form; with equal strides r2 - r1 is the only unknown, so one interval covers
-// every row.
+// every row.  Windows that lie apart as a whole (buffers of their own) are told at once.
 bool windows_overlap(const void* pa, int64_t lda, int64_t wa, const void* pb, int64_t ldb, int64_t wb,
                      int64_t m, int64_t es) {
     const int64_t a = (int64_t)reinterpret_cast<uintptr_t>(pa), b = (int64_t)reinterpret_cast<uintptr_t>(pb);
     const int64_t la = lda * es, lb = ldb * es, na = wa * es, nb = wb * es;
+    if (a + (m - 1) * la + na <= b || b + (m - 1) * lb + nb <= a) return false;
     if (la == lb) {
         // rows r1, r2 = r1 + t meet iff -nb < (b - a) + t*la < na, for some |t| <= m - 1
         const int64_t d = b - a;
@@ -489,6 +490,8 @@ wq_status wq_cache_read(const wq_cache_desc* d, const wq_seqs* s, const void* ca
     wq_status st = check_cache_rows(d, s, k, ldk, v, ldv, ydt, cache, &q, &q41);
     if (st != WQ_OK) return st;
     if (q.rows == 0 || q.batch == 0) return WQ_OK;
+    const int64_t width = (int64_t)d->kv_heads * d->head_dim;
+    if (windows_overlap(k, ldk, width, v, ldv, width, q.rows, ydt == WQ_F32 ? 4 : 2)) return WQ_ERR_INVALID_ARG;
     return from_hip(wq::launch_cache_read(q, q41, d->head_dim, ydt == WQ_F32, static_cast<const uint8_t*>(cache), k, ldk, v,
                                           ldv, static_cast<hipStream_t>(stream)));
 }
@@ -521,6 +524,8 @@ wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, con
         if (!aligned(ws, 16)) return WQ_ERR_ALIGNMENT;
         if (ws_bytes < wq::attn_workspace_bytes(a)) return WQ_ERR_WORKSPACE;
     }
+    // (a tile's queries are read when another tile's rows may be written already)
+    if (windows_overlap(q, ldq, width, y, ldy, width, a.s.rows, 2)) return WQ_ERR_INVALID_ARG;
     a.q = q;
     a.ldq = ldq;
     a.cache = static_cast<const uint8_t*>(cache);

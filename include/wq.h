@@ -330,7 +330,7 @@ wq_status wq_cache_write(const wq_cache_desc* d, const wq_seqs* s, const void* k
 
 /* Read the rows' tokens back: k and v (as above, type ydt) receive the values that the
  * cache stands for, rounded to nearest even for WQ_BF16; rows without a token receive
- * zeros.  Any tokens can be read: with row_start covering len[b] rows, all of them. */
+ * zeros.  The two windows must not share a byte (WQ_ERR_INVALID_ARG).  Any tokens can be read: with row_start covering len[b] rows, all of them. */
 wq_status wq_cache_read(const wq_cache_desc* d, const wq_seqs* s, const void* cache, void* k, int64_t ldk, void* v,
                         int64_t ldv, int32_t ydt, void* stream);
 
@@ -352,7 +352,8 @@ wq_status wq_attn_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32
  *             tokens (cross-attention: the rows are then no tokens of the cache)
  *   window  : with causal, > 0: the row sees only its last `window` tokens (itself among
  *             them); 0: no limit
- *   y       : bf16 [rows, q_heads * head_dim], as q with ldy; must not overlap q
+ *   y       : bf16 [rows, q_heads * head_dim], as q with ldy; the windows of q and y must not share a
+ *             byte (WQ_ERR_INVALID_ARG)
  *   ws      : workspace (16-byte aligned, see wq_attn_workspace_size) or NULL
  * rows * q_heads is at most 2^31 - 1, and the call has fewer than 2^23 tiles (else
  * WQ_ERR_SHAPE): a tile is one key/value head with 16 pairs (128 or 256 in calls with more

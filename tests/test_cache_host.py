@@ -297,3 +297,20 @@ def test_decoder_caches():
             policy.decoder_caches(bad, 1)
     with pytest.raises(ValueError):
         policy.decoder_caches("q4_0", 0)
+
+
+def test_overlapping_windows_are_refused():
+    """Rows that are read or written twice: Y over Q, and the two outputs of a read over each other, at equal and at
+    different leading dimensions.  (A window that is accepted would be launched, so only refusals are made here.)"""
+    d, s = _desc(), _seqs(rows=6)
+    at = lambda q, ldq, y, ldy: _status(wq.wq_attn, d, s, 32, q, ldq, FAKE, 0.1, 1, 0, y, ldy, None, 0, 0)  # noqa: E731
+    far = FAKE + 2 * 5 * 4104 + 2 * 4096 - 16             # the last 8 columns of Q's last row
+    for ldq in (4096, 4104):
+        assert at(FAKE, ldq, FAKE, ldq) == 1
+    for y, ldy in ((FAKE + 16, 4104), (FAKE, 8192), (far, 4104), (far, 1 << 20), (FAKE + 2 * 4104 - 16, 4104)):
+        assert at(FAKE, 4104, y, ldy) == 1 and at(y, ldy, FAKE, 4104) == 1
+    for dt, es in ((wq.WQ_BF16, 2), (wq.WQ_F32, 4)):
+        rd = lambda k, ldk, v, ldv: _status(wq.wq_cache_read, d, s, FAKE, k, ldk, v, ldv, dt, 0)  # noqa: E731
+        assert rd(FAKE, 1024, FAKE, 1024) == 1
+        assert rd(FAKE, 2048, FAKE + es * 1016, 2048) == 1 and rd(FAKE + es * 1016, 2048, FAKE, 2048) == 1
+        assert rd(FAKE, 1024, FAKE + es * (6 * 1024 - 8), 1032) == 1

@@ -463,3 +463,18 @@ def test_a_decoder_layer(orc, fmt):
         want = yf.astype(np.float64) @ wo_hat.astype(np.float64).T
         bound = 4e-3 * (np.abs(yf.astype(np.float64)) @ np.abs(wo_hat.astype(np.float64)).T) + 1e-6
         assert np.all(np.abs(z.cpu().numpy() - want) <= bound)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 140])
+def test_queries_and_outputs_side_by_side(orc, rows):
+    """Q and Y as the columns of one buffer share no byte: the call is taken, and gives what separate buffers give."""
+    c = Case(Q4_0, 64, 2, 64, [rows], [200], seed=40)
+    c.fill(*c.random_kv())
+    q = _q(c, 2)
+    want = run_attn(c, q, 2, 0.125, 1, 0, ws=None)[1]
+    both = torch.zeros((rows, 2 * 256 + 8), dtype=torch.int16, device=DEV)
+    both[:, :256] = dev_bf16(q.reshape(rows, -1))
+    wq.wq_attn(c.desc, c.seqs, 4, both, both.shape[1], c.cache, 0.125, 1, 0, both[:, 256:], both.shape[1])
+    torch.cuda.synchronize()
+    assert np.array_equal(both[:, 256:512].cpu().numpy().view(np.uint16).reshape(want.shape), want)
+    assert not both[:, 512:].any()
