@@ -394,6 +394,10 @@ struct Launch {
     int per_row, groups;
     dim3 grid, block;
 };
+// Units of 32 tokens: n rows touch at most n / 32 + 2.  Threads per workgroup: whole waves.
+int64_t unit_bound(const Seqs& s) { return (int64_t)s.rows / kUnit + 2 * (int64_t)std::min(s.rows, s.batch); }
+constexpr int unit_threads(int nb) { return nb == 3 ? 128 : 32 * nb; }
+
 Launch group_launch(const Seqs& s, int nb) {
     Launch l;
     l.per_row = s.heads * nb * 4;
@@ -409,11 +413,10 @@ Launch group_launch(const Seqs& s, int nb) {
 template <int NB>
 void write_nb(const Seqs& q, bool q41, bool f32, const void* k, int64_t ldk, const void* v, int64_t ldv, uint8_t* cache, hipStream_t s) {
     if (q.row_start && (int64_t)q.rows >= kManyRows * (int64_t)q.batch) {
-        // units of 32 tokens: n rows touch at most n / 32 + 2
-        const dim3 grid((unsigned)((int64_t)q.rows / kUnit + 2 * (int64_t)std::min(q.rows, q.batch)), (unsigned)q.heads);
+        const dim3 grid((unsigned)unit_bound(q), (unsigned)q.heads);
         auto f = q41 ? (f32 ? k_cache_write_units<true, true, NB> : k_cache_write_units<true, false, NB>)
                      : (f32 ? k_cache_write_units<false, true, NB> : k_cache_write_units<false, false, NB>);
-        hipLaunchKernelGGL(f, grid, dim3(NB == 3 ? 128 : 32 * NB), 0, s, q, k, ldk, v, ldv, cache);
+        hipLaunchKernelGGL(f, grid, dim3(unit_threads(NB)), 0, s, q, k, ldk, v, ldv, cache);
         return;
     }
     const Launch l = group_launch(q, NB);
@@ -430,6 +433,13 @@ void read_nb(const Seqs& q, bool q41, bool f32, const uint8_t* cache, void* k, i
 }
 
 }  // namespace
+
+// A launch has fewer than 2^32 threads along x, whichever kernel the call takes.  (The workgroups fit 32 bits before that.)
+bool cache_fits(const Seqs& q, int dim) {
+    const Launch l = group_launch(q, dim / 32);
+    const int64_t most = (int64_t(1) << 32) - 1;
+    return (int64_t)l.grid.x * l.block.x <= most && unit_bound(q) * unit_threads(dim / 32) <= most;
+}
 
 hipError_t launch_cache_write(const Seqs& q, bool q41, int dim, bool f32, const void* k, int64_t ldk, const void* v, int64_t ldv,
                               uint8_t* cache, hipStream_t s) {

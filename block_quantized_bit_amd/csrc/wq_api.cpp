@@ -231,9 +231,7 @@ wq_status check_cache_rows(const wq_cache_desc* d, const wq_seqs* s, const void*
     if ((st = check_rows(v, ldv, width)) != WQ_OK) return st;
     if (!cache) return WQ_ERR_INVALID_ARG;
     if (!aligned(cache, 16)) return WQ_ERR_ALIGNMENT;
-    // chunks of 8 channels, 256 to a workgroup, at most 2^31 - 1 workgroups
-    if ((int64_t)q->rows > (int64_t(0x7FFFFFFF) * 256) / (width / 8)) return WQ_ERR_SHAPE;
-    return WQ_OK;
+    return wq::cache_fits(*q, d->head_dim) ? WQ_OK : WQ_ERR_SHAPE;
 }
 
 wq_status check_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, wq::AttnArgs* a) {

@@ -72,7 +72,8 @@ hipError_t launch_quantize_act(int64_t m, int64_t k, const uint16_t* x, int64_t 
 hipError_t launch_expand_act(int64_t m, int64_t k, const uint8_t* codes, const uint8_t* scales,
                              const uint8_t* gw, uint16_t* xe, float* gprod, hipStream_t s);
 
-// 4-bit key/value cache (cache.hip): rows of K and V, bf16 or fp32, into and out of the pool.
+// 4-bit key/value cache (cache.hip): whether a call's launches are small enough; rows of K and V, bf16 or fp32, into and out of the pool.
+bool cache_fits(const Seqs& q, int dim);
 hipError_t launch_cache_write(const Seqs& q, bool q41, int dim, bool f32, const void* k, int64_t ldk, const void* v,
                               int64_t ldv, uint8_t* cache, hipStream_t s);
 hipError_t launch_cache_read(const Seqs& q, bool q41, int dim, bool f32, const uint8_t* cache, void* k, int64_t ldk,

@@ -324,7 +324,8 @@ wq_status wq_cache_size(const wq_cache_desc* d, size_t* bytes);
  *   k, v : [rows, kv_heads * head_dim] of type xdt (WQ_BF16 or WQ_F32), 16-byte aligned,
  *          leading dimensions ldk, ldv >= kv_heads * head_dim, multiples of 8, at most
  *          2^31 - 1
- * Rows without a token (see wq_seqs) are skipped. */
+ * Rows without a token (see wq_seqs) are skipped.  A call whose launch would have 2^32 threads
+ * or more is refused (WQ_ERR_SHAPE; wq_cache_read too): up to 2^26 - 8 (batch + 1) rows are always taken. */
 wq_status wq_cache_write(const wq_cache_desc* d, const wq_seqs* s, const void* k, int64_t ldk, const void* v, int64_t ldv,
                          int32_t xdt, void* cache, void* stream);
 

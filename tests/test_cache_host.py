@@ -314,3 +314,17 @@ def test_overlapping_windows_are_refused():
         assert rd(FAKE, 1024, FAKE, 1024) == 1
         assert rd(FAKE, 2048, FAKE + es * 1016, 2048) == 1 and rd(FAKE + es * 1016, 2048, FAKE, 2048) == 1
         assert rd(FAKE, 1024, FAKE + es * (6 * 1024 - 8), 1032) == 1
+
+
+@pytest.mark.parametrize("dim,heads,most", [(64, 1, (1 << 31) - 125), (128, 8, (1 << 27) - 5), (256, 16, (1 << 26) - 1), (96, 5, (1 << 28) - 13)])
+def test_more_rows_than_a_launch_has(dim, heads, most):
+    """Groups of four tokens, each of heads * dim / 8 threads, K and V side by side: the last number of rows whose launch has
+    fewer than 2^32 threads along x.  (No sequences: a call that is taken does nothing.)"""
+    d, width = _desc(head_dim=dim, kv_heads=heads), dim * heads
+    for rows, want in ((most, 0), (most + 1, 3), ((1 << 31) - 1, 3)):
+        s = _seqs(batch=0, rows=rows, row_start=FAKE)
+        assert _status(wq.wq_cache_write, d, s, FAKE, width, FAKE, width, wq.WQ_BF16, FAKE, 0) == want
+        assert _status(wq.wq_cache_read, d, s, FAKE, FAKE, width, FAKE, width, wq.WQ_F32, 0) == want
+    # sequences count too: each may touch two groups more
+    s = _seqs(batch=1 << 20, rows=most, row_start=FAKE)
+    assert _status(wq.wq_cache_write, d, s, FAKE, width, FAKE, width, wq.WQ_BF16, FAKE, 0) == 3
