@@ -34,9 +34,8 @@ struct UnitRing {
     static constexpr int loads = full + (rest ? 1 : 0);
 };
 
-// The request for one unit: 16 bytes a lane, to LDS at m0 + offset + 16 lane.  The compiler does not see the write (and
-// sets m0 itself where it needs it); the memory clobbers keep LDS reads in order with it, and the counted waits below are
-// the only ones there are for it.  Five waiting states (s_nop 4) are what a load's address needs that the vector unit
+// The request for one unit: 16 bytes a lane, to LDS at m0 + offset + 16 lane.  The compiler does not see the write to
+// LDS; the memory clobbers keep LDS reads in order with it, and the counted waits below are the only ones there are for it.  Five waiting states (s_nop 4) are what a load's address needs that the vector unit
 // wrote: the compiler counts none before written assembly.
 template <int BYTES>
 __device__ inline void request_unit(const uint8_t* src, uint32_t lds) {
@@ -47,7 +46,7 @@ __device__ inline void request_unit(const uint8_t* src, uint32_t lds) {
     for (int c = 0; c < full + (rest ? 1 : 0); c++) {
         if (c < full || lane < rest) {
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-                         :: "s"(lds + c * 1024), "v"(off), "s"(src + c * 1024) : "memory");
+                         :: "s"(lds + c * 1024), "v"(off), "s"(src + c * 1024) : "m0", "memory");
         }
     }
 }

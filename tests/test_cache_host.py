@@ -328,3 +328,19 @@ def test_more_rows_than_a_launch_has(dim, heads, most):
     # sequences count too: each may touch two groups more
     s = _seqs(batch=1 << 20, rows=most, row_start=FAKE)
     assert _status(wq.wq_cache_write, d, s, FAKE, width, FAKE, width, wq.WQ_BF16, FAKE, 0) == 3
+
+
+def test_written_assembly_names_what_it_writes():
+    """A statement that writes m0 says so, so that the compiler keeps nothing there across it."""
+    import os
+    import re
+    found = 0
+    for name in sorted(os.listdir(build.CSRC)):
+        with open(os.path.join(build.CSRC, name)) as f:
+            text = f.read()
+        for stmt in re.findall(r"\basm\b[^;]*;", text):
+            code, *rest = stmt.split(":")
+            if "m0" in code:
+                found += 1
+                assert '"m0"' in "".join(rest), f"{name}: {stmt}"
+    assert found > 0
