@@ -71,10 +71,19 @@ def desc(fmt, n: int, k: int, dq: bool = False, block: int = 0) -> wq_desc:
     return wq_desc(int(fmt), int(block), int(n), int(k), 256 if dq else 0, 0)
 
 
+def _int32(where: str, name: str, v) -> int:
+    """v as a 32-bit argument: ctypes would pass its low bits."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{where}: {name} {v} does not fit 32 bits")
+    return v
+
+
 def cache_desc(fmt, head_dim: int, kv_heads: int, page: int, pages: int) -> wq_cache_desc:
     if isinstance(fmt, str):
         fmt = format_from_name(fmt)
-    return wq_cache_desc(int(fmt), int(head_dim), int(kv_heads), int(page), int(pages), 0)
+    return wq_cache_desc(*(_int32("cache_desc", *a) for a in (("format", fmt), ("head_dim", head_dim), ("kv_heads", kv_heads), ("page", page))),
+                         int(pages), 0)
 
 
 def seqs(batch: int, rows: int, len, table=None, row_start=None, table_ld: int | None = None) -> wq_seqs:  # noqa: A002
@@ -94,7 +103,8 @@ def seqs(batch: int, rows: int, len, table=None, row_start=None, table_ld: int |
         if table_ld is not None and table_ld != table.shape[1]:
             raise ValueError(f"seqs: table has {table.shape[1]} entries per sequence, not {table_ld}")
         table_ld = table.shape[1]
-    s = wq_seqs(int(batch), int(rows), _ptr(row_start), _ptr(len), _ptr(table), int(table_ld or 0), 0)
+    s = wq_seqs(_int32("seqs", "batch", batch), _int32("seqs", "rows", rows), _ptr(row_start), _ptr(len), _ptr(table),
+                _int32("seqs", "table_ld", table_ld or 0), 0)
     s.tensors = (row_start, len, table)
     s.device = _device("seqs", *s.tensors)
     return s
@@ -320,12 +330,13 @@ def wq_cache_read(d: wq_cache_desc, s: wq_seqs, cache, k, ldk: int, v, ldv: int,
 
 def wq_attn_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int) -> int:
     b = ctypes.c_size_t()
-    _check(lib().wq_attn_workspace_size(ctypes.byref(d), ctypes.byref(s), int(q_heads), ctypes.byref(b)),
+    _check(lib().wq_attn_workspace_size(ctypes.byref(d), ctypes.byref(s), _int32("wq_attn_workspace_size", "q_heads", q_heads), ctypes.byref(b)),
            "wq_attn_workspace_size", True)
     return b.value
 
 
 def wq_attn(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scale: float, causal, window: int, y, ldy: int,
             ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
-    return _call_on("wq_attn", s, (q, cache, y, ws), stream, check, lib().wq_attn, ctypes.byref(d), ctypes.byref(s), q_heads,
-                    _ptr(q), ldq, _ptr(cache), scale, int(causal), window, _ptr(y), ldy, _ptr(ws), ws_bytes)
+    return _call_on("wq_attn", s, (q, cache, y, ws), stream, check, lib().wq_attn, ctypes.byref(d), ctypes.byref(s),
+                    _int32("wq_attn", "q_heads", q_heads), _ptr(q), ldq, _ptr(cache), scale, _int32("wq_attn", "causal", causal),
+                    _int32("wq_attn", "window", window), _ptr(y), ldy, _ptr(ws), ws_bytes)

@@ -344,3 +344,20 @@ def test_written_assembly_names_what_it_writes():
                 found += 1
                 assert '"m0"' in "".join(rest), f"{name}: {stmt}"
     assert found > 0
+
+
+@pytest.mark.parametrize("past", [1 << 32, -(1 << 32), 1 << 31])
+def test_binding_refuses_numbers_past_32_bits(past):
+    """Such a number would be passed as its low 32 bits: another page size, batch or window.  (Window and heads are tried on
+    a descriptor that is refused anyway.)"""
+    d, s = _desc(), _seqs()
+    for call in (lambda: wq.cache_desc("q4_0", 128, 8, past + 64, 10), lambda: wq.cache_desc("q4_0", 128, past + 8, 64, 10),
+                 lambda: wq.cache_desc("q4_0", past + 128, 8, 64, 10), lambda: wq.seqs(past + 4, 4, FAKE, FAKE, FAKE, 10),
+                 lambda: wq.seqs(4, past + 4, FAKE, FAKE, FAKE, 10), lambda: wq.seqs(4, 4, FAKE, FAKE, FAKE, past + 10),
+                 lambda: wq.wq_attn_workspace_size(d, s, past + 32),
+                 lambda: wq.wq_attn(_desc(page=1), s, past + 32, FAKE, 4096, FAKE, 0.1, 1, 0, 2 * FAKE, 4096, stream=0),
+                 lambda: wq.wq_attn(_desc(page=1), s, 32, FAKE, 4096, FAKE, 0.1, 1, past + 5, 2 * FAKE, 4096, stream=0),
+                 lambda: wq.wq_attn(_desc(page=1), s, 32, FAKE, 4096, FAKE, 0.1, past + 1, 0, 2 * FAKE, 4096, stream=0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    assert wq.cache_desc("q4_0", 128, 8, 64, 1 << 33).pages == 1 << 33     # (64 bits in the descriptor)
