@@ -240,7 +240,6 @@ wq_status check_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, 
     if ((st = check_seqs(s, &a->s)) != WQ_OK) return st;
     if (q_heads < 1 || q_heads > 65535 || q_heads % d->kv_heads != 0) return WQ_ERR_SHAPE;
     if ((int64_t)a->s.rows > 0x7FFFFFFF / q_heads) return WQ_ERR_SHAPE;   // rows and heads: the launch's workgroups
-    a->q_heads = q_heads;
     a->group = q_heads / d->kv_heads;
     a->dim = d->head_dim;
     if (a->s.rows > 0 && a->s.batch > 0 && !wq::attn_fits(*a)) return WQ_ERR_SHAPE;

@@ -88,7 +88,7 @@ struct AttnArgs {
     int64_t ldq, ldy;
     uint8_t* ws;           // null: no split of a sequence over workgroups
     float scale_log2;      // softmax scale times log2(e)
-    int32_t q_heads, group, dim, window;
+    int32_t group, dim, window;
     int32_t tile_cols;     // columns (rows x heads) per tile of the kernel that runs
     int32_t workgroups;    // > 0: sequences are shared out over so many
     int32_t least_units;   // units that each then takes at least

@@ -144,7 +144,6 @@ def _call_on(where: str, s: wq_seqs, tensors, stream, check: bool, fn, *args) ->
         if stream is None:
             return _check(fn(*args, _torch._C._cuda_getCurrentRawStream(dev)), where, check)
     return _check(fn(*args, _stream(stream)), where, check)
-    return _check(fn(*args, _stream(stream)), where, check)
 
 
 _lib = None
