@@ -361,3 +361,12 @@ def test_binding_refuses_numbers_past_32_bits(past):
         with pytest.raises(ValueError, match="32 bits"):
             call()
     assert wq.cache_desc("q4_0", 128, 8, 64, 1 << 33).pages == 1 << 33     # (64 bits in the descriptor)
+
+
+def test_workspace_refusal_of_a_split_call():
+    """The call does ask for a workspace; one byte less is refused, as is a misaligned one."""
+    d, s = _desc(pages=5000), _seqs(batch=1, rows=1, table_ld=4096)
+    need = wq.wq_attn_workspace_size(d, s, 32)
+    assert need > 0
+    at = lambda ws, n: _status(wq.wq_attn, d, s, 32, FAKE, 4096, FAKE, 0.1, 1, 0, 2 * FAKE, 4096, ws, n, 0)  # noqa: E731
+    assert at(FAKE, need - 1) == 6 and at(FAKE, 0) == 6 and at(FAKE + 8, need) == 4

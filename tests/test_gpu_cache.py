@@ -226,3 +226,22 @@ def test_offsets_past_32_bits(orc):
     want = stored(orc, Q4_0, x.reshape(300, 8, 256)).reshape(300, -1)
     for o in out:
         _same(o.cpu().numpy(), want.view(np.uint32), wq.WQ_F32)
+
+
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("counts", [[1, 1], [5, 40]], ids=["token", "rows"])
+def test_read_leaves_the_padding(orc, fmt, counts):
+    """Columns behind the heads and rows behind the last sequence keep the bytes they had, in both types."""
+    c = Case(fmt, 96, 3, 64, counts, [70, 40], seed=9, one_row=max(counts) == 1, pad_rows=3)
+    k, v = _values(c, wq.WQ_F32, "normal")
+    K, V = (_dev(x.reshape(c.rows, -1), wq.WQ_F32, 0) for x in (k, v))
+    width, ld, n = 3 * 96, 3 * 96 + 16, int(c.start[-1])
+    wq.wq_cache_write(c.desc, c.seqs, K, width, V, width, wq.WQ_F32, c.cache)
+    for ydt, kind, fill in ((wq.WQ_F32, torch.int32, 0x7FA5A5A5), (wq.WQ_BF16, torch.int16, 0x7FA5)):
+        out = [torch.full((c.rows, ld), fill, dtype=kind, device=DEV) for _ in range(2)]
+        wq.wq_cache_read(c.desc, c.seqs, c.cache, out[0], ld, out[1], ld, ydt)
+        torch.cuda.synchronize()
+        for o, x in zip(out, (k, v)):
+            assert bool((o[:, width:] == fill).all()) and bool((o[n:] == fill).all())
+            got = np.ascontiguousarray(o[:n, :width].cpu().numpy()).view(np.uint32 if ydt == wq.WQ_F32 else np.uint16)
+            _same(got, _expected(c, x, ydt, orc)[:n], ydt)
