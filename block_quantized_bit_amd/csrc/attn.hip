@@ -4,6 +4,12 @@
 // o = sum 2^(x_t - ref) v^_t in fp32; where a score passes ref by too much, o and l are scaled to a new one.  Parts of a
 // column (waves, workgroups) are joined by y = sum_i 2^(ref_i - ref) o_i / sum_i 2^(ref_i - ref) l_i.  Nothing of the size
 // rows x tokens is written, and keys and values are read packed.
+//
+// Rounded to fp16, because the matrix instructions take 16-bit operands and fp16 has three bits more than bf16: probabilities
+// (2^(x - ref), at most 2^15; the sum that divides is of the unrounded ones), values, queries (times a power of two per row and
+// head, mostly exact), and keys, but for q4_0 in calls with few rows, whose codes are exact there.  Each is off by half a step,
+// 2^-11 of itself.  In calls with ordinary scores the outputs' error is that of their own rounding to bf16 (0.0017 of their
+// magnitude against 64 bits, as for the same computed in fp32).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -19,9 +25,10 @@ namespace wq {
 // What bounds it: with one row per sequence a group's heads share every unit that is read, at 2 x 16 columns of products
 // per 4.5 or 5 bits, so a call with enough tokens is bound by memory, and a short one by the way to memory and back
 // (lengths, pages, units, one after the other).  Measured (a copy runs at 5.1 TB/s on the card): 32 sequences
-// of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0 (1.16 GB) 226 us with the join, 5.1 TB/s; one of 131077 tokens, 8 x 8
-// heads (151 MB) 42 us; 16 of 1500 tokens, 20 heads of 64 (35 MB) 16 us; one of 224 tokens 5.8 us; 16 x 5 rows that see 4096
-// tokens, 2 x 8 heads of 256, q4_1 (43 MB) 44 us, where three tiles take each unit and their conversions bound it.
+// of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0 (1.16 GB) 227-233 us with the join, 5.0-5.1 TB/s; one of 131077 tokens,
+// 8 x 8 heads (151 MB) 43 us; 16 of 1500 tokens, 20 heads of 64 (35 MB) 16 us, with neither memory (2.1 TB/s) nor the vector
+// unit (32 % of the cycles) busy; one of 224 tokens 6 us; 16 x 5 rows that see 4096 tokens, 2 x 8 heads of 256, q4_1 (43 MB)
+// 43 us, where three tiles take each unit and their conversions bound it.
 // 16 columns, since a group's heads of one token are seldom more; with 32 columns a wave spills, and was slower in all of
 // these.
 //
@@ -34,9 +41,10 @@ struct UnitRing {
     static constexpr int loads = full + (rest ? 1 : 0);
 };
 
-// The request for one unit: 16 bytes a lane, to LDS at m0 + offset + 16 lane.  The compiler does not see the write to
-// LDS; the memory clobbers keep LDS reads in order with it, and the counted waits below are the only ones there are for it.  Five waiting states (s_nop 4) are what a load's address needs that the vector unit
-// wrote: the compiler counts none before written assembly.
+// The request for one unit: 16 bytes a lane, to LDS at m0 + offset + 16 lane.  The compiler does not see the write to LDS; the
+// memory clobbers keep LDS reads in order with it, and the counted waits below are the only ones there are for it.  Five
+// waiting states (s_nop 4) are what a load's address needs that the vector unit wrote: the compiler counts none before written
+// assembly.
 template <int BYTES>
 __device__ inline void request_unit(const uint8_t* src, uint32_t lds) {
     const int lane = threadIdx.x & 63;
@@ -105,7 +113,7 @@ struct ColState {
 // q4_1's values d q + m, rounded to fp16 once.  Either way a product's terms are the keys' own, so its fp32 error follows
 // sum |q k^|.  (Terms that only cancel, codes from 128 on against a start of -136 sum q, or m sum q beside q4_1's codes, leave
 // errors of the size of the block's scale times sum |q|: a key of 32768 beside a query of nearly zero moved scores of 0.6 by
-// 0.1.  They were no faster: 32 sequences of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0, 223-227 us that way, 227-228 us.)
+// 0.1.  They took 223-227 us where this takes 227-233, for 32 sequences of 30011 to 32768 tokens, 8 x 5 heads of 128, q4_0.)
 template <int NB, bool Q41, bool MASKED>
 __device__ inline void unit_step(const uint8_t* unit, const f16x8 (&qf)[NB], float sl2, int t0, int lo, int hi, int tokens,
                                  uint32_t f1024, f16x2 s16, ColState<NB>* st) {
@@ -393,8 +401,8 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
 
 // Sequences shared out evenly: workgroup i takes units [i share, (i + 1) share) of the call's work, whatever the lengths
 // are; a tile that more than one workgroup has a part of is joined by k_attn_join_token.  With `workgroups` 0 every
-// workgroup has one whole tile.  (61 sequences of 1 to 8191 tokens, 8 x 4 heads of 128, q4_1: 74 us and 5 for the join,
-// 4.1 TB/s; 102 us where what beginning a tile costs is not counted.)
+// workgroup has one whole tile.  (61 sequences of 1 to 8191 tokens, 8 x 4 heads of 128, q4_1: 80 us with 5 for the join,
+// 4.0 TB/s; counting what beginning a tile costs took it from 102 us to 81.)
 template <int NB, bool Q41, int NW, int D>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_token(AttnArgs a) {
     constexpr int ring_bytes = NW * D * UnitRing<NB, Q41>::bytes, join_bytes = NW * 16 * (32 * NB + 4 + 2) * 4;
@@ -705,11 +713,14 @@ __device__ inline void store_pair(const Pair<Q41>& r, const PairPlace& at, uint3
 // independent of each other, so that the matrix unit works beside the vector unit: the scores of unit i + 1 beside the
 // exponentials of unit i, the sums over unit i's values beside the maximum of unit i + 1 and the conversions to fp16.
 //
-// Bound by the vector unit beside the matrix unit: 2048 rows of 8 x 4 heads of 128 over 18432 tokens (584 GFLOP) 612 us,
-// 955 TFLOP/s, where a large fp16 matrix product reaches 1405.  The products alone take 418 us; the conversions and
-// their loads the rest, which is why 256 columns share each of them.  64 columns per wave would halve them again, but the
-// accumulators then leave no registers (spills, and moves to and from the accumulation registers every step: slower); a ring
-// of 4 buffers, or two units per step with 128 columns of heads of 128, gained nothing.
+// Bound by the vector unit beside the matrix unit (issuing in 51 % and busy in 46 % of the cycles): 2048 rows of 8 x 4 heads of
+// 128 over 18432 tokens (584 GFLOP), q4_0, 604-617 us, 947-967 TFLOP/s, where a large fp16 matrix product reaches 1405; the
+// conversions and their loads come on top of the products, which is why 256 columns share each of them.  64 columns per wave
+// would halve them again, but the accumulators then leave no registers (spills, and moves to and from the accumulation
+// registers every step: slower); a ring of 4 buffers, or two units per step with 128 columns of heads of 128, gained nothing.
+// The same rows and tokens, q4_0 and q4_1: heads of 64 402 and 425 us (292 GFLOP), of 96 526 and 528 (438 GFLOP), of 128 609 and
+// 643, 4 x 4 heads of 256 875 and 1552 (584 GFLOP).  Heads of 256 have one wave per SIMD and reload 18 (q4_0) and 25 (q4_1)
+// spilled registers inside the step loop, q4_1 with heads of 128 one (256 columns) or 6 (128 columns); the others none.
 template <int NB, bool Q41, int NW, int KS>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows(AttnArgs a) {
     constexpr int dim = 32 * NB, unit_lds = 64 * dim, buffer = 2 * KS * unit_lds;   // fp16 bytes of a unit's K, or V; a step
@@ -1005,8 +1016,8 @@ namespace {
 // Workgroups that a shared-out call has, and the units that each takes at least.
 constexpr int kShareWorkgroups = kJoinParts, kShareLeast = 24;
 // Columns per sequence, on average, from which a call takes tiles of 128 or 256 columns: measured in us, tiles of 16 and
-// of 128, 16 sequences of 4096 tokens, 8 x 4 heads of 128: 64 columns 56 and 110, 128 columns 108 and 126; one of 65536
-// tokens, 64 columns 71 and 67, 256 columns 220 and 146.
+// of 128, 16 sequences of 4096 tokens, 8 x 4 heads of 128: 64 columns 60 and 121, 128 columns 110 and 122; one of 65536
+// tokens, 64 columns 69 and 71, 256 columns 214 and 199.
 constexpr int kManyCols = 129;
 // Tiles of 128 columns: with fewer (tiles x heads) than this their tokens are shared out; units that a part has at least.
 constexpr int kRowItems = 128, kRowLeast = 16;
@@ -1030,8 +1041,8 @@ Schedule schedule(const AttnArgs& a, bool share) {
     s.splits = 1;
     if (a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch) {
         // Twice as many columns share a conversion to fp16, with one workgroup per compute unit instead of two: in us, 256
-        // and 128 columns, 2048 rows of 8 x 4 heads of 128 over 18432 tokens 596 and 719, two prompts of 2048 rows 108 and
-        // 122, but 8 prompts of 700 rows, 12 heads of 96, 51 and 45, 4 of 1500, 20 heads of 64, 80 and 75.
+        // and 128 columns, 2048 rows of 8 x 4 heads of 128 over 18432 tokens 610 and 712, two prompts of 2048 rows 95 and
+        // 108, but 8 prompts of 700 rows, 12 heads of 96, 49 and 41, 4 of 1500, 20 heads of 64, 76 and 70.
         items(256);
         if (s.items < 256 || units < 64 || a.dim == 256) items(128);
         if (share && s.items <= kRowItems)
@@ -1039,8 +1050,9 @@ Schedule schedule(const AttnArgs& a, bool share) {
     } else {
         items(kTokenCols);
         // Shared out, and joined by a second launch, where a sequence can be long.  Measured in us, whole and shared out,
-        // 8 heads of 128: 8 tiles of 1024 tokens 11.2 and 17.0, of 2048 tokens 18 and 17.1; 256 tiles of 2048 24.8 and
-        // 30.2, of 4096 42.9 and 42.6, 288 tiles of 4096 42.9 and 48.9 (equal lengths: unequal ones only gain).  Work is counted in 32 bits.
+        // 8 heads of 128: 8 tiles of 1024 tokens 11.4 and 17.7, of 2048 tokens 17.9 and 17.4; 256 tiles of 2048 22 and 29,
+        // of 4096 34 and 42, of 8192 65 and 72, but 288 tiles of 4096, of which 64 share a compute unit, 57 and 46 (equal
+        // lengths: unequal ones only gain).  Work is counted in 32 bits.
         if (share && units > (s.items < 256 ? 64 : 128) && s.items * (units + kTileCost) <= 0x7FFFFFFF)
             s.workgroups = kShareWorkgroups;
     }
@@ -1094,8 +1106,8 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
         return hipGetLastError();
     }
     const dim3 grid((unsigned)(c.workgroups ? c.workgroups : c.items));
-    // With at most a tile per compute unit eight waves share a tile's tokens (1024 tokens, 8 tiles of 4 x 128: 13.0 ->
-    // 11.2 us; 80 tiles of 1500 x 64: 13.5 -> 10.7); with more, four (320 tiles of 1500 x 64: 21.0 -> 17.1 us).
+    // With at most a tile per compute unit eight waves share a tile's tokens (1024 tokens, 8 tiles of 4 x 128: 13.6 ->
+    // 11.4 us; 80 tiles of 1500 x 64: 12.3 -> 10.3); with more, four (320 tiles of 1500 x 64: 20.2 -> 16.5 us).
     const bool few = !c.workgroups && c.items <= 256;
     switch (a.dim) {
     case 64: few ? launch_token<2, 8, 3>(a, grid, s) : launch_token<2, 4, 4>(a, grid, s); break;

@@ -264,8 +264,8 @@ __device__ inline void store_some(GroupCodes& c, bool is_v, int u0, int b, int g
 }
 
 // Few rows per sequence: a thread takes 8 channels of four tokens, K or V (blockIdx.z), so that a whole group's words and
-// scales are whole stores.  Bound by the way to memory and back (lengths, pages, rows): one row of 20 heads of 64 3.4 us, 32
-// rows of 8 heads of 128 4.2 us.
+// scales are whole stores.  Bound by the way to memory and back (lengths, pages, rows): one row of 20 heads of 64 3.3-3.7 us,
+// 96 sequences of one row, 8 heads of 128, 4.2-4.9 us.
 template <bool Q41, bool F32, int NB>
 __global__ __launch_bounds__(256) void k_cache_write(Seqs s, int per_row, int groups_per_block, const void* __restrict__ k, int64_t ldk,
                                                      const void* __restrict__ v, int64_t ldv, uint8_t* __restrict__ cache) {
@@ -330,8 +330,9 @@ __global__ __launch_bounds__(NB == 3 ? 128 : 32 * NB) void k_cache_write_units(S
     for (int i = threadIdx.x; i < 2 * half / 16; i += threads) reinterpret_cast<u32x4*>(to)[i] = reinterpret_cast<const u32x4*>(lds)[i];
 }
 
-// A thread takes 8 channels of four tokens, K or V.  Bound by memory: 36176 rows of 8 heads of 128, q4_1 to bf16 (195 MB),
-// 40 us, 4.8 TB/s.
+// A thread takes 8 channels of four tokens, K or V.  36176 rows of 8 heads of 128, q4_1 to bf16 (195 MB), 40 us, 4.8 TB/s:
+// near the copy's 5.1, with the vector unit issuing in 87 % of the cycles.  Fewer rows are bound by each thread's chain of row
+// starts, lengths, table and unit: 4 x 1500 rows of 20 heads of 64, q4_0 to bf16 (39 MB), 13-15 us, where the bytes take 7.8.
 template <bool Q41, bool F32, int NB>
 __global__ __launch_bounds__(256) void k_cache_read(Seqs s, int per_row, int groups_per_block, const uint8_t* __restrict__ cache,
                                                     void* __restrict__ k, int64_t ldk, void* __restrict__ v, int64_t ldv) {
