@@ -34,7 +34,9 @@ SOURCES = [
     ("quant.hip", ["-ffp-contract=off"]),
     ("act.hip", ["-ffp-contract=off"]),
     ("cache.hip", ["-ffp-contract=off"]),
+    ("pages.hip", []),
     ("attn.hip", []),
+    ("attn_parts.hip", []),
     ("gemv.hip", []),
     ("gemm.hip", ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]),
     ("gemm_nvfp4_wide.hip", []),

@@ -85,6 +85,70 @@ __device__ inline void row_units(const AttnArgs& a, const SeqInfo& q, int i0, in
     *u1 = hi > lo ? (hi + kUnit - 1) / kUnit : *u0;
 }
 
+// The same with sinks, or of a tree of drafted tokens: the rows' units in ascending order, without those that no row sees.
+struct UnitList {
+    int far, near, count;    // units 0 .. far - 1, then near, near + 1 ...: `count` in all
+    __device__ int operator[](int i) const { return i < far ? i : i - far + near; }
+    // Whether units are left out between the i-th and the one `step` after it.
+    __device__ bool gap(int i, int step) const { return i < far && i + step >= far && near > far; }
+};
+
+// Tokens [lo, hi) that row i of the sequence sees besides sinks and drafted tokens: with a tree, those before the first row,
+// as far back as the window goes when the drafted tokens that the row sees (itself among them) are the nearest part of it.
+__device__ inline int drafts_seen(const AttnArgs& a, const SeqInfo& q, int i) {
+    const uint32_t* const w = a.tree + (int64_t)(q.r0 + i) * a.tree_ld;
+    int seen = 0;
+    for (int k = 0; k < a.tree_ld && k * 32 < q.n; k++) seen += __popc(q.n - k * 32 < 32 ? w[k] & ((1u << (q.n - k * 32)) - 1) : w[k]);
+    return seen;
+}
+__device__ inline int clamped(int64_t v, int most) { return v < 0 ? 0 : v < most ? (int)v : most; }
+__device__ inline void row_context(const AttnArgs& a, const SeqInfo& q, int i, int* lo, int* hi) {
+    if (!a.tree) return row_tokens(a, q, i, lo, hi);
+    *lo = 0;
+    *hi = clamped(q.pos0, q.tokens);
+    if (a.window > 0) *lo = clamped(q.pos0 + drafts_seen(a, q, i) - a.window, *hi);
+}
+// What rows [i0, i1] see all of: the tokens [lo_most, hi_least), at least.
+__device__ inline void parts_between(const AttnArgs& a, const SeqInfo& q, int i0, int i1, int* lo_most, int* hi_least) {
+    if (!a.tree) {
+        int x;
+        row_tokens(a, q, i0, &x, hi_least);
+        row_tokens(a, q, i1, lo_most, &x);
+        return;
+    }
+    *hi_least = clamped(q.pos0, q.tokens);
+    *lo_most = a.window > 0 ? clamped(q.pos0 + q.n - a.window, *hi_least) : 0;
+}
+// Units of rows [i0, i1).
+__device__ inline UnitList row_parts(const AttnArgs& a, const SeqInfo& q, int i0, int i1) {
+    int lo, hi, x, sinks;
+    if (a.tree) {
+        const int context = clamped(q.pos0, q.tokens);
+        lo = a.window > 0 ? clamped(q.pos0 - a.window, context) : 0;
+        hi = q.tokens;
+        sinks = min(a.sinks, context);
+    } else {
+        row_tokens(a, q, i0, &lo, &x);
+        row_tokens(a, q, i1 - 1, &x, &hi);
+        sinks = min(a.sinks, hi);
+    }
+    UnitList r;
+    r.near = lo / kUnit;
+    r.far = min((sinks + kUnit - 1) / kUnit, r.near);
+    r.count = r.far + (hi > lo ? (hi + kUnit - 1) / kUnit - r.near : 0);
+    return r;
+}
+// Which of the 32 tokens from t0 on are drafted ones that row i sees, a bit each.
+__device__ inline uint32_t seen_nodes(const AttnArgs& a, const SeqInfo& q, int i, int t0) {
+    if (!a.tree || t0 >= q.tokens || t0 + kUnit <= q.pos0) return 0;
+    const int64_t at = t0 - q.pos0;   // bit of token t0, -31 or more
+    const uint32_t* const w = a.tree + (int64_t)(q.r0 + i) * a.tree_ld;
+    const int64_t k = at >> 5;        // floor
+    const uint32_t low = k >= 0 && k < a.tree_ld ? w[k] : 0, high = k + 1 < a.tree_ld ? w[k + 1] : 0;   // (k >= -1)
+    const uint32_t bits = __builtin_amdgcn_alignbit(high, low, (uint32_t)at & 31);
+    return q.tokens - t0 < kUnit ? bits & ((1u << (q.tokens - t0)) - 1) : bits;
+}
+
 __device__ inline int tiles_of(const TileShape& ts, int n) { return (n + ts.rows - 1) / ts.rows * ts.ht; }
 
 struct TileCount {
@@ -133,6 +197,12 @@ struct UnitWalk {
         const int entry = __builtin_amdgcn_readlane(entries, j - j0);
         there = (unsigned)entry < (unsigned)pages;
         cur = there ? ((int64_t)entry * per_page + (head_units + k)) * unit_bytes : 0;
+    }
+    __device__ void seek(int unit) {   // on to a later unit
+        j = uniform(unit / upp);
+        k = unit - j * upp;
+        if (j - j0 >= 64) hold();
+        place();
     }
     __device__ void step(int n) {
         k += n;

@@ -387,6 +387,100 @@ __global__ __launch_bounds__(256) void k_cache_read(Seqs s, int per_row, int gro
 
 namespace {
 
+// What a token's row of one head has in K's or V's part of a unit, in pieces of one size: K's words of 8 channels, V's bytes
+// of 2, and its scales.  A piece's place goes by the token's place in the unit.
+template <bool Q41, int NB>
+struct Pieces {
+    static constexpr int dim = 32 * NB, half = cache_half_bytes(Q41, dim), scales = NB * (Q41 ? 2 : 1);
+    static constexpr int words = 4 * NB, bytes = 16 * NB, all = words + bytes + 2 * scales, threads = (all + 63) / 64 * 64;
+    static __device__ int at(int i, int u, int* size) {
+        if (i < words) {
+            *size = 4;
+            return cache_k_word(NB, u, i >> 2, i & 3);
+        }
+        if ((i -= words) < bytes) {
+            *size = 1;
+            return half + cache_v_byte(NB, u, i >> 4, i & 15);
+        }
+        i -= bytes;
+        *size = 2;
+        const int v = i >= scales ? 1 : 0;
+        i -= v * scales;
+        return v * half + 16 * dim + (i >= NB ? cache_plane_bytes(dim) : 0) + 2 * cache_scale(NB, u, i >= NB ? i - NB : i);
+    }
+};
+constexpr int kKeepAtOnce = 64;   // path entries whose places are looked up together, one a lane
+
+}  // namespace
+
+// The accepted rows of a draft, moved to the places behind its context, a workgroup per sequence, head and pool.  A thread
+// has one piece of a row, and moves it for one entry of the path after the other: an entry's source lies behind all places
+// that earlier entries were moved to (a path ascends), so whole groups are read before they are written.
+template <bool Q41, int NB>
+__global__ __launch_bounds__((Pieces<Q41, NB>::threads)) void k_cache_keep(KeepArgs a) {
+    __shared__ int64_t from[kKeepAtOnce], to[kKeepAtOnce];
+    __shared__ int from_u[kKeepAtOnce], to_u[kKeepAtOnce];
+    const Seqs& s = a.s;
+    const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63;
+    uint8_t* const cache = a.cache[blockIdx.z];
+    int r0, r1;
+    seq_rows(s, b, &r0, &r1);
+    const int n = r1 - r0;
+    const int64_t pos0 = (int64_t)s.len[b] - n, capacity = (int64_t)s.table_ld * s.page;
+    const int count = min(a.count[b], a.path_ld);
+    const int32_t* const path = a.path + (int64_t)b * a.path_ld;
+    int size, kept = 0;
+    for (int j0 = 0; j0 < count; j0 += kKeepAtOnce) {
+        // the path ends before an entry that is no row, is not above the one before it, or has no place to be or to go
+        const int j = j0 + lane;
+        int64_t source = -1, target = -1;
+        int su = 0, tu = 0;
+        if (j < count) {
+            const int i = path[j], last = j > 0 ? path[j - 1] : -1;
+            const int64_t st = pos0 + i, tt = pos0 + j;
+            if (i > last && i >= 0 && i < n && tt >= 0 && st < capacity) {
+                source = seq_unit(s, b, h, (int)st);
+                target = seq_unit(s, b, h, (int)tt);
+                su = (int)st % s.page % kUnit;
+                tu = (int)tt % s.page % kUnit;
+            }
+        }
+        const uint64_t good = __ballot(source >= 0 && target >= 0);
+        const int m = good == ~0ull ? kKeepAtOnce : __builtin_ctzll(~good);
+        __syncthreads();
+        if (threadIdx.x < kKeepAtOnce) {
+            from[lane] = source;
+            to[lane] = target;
+            from_u[lane] = su;
+            to_u[lane] = tu;
+        }
+        __syncthreads();
+        constexpr int group = 8;
+        for (int k0 = 0; k0 < m && threadIdx.x < Pieces<Q41, NB>::all; k0 += group) {
+            uint32_t v[group];
+#pragma unroll
+            for (int k = 0; k < group; k++) {
+                if (k0 + k >= m) break;
+                const uint8_t* const p = cache + from[k0 + k] + Pieces<Q41, NB>::at(threadIdx.x, from_u[k0 + k], &size);
+                v[k] = size == 4 ? *reinterpret_cast<const uint32_t*>(p) : size == 2 ? *reinterpret_cast<const uint16_t*>(p) : *p;
+            }
+#pragma unroll
+            for (int k = 0; k < group; k++) {
+                if (k0 + k >= m) break;
+                uint8_t* const p = cache + to[k0 + k] + Pieces<Q41, NB>::at(threadIdx.x, to_u[k0 + k], &size);
+                if (size == 4) *reinterpret_cast<uint32_t*>(p) = v[k];
+                else if (size == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)v[k];
+                else *p = (uint8_t)v[k];
+            }
+        }
+        kept += m;
+        if (m < kKeepAtOnce) break;
+    }
+    if (threadIdx.x == 0 && h == 0 && blockIdx.z == 0 && a.want) a.want[b] = (int)max(pos0 + kept, (int64_t)0);
+}
+
+namespace {
+
 // Rows per sequence, on average, from which whole units are written.
 constexpr int64_t kManyRows = 16;
 
@@ -449,6 +543,23 @@ hipError_t launch_cache_write(const Seqs& q, bool q41, int dim, bool f32, const 
     case 96: write_nb<3>(q, q41, f32, k, ldk, v, ldv, cache, s); break;
     case 128: write_nb<4>(q, q41, f32, k, ldk, v, ldv, cache, s); break;
     default: write_nb<8>(q, q41, f32, k, ldk, v, ldv, cache, s); break;
+    }
+    return hipGetLastError();
+}
+
+template <int NB>
+void keep_nb(const KeepArgs& a, bool q41, hipStream_t s) {
+    const dim3 grid((unsigned)a.s.batch, (unsigned)a.s.heads, (unsigned)a.caches);
+    if (q41) hipLaunchKernelGGL((k_cache_keep<true, NB>), grid, dim3(Pieces<true, NB>::threads), 0, s, a);
+    else hipLaunchKernelGGL((k_cache_keep<false, NB>), grid, dim3(Pieces<false, NB>::threads), 0, s, a);
+}
+
+hipError_t launch_cache_keep(const KeepArgs& a, bool q41, int dim, hipStream_t s) {
+    switch (dim) {
+    case 64: keep_nb<2>(a, q41, s); break;
+    case 96: keep_nb<3>(a, q41, s); break;
+    case 128: keep_nb<4>(a, q41, s); break;
+    default: keep_nb<8>(a, q41, s); break;
     }
     return hipGetLastError();
 }

@@ -196,9 +196,11 @@ wq_status check_cache(const wq_cache_desc* d, wq::Seqs* q, bool* q41) {
     return WQ_OK;
 }
 
+constexpr int32_t kMaxBatch = 1 << 20;
+
 wq_status check_seqs(const wq_seqs* s, wq::Seqs* q) {
     if (!s || s->reserved != 0) return WQ_ERR_INVALID_ARG;
-    if (s->batch < 0 || s->batch > (1 << 20) || s->rows < 0) return WQ_ERR_SHAPE;
+    if (s->batch < 0 || s->batch > kMaxBatch || s->rows < 0) return WQ_ERR_SHAPE;
     if (!s->len) return WQ_ERR_INVALID_ARG;
     if (!aligned(s->len, 4) || !aligned(s->table, 4) || !aligned(s->row_start, 4)) return WQ_ERR_ALIGNMENT;
     if (!s->row_start && s->rows < s->batch) return WQ_ERR_SHAPE;
@@ -244,6 +246,46 @@ wq_status check_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, 
     a->dim = d->head_dim;
     if (a->s.rows > 0 && a->s.batch > 0 && !wq::attn_fits(*a)) return WQ_ERR_SHAPE;
     return WQ_OK;
+}
+
+// The same for rows that see first tokens and a window, or a tree.
+wq_status check_parts(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks, wq::AttnArgs* a) {
+    a->parts = true;
+    a->causal = true;
+    a->window = std::max(window, 0);   // (a negative one is refused later, in the order of the other checks)
+    a->sinks = std::max(sinks, 0);
+    return check_attn(d, s, q_heads, a);
+}
+constexpr int32_t kMaxTreeWords = 1 << 16;
+bool tree_window_ok(int32_t window, int32_t sinks) { return window >= 0 && sinks >= 0 && (window > 0 || sinks == 0); }
+
+// The checks that attention's entry points share, after those of the descriptor, sequences and heads (a has their results and
+// what a row sees), and the launch.  seen: the status of what a row sees.
+wq_status run_attn(wq::AttnArgs* a, const wq_cache_desc* d, int32_t q_heads, const uint16_t* q, int64_t ldq, const void* cache,
+                   float scale, wq_status seen, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    const int64_t width = (int64_t)q_heads * d->head_dim;
+    wq_status st;
+    if ((st = check_rows(q, ldq, width)) != WQ_OK) return st;
+    if ((st = check_rows(y, ldy, width)) != WQ_OK) return st;
+    if (!cache) return WQ_ERR_INVALID_ARG;
+    if (!aligned(cache, 16)) return WQ_ERR_ALIGNMENT;
+    if (!std::isfinite(scale * 1.44269504088896340736f)) return WQ_ERR_INVALID_ARG;
+    if (seen != WQ_OK) return seen;
+    if (a->s.rows == 0 || a->s.batch == 0) return WQ_OK;
+    if (ws) {
+        if (!aligned(ws, 16)) return WQ_ERR_ALIGNMENT;
+        if (ws_bytes < wq::attn_workspace_bytes(*a)) return WQ_ERR_WORKSPACE;
+    }
+    // (a tile's queries are read when another tile's rows may be written already)
+    if (windows_overlap(q, ldq, width, y, ldy, width, a->s.rows, 2)) return WQ_ERR_INVALID_ARG;
+    a->q = q;
+    a->ldq = ldq;
+    a->cache = static_cast<const uint8_t*>(cache);
+    a->y = y;
+    a->ldy = ldy;
+    a->ws = static_cast<uint8_t*>(ws);
+    a->scale_log2 = scale * 1.44269504088896340736f;
+    return from_hip(wq::launch_attn(*a, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -508,31 +550,106 @@ wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, con
     wq::AttnArgs a{};
     wq_status st = check_attn(d, s, q_heads, &a);
     if (st != WQ_OK) return st;
-    const int64_t width = (int64_t)q_heads * d->head_dim;
-    if ((st = check_rows(q, ldq, width)) != WQ_OK) return st;
-    if ((st = check_rows(y, ldy, width)) != WQ_OK) return st;
-    if (!cache) return WQ_ERR_INVALID_ARG;
-    if (!aligned(cache, 16)) return WQ_ERR_ALIGNMENT;
-    if (!std::isfinite(scale * 1.44269504088896340736f)) return WQ_ERR_INVALID_ARG;
-    if (causal != 0 && causal != 1) return WQ_ERR_INVALID_ARG;
-    if (window < 0 || (window > 0 && !causal)) return WQ_ERR_INVALID_ARG;
-    if (a.s.rows == 0 || a.s.batch == 0) return WQ_OK;
-    if (ws) {
-        if (!aligned(ws, 16)) return WQ_ERR_ALIGNMENT;
-        if (ws_bytes < wq::attn_workspace_bytes(a)) return WQ_ERR_WORKSPACE;
-    }
-    // (a tile's queries are read when another tile's rows may be written already)
-    if (windows_overlap(q, ldq, width, y, ldy, width, a.s.rows, 2)) return WQ_ERR_INVALID_ARG;
-    a.q = q;
-    a.ldq = ldq;
-    a.cache = static_cast<const uint8_t*>(cache);
-    a.y = y;
-    a.ldy = ldy;
-    a.ws = static_cast<uint8_t*>(ws);
-    a.scale_log2 = scale * 1.44269504088896340736f;
     a.causal = causal == 1;
     a.window = window;
-    return from_hip(wq::launch_attn(a, static_cast<hipStream_t>(stream)));
+    const bool seen = (causal == 0 || causal == 1) && window >= 0 && (window == 0 || causal);
+    return run_attn(&a, d, q_heads, q, ldq, cache, scale, seen ? WQ_OK : WQ_ERR_INVALID_ARG, y, ldy, ws, ws_bytes, stream);
+}
+
+wq_status wq_attn_sinks_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks,
+                                       size_t* bytes) {
+    wq::AttnArgs a{};
+    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    if (st != WQ_OK) return st;
+    if (window < 1 || sinks < 0 || !bytes) return WQ_ERR_INVALID_ARG;
+    *bytes = a.s.rows == 0 || a.s.batch == 0 ? 0 : wq::attn_workspace_bytes(a);
+    return WQ_OK;
+}
+
+wq_status wq_attn_sinks(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq,
+                        const void* cache, float scale, int32_t window, int32_t sinks, uint16_t* y, int64_t ldy, void* ws,
+                        size_t ws_bytes, void* stream) {
+    wq::AttnArgs a{};
+    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    if (st != WQ_OK) return st;
+    const bool seen = window >= 1 && sinks >= 0;
+    return run_attn(&a, d, q_heads, q, ldq, cache, scale, seen ? WQ_OK : WQ_ERR_INVALID_ARG, y, ldy, ws, ws_bytes, stream);
+}
+
+wq_status wq_attn_tree_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks,
+                                      size_t* bytes) {
+    wq::AttnArgs a{};
+    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    if (st != WQ_OK) return st;
+    if (!tree_window_ok(window, sinks) || !bytes) return WQ_ERR_INVALID_ARG;
+    *bytes = a.s.rows == 0 || a.s.batch == 0 ? 0 : wq::attn_workspace_bytes(a);
+    return WQ_OK;
+}
+
+wq_status wq_attn_tree(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq,
+                       const void* cache, float scale, int32_t window, int32_t sinks, const uint32_t* tree, int32_t tree_ld,
+                       uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    wq::AttnArgs a{};
+    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    if (st != WQ_OK) return st;
+    if (!tree_window_ok(window, sinks) || !tree || tree_ld < 1 || tree_ld > kMaxTreeWords) st = WQ_ERR_INVALID_ARG;
+    else if (!aligned(tree, 4)) st = WQ_ERR_ALIGNMENT;
+    a.tree = tree;
+    a.tree_ld = tree_ld;
+    return run_attn(&a, d, q_heads, q, ldq, cache, scale, st, y, ldy, ws, ws_bytes, stream);
+}
+
+wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream) {
+    if (pages < 1 || pages > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+    if (!pool) return WQ_ERR_INVALID_ARG;
+    if (!aligned(pool, 4)) return WQ_ERR_ALIGNMENT;
+    return from_hip(wq::launch_pages_init((int)pages, pool, static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, const int32_t* want, int32_t* table,
+                          int32_t table_ld, int32_t* pool, int32_t rows, int32_t* row_start, int32_t* pos, int64_t* slot,
+                          void* stream) {
+    wq::Seqs q{};
+    bool q41;
+    wq_status st = check_cache(d, &q, &q41);
+    if (st != WQ_OK) return st;
+    if (batch < 0 || batch > kMaxBatch || rows < 0) return WQ_ERR_SHAPE;
+    if (!len || !want || !table || !pool || !row_start || table_ld < 1) return WQ_ERR_INVALID_ARG;
+    if (!aligned(len, 4) || !aligned(want, 4) || !aligned(table, 4) || !aligned(pool, 4) || !aligned(row_start, 4) ||
+        !aligned(pos, 4) || !aligned(slot, 8))
+        return WQ_ERR_ALIGNMENT;
+    if ((int64_t)table_ld * q.page > 0x7FFFFFFF) return WQ_ERR_SHAPE;
+    if (want == len) return WQ_ERR_INVALID_ARG;   // (lengths are written while others are still read)
+    if (batch == 0) return WQ_OK;
+    const wq::PagesArgs a = {len, want, table, pool, row_start, pos, slot, batch, table_ld, q.page, (int)q.pages, rows};
+    return from_hip(wq::launch_pages_assign(a, static_cast<hipStream_t>(stream)));
+}
+
+wq_status wq_cache_keep(const wq_cache_desc* d, const wq_seqs* s, const int32_t* path, int32_t path_ld, const int32_t* count,
+                        void* const* caches, int32_t n_caches, int32_t* want, void* stream) {
+    wq::KeepArgs a{};
+    bool q41;
+    wq_status st = check_cache(d, &a.s, &q41);
+    if (st != WQ_OK) return st;
+    if ((st = check_seqs(s, &a.s)) != WQ_OK) return st;
+    if (!path || !count || !caches || path_ld < 1 || n_caches < 1) return WQ_ERR_INVALID_ARG;
+    if (n_caches > wq::kKeepCaches) return WQ_ERR_UNSUPPORTED;
+    if (!aligned(path, 4) || !aligned(count, 4) || !aligned(want, 4)) return WQ_ERR_ALIGNMENT;
+    for (int i = 0; i < n_caches; i++) {
+        if (!caches[i]) return WQ_ERR_INVALID_ARG;
+        if (!aligned(caches[i], 16)) return WQ_ERR_ALIGNMENT;
+        for (int j = 0; j < i; j++)
+            if (caches[i] == caches[j]) return WQ_ERR_INVALID_ARG;   // its rows would be moved twice
+        a.cache[i] = static_cast<uint8_t*>(caches[i]);
+    }
+    if (want && want == s->len) return WQ_ERR_INVALID_ARG;           // (other workgroups still read the lengths)
+    if (a.s.batch == 0) return WQ_OK;
+    a.path = path;
+    a.path_ld = path_ld;
+    a.count = count;
+    a.want = want;
+    a.caches = n_caches;
+    return from_hip(wq::launch_cache_keep(a, q41, d->head_dim, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

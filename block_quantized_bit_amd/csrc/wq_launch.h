@@ -79,6 +79,32 @@ hipError_t launch_cache_write(const Seqs& q, bool q41, int dim, bool f32, const 
 hipError_t launch_cache_read(const Seqs& q, bool q41, int dim, bool f32, const uint8_t* cache, void* k, int64_t ldk,
                              void* v, int64_t ldv, hipStream_t s);
 
+// Rows of drafts moved to where a path says (cache.hip): row path[b][j] of sequence b to its place j.
+constexpr int kKeepCaches = 64;   // pools of one call: their addresses are kernel arguments
+struct KeepArgs {
+    Seqs s;
+    const int32_t* path;
+    const int32_t* count;
+    int32_t* want;
+    int32_t path_ld, caches;
+    uint8_t* cache[kKeepCaches];
+};
+hipError_t launch_cache_keep(const KeepArgs& a, bool q41, int dim, hipStream_t s);
+
+// Pages of sequences (pages.hip).
+struct PagesArgs {
+    int32_t* len;          // [batch]
+    const int32_t* want;   // [batch]
+    int32_t* table;        // [batch][table_ld]
+    int32_t* pool;         // free pages, pages lacking, two words of the kernel's own, the list: the next page to take last
+    int32_t* row_start;    // [batch + 1]
+    int32_t* pos;          // [rows], or null
+    int64_t* slot;         // [rows], or null
+    int32_t batch, table_ld, page, pages, rows;
+};
+hipError_t launch_pages_init(int pages, int32_t* pool, hipStream_t s);
+hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s);
+
 // Attention over the cache (attn.hip).
 struct AttnArgs {
     Seqs s;
@@ -95,9 +121,16 @@ struct AttnArgs {
     int32_t splits;        // tiles of 128 columns: parts that each tile's tokens are shared out in
     int32_t slots;         // partial results that the workspace holds
     bool q41, causal;
+    bool parts;            // a row sees parts: the two below, or a tree
+    int32_t sinks;         // first tokens that stay visible
+    int32_t tree_ld;       // words of a row's mask
+    const uint32_t* tree;  // null: the rows are no tree
 };
 bool attn_fits(const AttnArgs& a);
 size_t attn_workspace_bytes(const AttnArgs& a);
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
+// Of its kernels, those for rows that see parts (attn_parts.hip): tiles of 16 columns, few of them; of 128 or 256 columns.
+void launch_parts_token(const AttnArgs& a, dim3 grid, bool few, hipStream_t s);
+void launch_parts_rows(const AttnArgs& a, dim3 grid, bool wide, hipStream_t s);
 
 }  // namespace wq

@@ -23,7 +23,9 @@ WQ_BF16, WQ_F32 = 1, 2
 EXPORTS = ("wq_status_str", "wq_packed_size", "wq_quantize", "wq_dequantize",
            "wq_workspace_size", "wq_matmul", "wq_matmul_noalloc", "wq_matmul_qkv",
            "wq_act_packed_size", "wq_quantize_act", "wq_w4a4_workspace_size", "wq_matmul_w4a4",
-           "wq_cache_size", "wq_cache_write", "wq_cache_read", "wq_attn_workspace_size", "wq_attn")
+           "wq_cache_size", "wq_cache_write", "wq_cache_read", "wq_attn_workspace_size", "wq_attn",
+           "wq_attn_sinks_workspace_size", "wq_attn_sinks", "wq_attn_tree_workspace_size", "wq_attn_tree",
+           "wq_pages_init", "wq_pages_assign", "wq_cache_keep")
 
 # Format names accepted by the harness; aliases follow the NF4 option's names
 # ("asr: add a 4-bit nf4 option for the Whisper engine": nf4, aliases 4bit, int4).
@@ -194,6 +196,19 @@ def lib():
         L.wq_attn_workspace_size.argtypes = [pc, ps, i32, ctypes.POINTER(sz)]
         L.wq_attn.restype = ctypes.c_int
         L.wq_attn.argtypes = [pc, ps, i32, P, i64, P, ctypes.c_float, i32, i32, P, i64, P, sz, P]
+        for f in (L.wq_attn_sinks_workspace_size, L.wq_attn_tree_workspace_size):
+            f.restype = ctypes.c_int
+            f.argtypes = [pc, ps, i32, i32, i32, ctypes.POINTER(sz)]
+        L.wq_attn_sinks.restype = ctypes.c_int
+        L.wq_attn_sinks.argtypes = [pc, ps, i32, P, i64, P, ctypes.c_float, i32, i32, P, i64, P, sz, P]
+        L.wq_attn_tree.restype = ctypes.c_int
+        L.wq_attn_tree.argtypes = [pc, ps, i32, P, i64, P, ctypes.c_float, i32, i32, P, i32, P, i64, P, sz, P]
+        L.wq_pages_init.restype = ctypes.c_int
+        L.wq_pages_init.argtypes = [i64, P, P]
+        L.wq_pages_assign.restype = ctypes.c_int
+        L.wq_pages_assign.argtypes = [pc, i32, P, P, P, i32, P, i32, P, P, P, P]
+        L.wq_cache_keep.restype = ctypes.c_int
+        L.wq_cache_keep.argtypes = [pc, ps, P, i32, P, ctypes.POINTER(P), i32, P, P]
         _lib = L
     return _lib
 
@@ -339,3 +354,75 @@ def wq_attn(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scal
     return _call_on("wq_attn", s, (q, cache, y, ws), stream, check, lib().wq_attn, ctypes.byref(d), ctypes.byref(s),
                     _int32("wq_attn", "q_heads", q_heads), _ptr(q), ldq, _ptr(cache), scale, _int32("wq_attn", "causal", causal),
                     _int32("wq_attn", "window", window), _ptr(y), ldy, _ptr(ws), ws_bytes)
+
+
+def _attn_size(where: str, fn, d: wq_cache_desc, s: wq_seqs, q_heads: int, window: int, sinks: int) -> int:
+    b = ctypes.c_size_t()
+    _check(fn(ctypes.byref(d), ctypes.byref(s), _int32(where, "q_heads", q_heads), _int32(where, "window", window),
+              _int32(where, "sinks", sinks), ctypes.byref(b)), where, True)
+    return b.value
+
+
+def wq_attn_sinks_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int, window: int, sinks: int) -> int:
+    return _attn_size("wq_attn_sinks_workspace_size", lib().wq_attn_sinks_workspace_size, d, s, q_heads, window, sinks)
+
+
+def wq_attn_sinks(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scale: float, window: int, sinks: int, y,
+                  ldy: int, ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
+    return _call_on("wq_attn_sinks", s, (q, cache, y, ws), stream, check, lib().wq_attn_sinks, ctypes.byref(d), ctypes.byref(s),
+                    _int32("wq_attn_sinks", "q_heads", q_heads), _ptr(q), ldq, _ptr(cache), scale,
+                    _int32("wq_attn_sinks", "window", window), _int32("wq_attn_sinks", "sinks", sinks), _ptr(y), ldy, _ptr(ws),
+                    ws_bytes)
+
+
+def wq_attn_tree_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int, window: int, sinks: int) -> int:
+    return _attn_size("wq_attn_tree_workspace_size", lib().wq_attn_tree_workspace_size, d, s, q_heads, window, sinks)
+
+
+def wq_attn_tree(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scale: float, window: int, sinks: int, tree,
+                 tree_ld: int, y, ldy: int, ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
+    """`tree`: a contiguous int32 or uint32 tensor of at least rows * tree_ld words, or a device address."""
+    _words("wq_attn_tree", "tree", tree, s.rows * tree_ld)
+    return _call_on("wq_attn_tree", s, (q, cache, tree, y, ws), stream, check, lib().wq_attn_tree, ctypes.byref(d), ctypes.byref(s),
+                    _int32("wq_attn_tree", "q_heads", q_heads), _ptr(q), ldq, _ptr(cache), scale,
+                    _int32("wq_attn_tree", "window", window), _int32("wq_attn_tree", "sinks", sinks), _ptr(tree),
+                    _int32("wq_attn_tree", "tree_ld", tree_ld), _ptr(y), ldy, _ptr(ws), ws_bytes)
+
+
+def _words(where: str, name: str, t, n: int, types=("torch.int32", "torch.uint32")):
+    """Refuses a tensor that is not n contiguous elements, at least, of one of the types."""
+    if t is None or isinstance(t, int):
+        return
+    if str(t.dtype) not in types or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous {types[0][6:]} tensor, got {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{where}: {name} has {t.numel()} entries; {n} are needed")
+
+
+def wq_pages_init(pages: int, pool, stream=None, check=True) -> int:
+    _words("wq_pages_init", "pool", pool, 4 + pages)
+    return _call_on("wq_pages_init", None, (pool,), stream, check, lib().wq_pages_init, int(pages), _ptr(pool))
+
+
+def wq_pages_assign(d: wq_cache_desc, batch: int, len, want, table, table_ld: int, pool, rows: int, row_start, pos=None,  # noqa: A002
+                    slot=None, stream=None, check=True) -> int:
+    """The arrays are contiguous int32 tensors (`slot` int64) of at least the entries that the call touches, or device
+    addresses."""
+    for name, t, n in (("len", len, batch), ("want", want, batch), ("table", table, batch * table_ld), ("pool", pool, 4 + d.pages),
+                       ("row_start", row_start, batch + 1), ("pos", pos, rows)):
+        _words("wq_pages_assign", name, t, n)
+    _words("wq_pages_assign", "slot", slot, rows, ("torch.int64",))
+    return _call_on("wq_pages_assign", None, (len, want, table, pool, row_start, pos, slot), stream, check, lib().wq_pages_assign,
+                    ctypes.byref(d), _int32("wq_pages_assign", "batch", batch), _ptr(len), _ptr(want), _ptr(table),
+                    _int32("wq_pages_assign", "table_ld", table_ld), _ptr(pool), _int32("wq_pages_assign", "rows", rows),
+                    _ptr(row_start), _ptr(pos), _ptr(slot))
+
+
+def wq_cache_keep(d: wq_cache_desc, s: wq_seqs, path, path_ld: int, count, caches, want=None, stream=None, check=True) -> int:
+    """`caches`: a list of the layers' cache buffers; `path`, `count`, `want`: contiguous int32 tensors or device addresses."""
+    for name, t, n in (("path", path, s.batch * path_ld), ("count", count, s.batch), ("want", want, s.batch)):
+        _words("wq_cache_keep", name, t, n)
+    pools = (ctypes.c_void_p * len(caches))(*[_ptr(c) for c in caches])
+    return _call_on("wq_cache_keep", s, (path, count, want, *caches), stream, check, lib().wq_cache_keep, ctypes.byref(d),
+                    ctypes.byref(s), _ptr(path), _int32("wq_cache_keep", "path_ld", path_ld), _ptr(count), pools, len(caches),
+                    _ptr(want))

@@ -371,6 +371,104 @@ wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, con
                   float scale, int32_t causal, int32_t window, uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes,
                   void* stream);
 
+/* ---- Sequences without an end, and drafts: sinks, trees, pages -------------------
+ * A step of serving with drafted tokens over the cache, all of it on the GPU and the same
+ * calls every time (so that one captured graph serves all steps):
+ *   wq_pages_assign   the sequences' new lengths -> pages, block table, row starts, positions
+ *   wq_cache_write    the drafts' keys and values
+ *   wq_attn_tree      (or wq_attn_sinks, wq_attn)
+ *   wq_cache_keep     the accepted rows moved into place, in every layer's cache
+ *   wq_pages_assign   back to the accepted length (the next step's first call does it too) */
+
+/* Host-only.  Workspace bytes wq_attn_sinks can use for such a call, as
+ * wq_attn_workspace_size; window and sinks as for the call. */
+wq_status wq_attn_sinks_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks,
+                                       size_t* bytes);
+
+/* wq_attn (causal) for sequences whose first tokens stay visible: the row at token p sees
+ * the tokens t <= p with t > p - window or t < sinks.
+ *   window : 1 .., tokens of the sliding window (the row's own among them)
+ *   sinks  : 0 .., first tokens of a sequence that every row at or behind them sees
+ * All else (arguments, refusals, rounding and error bound) as for wq_attn.  Tokens between
+ * the sinks and the window are not read. */
+wq_status wq_attn_sinks(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq,
+                        const void* cache, float scale, int32_t window, int32_t sinks, uint16_t* y, int64_t ldy, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* Host-only.  The same for wq_attn_tree. */
+wq_status wq_attn_tree_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks,
+                                      size_t* bytes);
+
+/* Attention of drafted tokens that form a tree.  A sequence's rows are its drafted tokens
+ * (its last ones, as ever, already written into the cache), its other tokens the context.
+ * A row sees the context and those of the sequence's rows that its mask says: its ancestors
+ * and itself, or whatever the caller's tree is.
+ *   tree    : device [rows][tree_ld] 32-bit words: bit j % 32 of word j / 32 of row r says
+ *             whether it sees row j of its sequence.  Bits for rows that the sequence does
+ *             not have are ignored; rows 32 * tree_ld and later are seen by none
+ *   tree_ld : 1 .. 65536 words per row
+ *   window  : 0: a row sees all of the context; > 0: its last window - n tokens, n being
+ *             how many rows it sees (they are the nearest part of its window, and seen
+ *             whatever n is)
+ *   sinks   : with a window, the context's first `sinks` tokens are seen too; else 0
+ * A row that sees nothing gets zeros.  The masks are read when the work runs.  All else as
+ * for wq_attn. */
+wq_status wq_attn_tree(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq,
+                       const void* cache, float scale, int32_t window, int32_t sinks, const uint32_t* tree, int32_t tree_ld,
+                       uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* A pool's free pages: device int32 [4 + pages].  Word 0 is how many are free, word 1 how
+ * many the last wq_pages_assign lacked, words 2 and 3 are the library's own (0 between
+ * calls); then the list, the next page to be taken last.  What lies behind the list's end
+ * is anything.  wq_pages_init makes all pages free, page 0 the first to be taken; a caller
+ * may also write such an array itself.  pages: 1 .. 2^31 - 1. */
+wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
+
+/* Lengths become what is wanted: sequence b, of len[b] tokens, gets or gives back pages so
+ * that its table has ceil(want[b] / page) of them, and len[b] becomes want[b].  One call
+ * serves sequences that grow, shrink and end (want 0) alike.
+ *   d         : of the cache(s); its page and pages are what counts
+ *   batch     : sequences, 0 .. 2^20
+ *   len       : device int32 [batch], in and out
+ *   want      : device int32 [batch], an array of its own
+ *   table     : device int32 [batch][table_ld], in and out; the entries of pages that a
+ *               sequence does not have are neither read nor written.  No page may be in
+ *               two sequences' tables
+ *   pool      : the free pages, in and out (above)
+ *   rows      : rows of the batch, 0 ..: what pos and slot have room for, and the most that
+ *               a row start says
+ *   row_start : device int32 [batch + 1], out: the sequences that grow have
+ *               want[b] - len[b] rows each, in order (as wq_seqs takes it), the others none
+ *   pos       : device int32 [rows] or NULL, out: the token that a row is, in its sequence
+ *   slot      : device int64 [rows] or NULL, out: page * (entry of the table) + the token's
+ *               place in the page; -1 where it has no page.  Entries of pos and slot
+ *               behind the last sequence's rows are left as they were
+ * The free pages form a queue: those given back go to its front, in the order of sequences
+ * and their pages, then the wanted ones are taken from its front in the same order; so what a
+ * call has taken, a call that takes it back puts where it was, and the result does not
+ * depend on timing.  Where there are not enough, the last wanted ones' entries become -1
+ * (their tokens are absent: see wq_seqs) and word 1 of the pool says how many; tokens past
+ * table_ld pages are absent too.  Negative lengths count as 0; entries that are no page are
+ * not given back. */
+wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, const int32_t* want, int32_t* table,
+                          int32_t table_ld, int32_t* pool, int32_t rows, int32_t* row_start, int32_t* pos, int64_t* slot,
+                          void* stream);
+
+/* Of each sequence's rows (its last tokens) keep those on its path: row path[b][j] is moved
+ * to the place of its row j, for j < count[b], bit for bit, in the caches of all layers.
+ *   path     : device int32 [batch][path_ld], ascending rows of the sequence, from 0.  A path
+ *              ends before an entry that is no row of the sequence, is not above the one
+ *              before it, or whose token or place is absent (see wq_seqs)
+ *   path_ld  : 1 ..
+ *   count    : device int32 [batch], entries of each path (at most path_ld count)
+ *   caches   : host array of n_caches different device buffers of descriptor d, 16-byte aligned
+ *   n_caches : 1 .. 64 (else WQ_ERR_UNSUPPORTED)
+ *   want     : device int32 [batch] or NULL, out: the tokens of each sequence that are then
+ *              in place, its context and the kept rows: what wq_pages_assign takes next
+ * The places of rows that are not kept hold anything that was there before or was moved. */
+wq_status wq_cache_keep(const wq_cache_desc* d, const wq_seqs* s, const int32_t* path, int32_t path_ld, const int32_t* count,
+                        void* const* caches, int32_t n_caches, int32_t* want, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
