@@ -2,6 +2,8 @@
 // end, with the block table, the row starts and the rows' places that the other calls take.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "cache_device.h"
 #include "wq_launch.h"
 
@@ -45,9 +47,186 @@ __global__ __launch_bounds__(256) void k_pages_init(int pages, int32_t* pool) {
     if (i < (uint32_t)pages) pool[4 + (int64_t)i] = pages - 1 - (int)i;
 }
 
-// One workgroup.  First what is given back goes on the list's end (its front), the first sequence's first page last; then what
-// is wanted is taken from there.
+// The call in one launch, for up to kSeqsAtOnce sequences.  Every workgroup makes the sums over all sequences for itself, in LDS
+// (rows, pages wanted, pages given back, each before a sequence), and then does its share of the rows, of the table's new
+// entries and of the list's.  Nothing that a workgroup reads is written by another: the page of a wanted entry comes from the
+// entry that is given back or from the list itself, not from the table; what is put on the list goes where nothing was; and
+// the lengths and counts are written by the workgroup that is the last to be done with reading.
+constexpr int kSeqsAtOnce = 8192, kRowsPerThread = 4;
+
+// a + b, at most `most`: associative for numbers that are at most that.
+__device__ inline uint32_t add_to(uint32_t a, uint32_t b, uint32_t most) { return min(a + b, most); }
+
+struct PagesLds {
+    uint32_t wave[3][kThreads / 64];
+    int last;
+    uint32_t row[kSeqsAtOnce + 1], come[kSeqsAtOnce + 1], gone[kSeqsAtOnce + 1];   // before a sequence
+};
+
+// The last sequence whose sum before it is at most i (that has the i-th item, for an i below the total).
+__device__ inline int holder(const uint32_t* before, int batch, uint32_t i) {
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+struct SumArrays {
+    uint32_t* of[3];
+};
+// Numbers per sequence become the sums before each (one entry more: the total), K arrays at once.  A thread has `per`
+// neighbouring sequences, an odd number, so that the threads' places are in different banks.
+template <int K>
+__device__ inline void sums_before(const SumArrays& arrays, int batch, const uint32_t* most, PagesLds& lds, uint32_t* total) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = ((batch + kThreads - 1) / kThreads) | 1, b0 = min(tid * per, batch), b1 = min(b0 + per, batch);
+    uint32_t sum[K];
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+        uint32_t in = 0;
+        for (int b = b0; b < b1; b++) in = add_to(in, arrays.of[k][b], most[k]);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t x = __shfl_up(in, d, 64);
+            if (lane >= d) in = add_to(in, x, most[k]);
+        }
+        if (lane == 63) lds.wave[k][wave] = in;
+        const uint32_t x = __shfl_up(in, 1, 64);
+        sum[k] = lane ? x : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+        uint32_t run = 0;
+        total[k] = 0;
+        for (int w = 0; w < kThreads / 64; w++) {
+            if (w < wave) run = add_to(run, lds.wave[k][w], most[k]);
+            total[k] = add_to(total[k], lds.wave[k][w], most[k]);
+        }
+        run = add_to(run, sum[k], most[k]);
+        for (int b = b0; b < b1; b++) {
+            const uint32_t n = arrays.of[k][b];
+            arrays.of[k][b] = run;
+            run = add_to(run, n, most[k]);
+        }
+        if (tid == 0) arrays.of[k][batch] = total[k];
+    }
+    __syncthreads();
+}
+
 __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
+    __shared__ PagesLds lds;
+    const int tid = threadIdx.x, batch = a.batch;
+    const uint32_t most[3] = {0x7FFFFFFFu, 0x7FFFFFFFu, (uint32_t)a.rows};
+    const int free0 = a.pool[0];
+    const uint32_t free = (uint32_t)(free0 < 0 ? 0 : min(free0, a.pages));
+    int32_t* const list = a.pool + 4;
+    for (int b = tid; b < batch; b += kThreads) {
+        const int len = max(a.len[b], 0), want = max(a.want[b], 0), had = pages_of(a, len), gets = pages_of(a, want);
+        lds.row[b] = (uint32_t)min(max(want - len, 0), a.rows);
+        lds.come[b] = (uint32_t)max(gets - had, 0);
+        lds.gone[b] = (uint32_t)max(had - gets, 0);
+    }
+    __syncthreads();
+    uint32_t total[3];
+    sums_before<3>({lds.gone, lds.come, lds.row}, batch, most, lds, total);
+    const uint32_t rows = total[2], come = total[1];
+    const uint32_t threads = gridDim.x * kThreads, at = blockIdx.x * kThreads + tid;
+
+    // Entries that are given back, by their number; if any of them is no page, pages are counted instead.
+    const auto entry = [&](int b, int j) { return a.table[(int64_t)b * a.table_ld + j]; };
+    const auto first_gone = [&](int b) { return pages_of(a, max(a.want[b], 0)); };
+    uint32_t gone = total[0];
+    int bad = 0;
+    for (uint32_t i = tid; i < gone; i += kThreads) {
+        const int b = holder(lds.gone, batch, i);
+        bad |= !is_page(a, entry(b, first_gone(b) + (int)(i - lds.gone[b])));
+    }
+    const bool holes = __syncthreads_or(bad);
+    if (holes) {
+        for (int b = tid; b < batch; b += kThreads) {
+            const int j0 = first_gone(b), j1 = max(j0, pages_of(a, max(a.len[b], 0)));
+            uint32_t n = 0;
+            for (int j = j0; j < j1; j++) n += is_page(a, entry(b, j)) ? 1 : 0;
+            lds.gone[b] = n;
+        }
+        __syncthreads();
+        sums_before<1>({lds.gone}, batch, most, lds, &gone);
+    }
+    const auto returned = [&](uint32_t i) {   // the i-th page that is given back
+        const int b = holder(lds.gone, batch, i);
+        int j = first_gone(b), skip = (int)(i - lds.gone[b]);
+        if (!holes) return entry(b, j + skip);
+        for (; j < a.table_ld; j++) {         // (it is among them, as they were counted)
+            const int p = entry(b, j);
+            if (is_page(a, p) && skip-- == 0) return p;
+        }
+        return -1;
+    };
+    const uint32_t top = free + gone;         // pages there are to take
+    // The page of the i-th wanted entry, -1 if there are not that many.
+    const auto taken = [&](uint32_t i) {
+        if (i < gone) return returned(i);
+        return i < top ? list[free - 1 - (i - gone)] : -1;
+    };
+    for (uint32_t i = at; i < come; i += threads) {
+        const int b = holder(lds.come, batch, i);
+        a.table[(int64_t)b * a.table_ld + pages_of(a, max(a.len[b], 0)) + (i - lds.come[b])] = taken(i);
+    }
+    for (uint32_t i = come + at; i < gone; i += threads)
+        if (top - 1 - i < (uint32_t)a.pages) list[top - 1 - i] = returned(i);
+    if (a.pos || a.slot) {
+        for (uint32_t r0 = at * kRowsPerThread; r0 < rows; r0 += threads * kRowsPerThread) {
+            int b = holder(lds.row, batch, r0), page = -1, on = -1;   // on: the table's entry that `page` is
+#pragma unroll
+            for (uint32_t k = 0; k < kRowsPerThread; k++) {
+                const uint32_t r = r0 + k;
+                if (r >= rows) break;
+                while (lds.row[b + 1] <= r) {
+                    b++;
+                    on = -1;
+                }
+                const int had = pages_of(a, max(a.len[b], 0));
+                const uint32_t n = lds.row[b + 1] - lds.row[b];
+                const int t = max(a.want[b], 0) - (int)n + (int)(r - lds.row[b]), j = t / a.page;
+                if (a.pos) a.pos[r] = t;
+                if (!a.slot) continue;
+                if (j != on) {
+                    on = j;
+                    page = j >= a.table_ld ? -1 : j < had ? a.table[(int64_t)b * a.table_ld + j] : taken(lds.come[b] + (j - had));
+                    if (!is_page(a, page)) page = -1;
+                }
+                a.slot[r] = page < 0 ? -1 : (int64_t)page * a.page + (t - j * a.page);
+            }
+        }
+    }
+    for (int b = at; b <= batch; b += threads) a.row_start[b] = (int)lds.row[b];
+    // what others may still read
+    if (gridDim.x > 1) {
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            lds.last = atomicAdd(reinterpret_cast<uint32_t*>(a.pool + 2), 1u) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!lds.last) return;
+    } else {
+        __syncthreads();
+    }
+    for (int b = tid; b < batch; b += kThreads) a.len[b] = max(a.want[b], 0);
+    if (tid == 0) {
+        a.pool[0] = (int)min(top > come ? top - come : 0u, (uint32_t)a.pages);
+        a.pool[1] = (int)(come > top ? come - top : 0u);
+        a.pool[2] = 0;
+    }
+}
+
+// More sequences, or more entries than 32 bits count: one workgroup, and the rows by a launch of their own.  First what is given back goes on the list's end (its front), the first sequence's first page last; then what
+// is wanted is taken from there.
+__global__ __launch_bounds__(kThreads) void k_pages_assign_many(PagesArgs a) {
     __shared__ int64_t lds[kThreads / 64];
     int32_t* const list = a.pool + 4;
     const int64_t free = a.pool[0] < 0 ? 0 : a.pool[0] < a.pages ? a.pool[0] : a.pages;
@@ -131,7 +310,13 @@ hipError_t launch_pages_init(int pages, int32_t* pool, hipStream_t s) {
 }
 
 hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(k_pages_assign, dim3(1), dim3(kThreads), 0, s, a);
+    if (a.batch <= kSeqsAtOnce && (int64_t)a.batch * a.table_ld <= 0x7FFFFFFF) {
+        const int64_t rows = a.pos || a.slot ? a.rows : 0;
+        const int64_t n = std::max<int64_t>(1, std::min<int64_t>(256, (rows + kThreads * kRowsPerThread - 1) / (kThreads * kRowsPerThread)));
+        hipLaunchKernelGGL(k_pages_assign, dim3((unsigned)n), dim3(kThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(k_pages_assign_many, dim3(1), dim3(kThreads), 0, s, a);
     if (a.rows > 0 && (a.pos || a.slot)) {
         Seqs q{};
         q.row_start = a.row_start;

@@ -389,14 +389,23 @@ def wq_attn_tree(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache,
                     _int32("wq_attn_tree", "tree_ld", tree_ld), _ptr(y), ldy, _ptr(ws), ws_bytes)
 
 
-def _words(where: str, name: str, t, n: int, types=("torch.int32", "torch.uint32")):
-    """Refuses a tensor that is not n contiguous elements, at least, of one of the types."""
+def _words(where: str, name: str, t, n: int, kind: str = "int32"):
+    """Refuses a tensor that is not n contiguous elements, at least, of its kind (int32 may also be unsigned)."""
     if t is None or isinstance(t, int):
         return
-    if str(t.dtype) not in types or not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be a contiguous {types[0][6:]} tensor, got {t.dtype}")
+    dt = t.dtype
+    if not (dt is _dtype(kind) or str(dt) in (f"torch.{kind}", f"torch.u{kind}")) or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous {kind} tensor, got {dt}")
     if t.numel() < n:
         raise ValueError(f"{where}: {name} has {t.numel()} entries; {n} are needed")
+
+
+def _dtype(kind: str):
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return getattr(_torch, kind)
 
 
 def wq_pages_init(pages: int, pool, stream=None, check=True) -> int:
@@ -411,7 +420,7 @@ def wq_pages_assign(d: wq_cache_desc, batch: int, len, want, table, table_ld: in
     for name, t, n in (("len", len, batch), ("want", want, batch), ("table", table, batch * table_ld), ("pool", pool, 4 + d.pages),
                        ("row_start", row_start, batch + 1), ("pos", pos, rows)):
         _words("wq_pages_assign", name, t, n)
-    _words("wq_pages_assign", "slot", slot, rows, ("torch.int64",))
+    _words("wq_pages_assign", "slot", slot, rows, "int64")
     return _call_on("wq_pages_assign", None, (len, want, table, pool, row_start, pos, slot), stream, check, lib().wq_pages_assign,
                     ctypes.byref(d), _int32("wq_pages_assign", "batch", batch), _ptr(len), _ptr(want), _ptr(table),
                     _int32("wq_pages_assign", "table_ld", table_ld), _ptr(pool), _int32("wq_pages_assign", "rows", rows),
