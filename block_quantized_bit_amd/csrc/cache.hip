@@ -423,27 +423,30 @@ __global__ __launch_bounds__((Pieces<Q41, NB>::threads)) void k_cache_keep(KeepA
     const Seqs& s = a.s;
     const int b = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63;
     uint8_t* const cache = a.cache[blockIdx.z];
+    const int32_t* const path = a.path + (int64_t)b * a.path_ld;
+    const auto row_at = [&](int j) { return j >= 0 && j < a.path_ld ? path[j] : -1; };
+    int i = row_at(lane), last = row_at(lane - 1);   // (requested with the lengths)
+    const int count = min(a.count[b], a.path_ld);
     int r0, r1;
     seq_rows(s, b, &r0, &r1);
     const int n = r1 - r0;
     const int64_t pos0 = (int64_t)s.len[b] - n, capacity = (int64_t)s.table_ld * s.page;
-    const int count = min(a.count[b], a.path_ld);
-    const int32_t* const path = a.path + (int64_t)b * a.path_ld;
     int size, kept = 0;
     for (int j0 = 0; j0 < count; j0 += kKeepAtOnce) {
         // the path ends before an entry that is no row, is not above the one before it, or has no place to be or to go
         const int j = j0 + lane;
+        if (j0 > 0) {
+            i = row_at(j);
+            last = row_at(j - 1);
+        }
         int64_t source = -1, target = -1;
         int su = 0, tu = 0;
-        if (j < count) {
-            const int i = path[j], last = j > 0 ? path[j - 1] : -1;
-            const int64_t st = pos0 + i, tt = pos0 + j;
-            if (i > last && i >= 0 && i < n && tt >= 0 && st < capacity) {
-                source = seq_unit(s, b, h, (int)st);
-                target = seq_unit(s, b, h, (int)tt);
-                su = (int)st % s.page % kUnit;
-                tu = (int)tt % s.page % kUnit;
-            }
+        const int64_t st = pos0 + i, tt = pos0 + j;
+        if (j < count && i > last && i >= 0 && i < n && tt >= 0 && st < capacity) {
+            source = seq_unit(s, b, h, (int)st);
+            target = seq_unit(s, b, h, (int)tt);
+            su = (int)st % s.page % kUnit;
+            tu = (int)tt % s.page % kUnit;
         }
         const uint64_t good = __ballot(source >= 0 && target >= 0);
         const int m = good == ~0ull ? kKeepAtOnce : __builtin_ctzll(~good);
@@ -455,18 +458,20 @@ __global__ __launch_bounds__((Pieces<Q41, NB>::threads)) void k_cache_keep(KeepA
             to_u[lane] = tu;
         }
         __syncthreads();
-        constexpr int group = 8;
+        constexpr int group = 16;
         for (int k0 = 0; k0 < m && threadIdx.x < Pieces<Q41, NB>::all; k0 += group) {
             uint32_t v[group];
 #pragma unroll
             for (int k = 0; k < group; k++) {
                 if (k0 + k >= m) break;
+                if (from[k0 + k] == to[k0 + k] && from_u[k0 + k] == to_u[k0 + k]) continue;   // it is where it belongs
                 const uint8_t* const p = cache + from[k0 + k] + Pieces<Q41, NB>::at(threadIdx.x, from_u[k0 + k], &size);
                 v[k] = size == 4 ? *reinterpret_cast<const uint32_t*>(p) : size == 2 ? *reinterpret_cast<const uint16_t*>(p) : *p;
             }
 #pragma unroll
             for (int k = 0; k < group; k++) {
                 if (k0 + k >= m) break;
+                if (from[k0 + k] == to[k0 + k] && from_u[k0 + k] == to_u[k0 + k]) continue;
                 uint8_t* const p = cache + to[k0 + k] + Pieces<Q41, NB>::at(threadIdx.x, to_u[k0 + k], &size);
                 if (size == 4) *reinterpret_cast<uint32_t*>(p) = v[k];
                 else if (size == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)v[k];

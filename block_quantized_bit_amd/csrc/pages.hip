@@ -52,15 +52,21 @@ __global__ __launch_bounds__(256) void k_pages_init(int pages, int32_t* pool) {
 // entries and of the list's.  Nothing that a workgroup reads is written by another: the page of a wanted entry comes from the
 // entry that is given back or from the list itself, not from the table; what is put on the list goes where nothing was; and
 // the lengths and counts are written by the workgroup that is the last to be done with reading.
-constexpr int kSeqsAtOnce = 8192, kRowsPerThread = 4;
+constexpr int kSeqsAtOnce = 8192, kAtOnce = 4;   // kAtOnce: items of a thread that are on their way together
 
 // a + b, at most `most`: associative for numbers that are at most that.
 __device__ inline uint32_t add_to(uint32_t a, uint32_t b, uint32_t most) { return min(a + b, most); }
+
+template <int CTRL, int ROWS>
+__device__ inline uint32_t add_dpp_to(uint32_t v, uint32_t most) {
+    return add_to(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false), most);
+}
 
 struct PagesLds {
     uint32_t wave[3][kThreads / 64];
     int last;
     uint32_t row[kSeqsAtOnce + 1], come[kSeqsAtOnce + 1], gone[kSeqsAtOnce + 1];   // before a sequence
+    int had[kSeqsAtOnce];                                                          // its pages
 };
 
 // The last sequence whose sum before it is at most i (that has the i-th item, for an i below the total).
@@ -88,11 +94,12 @@ __device__ inline void sums_before(const SumArrays& arrays, int batch, const uin
     for (int k = 0; k < K; k++) {
         uint32_t in = 0;
         for (int b = b0; b < b1; b++) in = add_to(in, arrays.of[k][b], most[k]);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t x = __shfl_up(in, d, 64);
-            if (lane >= d) in = add_to(in, x, most[k]);
-        }
+        in = add_dpp_to<0x111, 0xF>(in, most[k]);   // over rows of 16 lanes, then the rows' totals (as wave_scan)
+        in = add_dpp_to<0x112, 0xF>(in, most[k]);
+        in = add_dpp_to<0x114, 0xF>(in, most[k]);
+        in = add_dpp_to<0x118, 0xF>(in, most[k]);
+        in = add_dpp_to<0x142, 0xA>(in, most[k]);
+        in = add_dpp_to<0x143, 0xC>(in, most[k]);
         if (lane == 63) lds.wave[k][wave] = in;
         const uint32_t x = __shfl_up(in, 1, 64);
         sum[k] = lane ? x : 0;
@@ -129,6 +136,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
         lds.row[b] = (uint32_t)min(max(want - len, 0), a.rows);
         lds.come[b] = (uint32_t)max(gets - had, 0);
         lds.gone[b] = (uint32_t)max(had - gets, 0);
+        lds.had[b] = had;
     }
     __syncthreads();
     uint32_t total[3];
@@ -137,31 +145,39 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
     const uint32_t threads = gridDim.x * kThreads, at = blockIdx.x * kThreads + tid;
 
     // Entries that are given back, by their number; if any of them is no page, pages are counted instead.
-    const auto entry = [&](int b, int j) { return a.table[(int64_t)b * a.table_ld + j]; };
-    const auto first_gone = [&](int b) { return pages_of(a, max(a.want[b], 0)); };
     uint32_t gone = total[0];
-    int bad = 0;
-    for (uint32_t i = tid; i < gone; i += kThreads) {
+    const auto entry = [&](uint32_t i) {
         const int b = holder(lds.gone, batch, i);
-        bad |= !is_page(a, entry(b, first_gone(b) + (int)(i - lds.gone[b])));
+        return a.table[(int64_t)b * a.table_ld + (lds.had[b] - (int)(lds.gone[b + 1] - i))];
+    };
+    bool holes = false;
+    if (gone > 0) {
+        int bad = 0;
+        for (uint32_t i0 = tid; i0 < gone; i0 += kAtOnce * kThreads) {
+            int p[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; k++) p[k] = i0 + k * kThreads < gone ? entry(i0 + k * kThreads) : 0;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; k++) bad |= !is_page(a, p[k]);
+        }
+        holes = __syncthreads_or(bad);
     }
-    const bool holes = __syncthreads_or(bad);
+    const auto first_gone = [&](int b) { return pages_of(a, max(a.want[b], 0)); };
     if (holes) {
         for (int b = tid; b < batch; b += kThreads) {
-            const int j0 = first_gone(b), j1 = max(j0, pages_of(a, max(a.len[b], 0)));
             uint32_t n = 0;
-            for (int j = j0; j < j1; j++) n += is_page(a, entry(b, j)) ? 1 : 0;
+            for (int j = first_gone(b); j < lds.had[b]; j++) n += is_page(a, a.table[(int64_t)b * a.table_ld + j]) ? 1 : 0;
             lds.gone[b] = n;
         }
         __syncthreads();
         sums_before<1>({lds.gone}, batch, most, lds, &gone);
     }
     const auto returned = [&](uint32_t i) {   // the i-th page that is given back
+        if (!holes) return entry(i);
         const int b = holder(lds.gone, batch, i);
-        int j = first_gone(b), skip = (int)(i - lds.gone[b]);
-        if (!holes) return entry(b, j + skip);
-        for (; j < a.table_ld; j++) {         // (it is among them, as they were counted)
-            const int p = entry(b, j);
+        int skip = (int)(i - lds.gone[b]);
+        for (int j = first_gone(b); j < lds.had[b]; j++) {
+            const int p = a.table[(int64_t)b * a.table_ld + j];
             if (is_page(a, p) && skip-- == 0) return p;
         }
         return -1;
@@ -172,34 +188,59 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
         if (i < gone) return returned(i);
         return i < top ? list[free - 1 - (i - gone)] : -1;
     };
-    for (uint32_t i = at; i < come; i += threads) {
-        const int b = holder(lds.come, batch, i);
-        a.table[(int64_t)b * a.table_ld + pages_of(a, max(a.len[b], 0)) + (i - lds.come[b])] = taken(i);
-    }
-    for (uint32_t i = come + at; i < gone; i += threads)
-        if (top - 1 - i < (uint32_t)a.pages) list[top - 1 - i] = returned(i);
-    if (a.pos || a.slot) {
-        for (uint32_t r0 = at * kRowsPerThread; r0 < rows; r0 += threads * kRowsPerThread) {
-            int b = holder(lds.row, batch, r0), page = -1, on = -1;   // on: the table's entry that `page` is
+    // The table's new entries, and what goes on the list: by the last threads first, the rows by the first.
+    const uint32_t last = threads - 1 - at;
+    for (uint32_t i0 = last; i0 < come; i0 += kAtOnce * threads) {
+        int b[kAtOnce], p[kAtOnce];
 #pragma unroll
-            for (uint32_t k = 0; k < kRowsPerThread; k++) {
-                const uint32_t r = r0 + k;
+        for (int k = 0; k < kAtOnce; k++) {
+            const uint32_t i = i0 + k * threads;
+            if (i >= come) continue;
+            b[k] = holder(lds.come, batch, i);
+            p[k] = taken(i);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++) {
+            const uint32_t i = i0 + k * threads;
+            if (i < come) a.table[(int64_t)b[k] * a.table_ld + lds.had[b[k]] + (i - lds.come[b[k]])] = p[k];
+        }
+    }
+    for (uint32_t i0 = come + last; i0 < gone; i0 += kAtOnce * threads) {
+        int p[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++)
+            if (i0 + k * threads < gone) p[k] = returned(i0 + k * threads);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++) {
+            const uint32_t i = i0 + k * threads;
+            if (i < gone && top - 1 - i < (uint32_t)a.pages) list[top - 1 - i] = p[k];
+        }
+    }
+    if (a.pos || a.slot) {
+        for (uint32_t r0 = at; r0 < rows; r0 += kAtOnce * threads) {
+            int b[kAtOnce], t[kAtOnce], j[kAtOnce], p[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; k++) {
+                const uint32_t r = min(r0 + k * threads, rows - 1);
+                b[k] = holder(lds.row, batch, r);
+                t[k] = max(a.want[b[k]], 0) - (int)(lds.row[b[k] + 1] - r);
+            }
+            if (a.slot) {
+#pragma unroll
+                for (int k = 0; k < kAtOnce; k++) {
+                    j[k] = t[k] / a.page;
+                    const int had = lds.had[b[k]];
+                    p[k] = -1;
+                    if (j[k] < had) p[k] = a.table[(int64_t)b[k] * a.table_ld + j[k]];
+                    else if (j[k] < a.table_ld) p[k] = taken(lds.come[b[k]] + (j[k] - had));
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; k++) {
+                const uint32_t r = r0 + k * threads;
                 if (r >= rows) break;
-                while (lds.row[b + 1] <= r) {
-                    b++;
-                    on = -1;
-                }
-                const int had = pages_of(a, max(a.len[b], 0));
-                const uint32_t n = lds.row[b + 1] - lds.row[b];
-                const int t = max(a.want[b], 0) - (int)n + (int)(r - lds.row[b]), j = t / a.page;
-                if (a.pos) a.pos[r] = t;
-                if (!a.slot) continue;
-                if (j != on) {
-                    on = j;
-                    page = j >= a.table_ld ? -1 : j < had ? a.table[(int64_t)b * a.table_ld + j] : taken(lds.come[b] + (j - had));
-                    if (!is_page(a, page)) page = -1;
-                }
-                a.slot[r] = page < 0 ? -1 : (int64_t)page * a.page + (t - j * a.page);
+                if (a.pos) a.pos[r] = t[k];
+                if (a.slot) a.slot[r] = is_page(a, p[k]) ? (int64_t)p[k] * a.page + (t[k] - j[k] * a.page) : -1;
             }
         }
     }
@@ -312,7 +353,7 @@ hipError_t launch_pages_init(int pages, int32_t* pool, hipStream_t s) {
 hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s) {
     if (a.batch <= kSeqsAtOnce && (int64_t)a.batch * a.table_ld <= 0x7FFFFFFF) {
         const int64_t rows = a.pos || a.slot ? a.rows : 0;
-        const int64_t n = std::max<int64_t>(1, std::min<int64_t>(256, (rows + kThreads * kRowsPerThread - 1) / (kThreads * kRowsPerThread)));
+        const int64_t n = std::max<int64_t>(1, std::min<int64_t>(128, (rows + kThreads - 1) / kThreads));
         hipLaunchKernelGGL(k_pages_assign, dim3((unsigned)n), dim3(kThreads), 0, s, a);
         return hipGetLastError();
     }

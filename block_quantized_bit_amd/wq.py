@@ -76,7 +76,7 @@ def desc(fmt, n: int, k: int, dq: bool = False, block: int = 0) -> wq_desc:
 def _int32(where: str, name: str, v) -> int:
     """v as a 32-bit argument: ctypes would pass its low bits."""
     v = int(v)
-    if not -(1 << 31) <= v < 1 << 31:
+    if not -2147483648 <= v <= 2147483647:
         raise ValueError(f"{where}: {name} {v} does not fit 32 bits")
     return v
 
@@ -126,15 +126,30 @@ def _device(where: str, *args):
     return dev
 
 
-def _call_on(where: str, s: wq_seqs, tensors, stream, check: bool, fn, *args) -> int:
-    """fn(*args, stream) with the tensors' device current: a launch goes to the current device, and the default stream
-    is that device's."""
-    dev = _device(where, *tensors)
-    own = getattr(s, "device", None)
-    if own is not None:
-        if dev is not None and dev != own:
-            raise ValueError(f"{where}: tensors on device {dev}, sequences on {own}")
-        dev = own
+def _addresses(where: str, s, *args):
+    """The device that the tensors among the arguments and the sequences `s` (None: there are none) share, and the arguments'
+    device addresses."""
+    own = dev = getattr(s, "device", None)
+    out = []
+    for t in args:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                _ptr(t)                        # (says what it is)
+            if dev is not None:
+                raise ValueError(f"{where}: tensors on device {d}, sequences on {own}" if dev == own else
+                                 f"{where}: tensors on devices {dev} and {d}")
+            dev = d
+        out.append(t.data_ptr())
+    return dev, out
+
+
+def _call_on(where: str, dev, stream, check: bool, fn, *args) -> int:
+    """fn(*args, stream) with device `dev` current (None: as it is): a launch goes to the current device, and the default
+    stream is that device's."""
     if dev is not None:
         global _torch
         if _torch is None:
@@ -144,7 +159,8 @@ def _call_on(where: str, s: wq_seqs, tensors, stream, check: bool, fn, *args) ->
             with _torch.cuda.device(dev):
                 return _check(fn(*args, _stream(stream)), where, check)
         if stream is None:
-            return _check(fn(*args, _torch._C._cuda_getCurrentRawStream(dev)), where, check)
+            st = fn(*args, _torch._C._cuda_getCurrentRawStream(dev))
+            return _check(st, where, check) if st else st
     return _check(fn(*args, _stream(stream)), where, check)
 
 
@@ -333,13 +349,13 @@ def wq_cache_size(d: wq_cache_desc) -> int:
 
 
 def wq_cache_write(d: wq_cache_desc, s: wq_seqs, k, ldk: int, v, ldv: int, xdt: int, cache, stream=None, check=True) -> int:
-    return _call_on("wq_cache_write", s, (k, v, cache), stream, check, lib().wq_cache_write, ctypes.byref(d), ctypes.byref(s),
-                    _ptr(k), ldk, _ptr(v), ldv, xdt, _ptr(cache))
+    dev, (k, v, cache) = _addresses("wq_cache_write", s, k, v, cache)
+    return _call_on("wq_cache_write", dev, stream, check, (_lib or lib()).wq_cache_write, d, s, k, ldk, v, ldv, xdt, cache)
 
 
 def wq_cache_read(d: wq_cache_desc, s: wq_seqs, cache, k, ldk: int, v, ldv: int, ydt: int, stream=None, check=True) -> int:
-    return _call_on("wq_cache_read", s, (cache, k, v), stream, check, lib().wq_cache_read, ctypes.byref(d), ctypes.byref(s),
-                    _ptr(cache), _ptr(k), ldk, _ptr(v), ldv, ydt)
+    dev, (cache, k, v) = _addresses("wq_cache_read", s, cache, k, v)
+    return _call_on("wq_cache_read", dev, stream, check, (_lib or lib()).wq_cache_read, d, s, cache, k, ldk, v, ldv, ydt)
 
 
 def wq_attn_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int) -> int:
@@ -351,9 +367,9 @@ def wq_attn_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int) -> int:
 
 def wq_attn(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scale: float, causal, window: int, y, ldy: int,
             ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
-    return _call_on("wq_attn", s, (q, cache, y, ws), stream, check, lib().wq_attn, ctypes.byref(d), ctypes.byref(s),
-                    _int32("wq_attn", "q_heads", q_heads), _ptr(q), ldq, _ptr(cache), scale, _int32("wq_attn", "causal", causal),
-                    _int32("wq_attn", "window", window), _ptr(y), ldy, _ptr(ws), ws_bytes)
+    dev, (q, cache, y, ws) = _addresses("wq_attn", s, q, cache, y, ws)
+    return _call_on("wq_attn", dev, stream, check, (_lib or lib()).wq_attn, d, s, _int32("wq_attn", "q_heads", q_heads), q, ldq, cache,
+                    scale, _int32("wq_attn", "causal", causal), _int32("wq_attn", "window", window), y, ldy, ws, ws_bytes)
 
 
 def _attn_size(where: str, fn, d: wq_cache_desc, s: wq_seqs, q_heads: int, window: int, sinks: int) -> int:
@@ -369,10 +385,10 @@ def wq_attn_sinks_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int, win
 
 def wq_attn_sinks(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache, scale: float, window: int, sinks: int, y,
                   ldy: int, ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
-    return _call_on("wq_attn_sinks", s, (q, cache, y, ws), stream, check, lib().wq_attn_sinks, ctypes.byref(d), ctypes.byref(s),
-                    _int32("wq_attn_sinks", "q_heads", q_heads), _ptr(q), ldq, _ptr(cache), scale,
-                    _int32("wq_attn_sinks", "window", window), _int32("wq_attn_sinks", "sinks", sinks), _ptr(y), ldy, _ptr(ws),
-                    ws_bytes)
+    dev, (q, cache, y, ws) = _addresses("wq_attn_sinks", s, q, cache, y, ws)
+    return _call_on("wq_attn_sinks", dev, stream, check, (_lib or lib()).wq_attn_sinks, d, s, _int32("wq_attn_sinks", "q_heads", q_heads),
+                    q, ldq, cache, scale, _int32("wq_attn_sinks", "window", window), _int32("wq_attn_sinks", "sinks", sinks), y, ldy,
+                    ws, ws_bytes)
 
 
 def wq_attn_tree_workspace_size(d: wq_cache_desc, s: wq_seqs, q_heads: int, window: int, sinks: int) -> int:
@@ -383,55 +399,59 @@ def wq_attn_tree(d: wq_cache_desc, s: wq_seqs, q_heads: int, q, ldq: int, cache,
                  tree_ld: int, y, ldy: int, ws=None, ws_bytes: int = 0, stream=None, check=True) -> int:
     """`tree`: a contiguous int32 or uint32 tensor of at least rows * tree_ld words, or a device address."""
     _words("wq_attn_tree", "tree", tree, s.rows * tree_ld)
-    return _call_on("wq_attn_tree", s, (q, cache, tree, y, ws), stream, check, lib().wq_attn_tree, ctypes.byref(d), ctypes.byref(s),
-                    _int32("wq_attn_tree", "q_heads", q_heads), _ptr(q), ldq, _ptr(cache), scale,
-                    _int32("wq_attn_tree", "window", window), _int32("wq_attn_tree", "sinks", sinks), _ptr(tree),
-                    _int32("wq_attn_tree", "tree_ld", tree_ld), _ptr(y), ldy, _ptr(ws), ws_bytes)
+    dev, (q, cache, tree, y, ws) = _addresses("wq_attn_tree", s, q, cache, tree, y, ws)
+    return _call_on("wq_attn_tree", dev, stream, check, (_lib or lib()).wq_attn_tree, d, s, _int32("wq_attn_tree", "q_heads", q_heads),
+                    q, ldq, cache, scale, _int32("wq_attn_tree", "window", window), _int32("wq_attn_tree", "sinks", sinks), tree,
+                    _int32("wq_attn_tree", "tree_ld", tree_ld), y, ldy, ws, ws_bytes)
+
+
+_INT32 = None
 
 
 def _words(where: str, name: str, t, n: int, kind: str = "int32"):
     """Refuses a tensor that is not n contiguous elements, at least, of its kind (int32 may also be unsigned)."""
     if t is None or isinstance(t, int):
         return
+    global _INT32
+    if _INT32 is None:
+        import torch
+        _INT32 = torch.int32
     dt = t.dtype
-    if not (dt is _dtype(kind) or str(dt) in (f"torch.{kind}", f"torch.u{kind}")) or not t.is_contiguous():
+    if not (kind == "int32" and dt is _INT32 or str(dt) in (f"torch.{kind}", f"torch.u{kind}")) or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous {kind} tensor, got {dt}")
     if t.numel() < n:
         raise ValueError(f"{where}: {name} has {t.numel()} entries; {n} are needed")
 
 
-def _dtype(kind: str):
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return getattr(_torch, kind)
-
-
 def wq_pages_init(pages: int, pool, stream=None, check=True) -> int:
     _words("wq_pages_init", "pool", pool, 4 + pages)
-    return _call_on("wq_pages_init", None, (pool,), stream, check, lib().wq_pages_init, int(pages), _ptr(pool))
+    dev, (pool,) = _addresses("wq_pages_init", None, pool)
+    return _call_on("wq_pages_init", dev, stream, check, lib().wq_pages_init, int(pages), pool)
 
 
 def wq_pages_assign(d: wq_cache_desc, batch: int, len, want, table, table_ld: int, pool, rows: int, row_start, pos=None,  # noqa: A002
                     slot=None, stream=None, check=True) -> int:
     """The arrays are contiguous int32 tensors (`slot` int64) of at least the entries that the call touches, or device
     addresses."""
-    for name, t, n in (("len", len, batch), ("want", want, batch), ("table", table, batch * table_ld), ("pool", pool, 4 + d.pages),
-                       ("row_start", row_start, batch + 1), ("pos", pos, rows)):
-        _words("wq_pages_assign", name, t, n)
-    _words("wq_pages_assign", "slot", slot, rows, "int64")
-    return _call_on("wq_pages_assign", None, (len, want, table, pool, row_start, pos, slot), stream, check, lib().wq_pages_assign,
-                    ctypes.byref(d), _int32("wq_pages_assign", "batch", batch), _ptr(len), _ptr(want), _ptr(table),
-                    _int32("wq_pages_assign", "table_ld", table_ld), _ptr(pool), _int32("wq_pages_assign", "rows", rows),
-                    _ptr(row_start), _ptr(pos), _ptr(slot))
+    w = "wq_pages_assign"
+    _words(w, "len", len, batch)
+    _words(w, "want", want, batch)
+    _words(w, "table", table, batch * table_ld)
+    _words(w, "pool", pool, 4 + d.pages)
+    _words(w, "row_start", row_start, batch + 1)
+    _words(w, "pos", pos, rows)
+    _words(w, "slot", slot, rows, "int64")
+    dev, (len, want, table, pool, row_start, pos, slot) = _addresses(w, None, len, want, table, pool, row_start, pos, slot)  # noqa: A001
+    return _call_on(w, dev, stream, check, (_lib or lib()).wq_pages_assign, d, _int32(w, "batch", batch), len, want, table,
+                    _int32(w, "table_ld", table_ld), pool, _int32(w, "rows", rows), row_start, pos, slot)
 
 
 def wq_cache_keep(d: wq_cache_desc, s: wq_seqs, path, path_ld: int, count, caches, want=None, stream=None, check=True) -> int:
     """`caches`: a list of the layers' cache buffers; `path`, `count`, `want`: contiguous int32 tensors or device addresses."""
-    for name, t, n in (("path", path, s.batch * path_ld), ("count", count, s.batch), ("want", want, s.batch)):
-        _words("wq_cache_keep", name, t, n)
-    pools = (ctypes.c_void_p * len(caches))(*[_ptr(c) for c in caches])
-    return _call_on("wq_cache_keep", s, (path, count, want, *caches), stream, check, lib().wq_cache_keep, ctypes.byref(d),
-                    ctypes.byref(s), _ptr(path), _int32("wq_cache_keep", "path_ld", path_ld), _ptr(count), pools, len(caches),
-                    _ptr(want))
+    w, n = "wq_cache_keep", len(caches)
+    _words(w, "path", path, s.batch * path_ld)
+    _words(w, "count", count, s.batch)
+    _words(w, "want", want, s.batch)
+    dev, (path, count, want, *pools) = _addresses(w, s, path, count, want, *caches)
+    return _call_on(w, dev, stream, check, (_lib or lib()).wq_cache_keep, d, s, path, _int32(w, "path_ld", path_ld), count,
+                    (ctypes.c_void_p * n)(*pools), n, want)
