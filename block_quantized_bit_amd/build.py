@@ -37,6 +37,7 @@ SOURCES = [
     ("pages.hip", []),
     ("attn.hip", []),
     ("attn_parts.hip", []),
+    ("attn_wide.hip", []),
     ("gemv.hip", []),
     ("gemm.hip", ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]),
     ("gemm_nvfp4_wide.hip", []),

@@ -121,20 +121,78 @@ __device__ inline void join_column_wave(const AttnArgs& a, const Partials& p, in
     }
 }
 
+// Four columns by a wave, for the few parts of a draft's tiles, which have many columns: 16 lanes each, a lane's channels 64
+// apart in runs of four.
+__device__ inline void join_four_columns(const AttnArgs& a, const Partials& p, int n, int col, uint16_t* y, int slot0) {
+    const int lane = threadIdx.x & 15, group = threadIdx.x & 48, quads = a.dim / 4;
+    const auto slot = [&](int i) { return slot0 + 2 * i + (i == 0); };
+    constexpr int most = 4, ahead = 2;        // runs of a lane; parts requested before their factors are known
+    f32x4 o[most], early[ahead][most];
+#pragma unroll
+    for (int i = 0; i < ahead; i++)
+#pragma unroll
+        for (int k = 0; k < most; k++)
+            if (y && lane + 16 * k < quads && i < n) early[i][k] = p.read(slot(i), col, 4 * lane + 64 * k);
+    float m = -FLT_MAX, l = 0.0f;
+    if (y && lane < n) {
+        const f32x2 st = p.read_stat(slot(lane), col);
+        m = st[0];
+        l = st[1];
+    }
+    float ref = m;
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) ref = fmaxf(ref, __shfl_xor(ref, d, 64));
+    const float f = exp2_fast(m - ref);
+    l *= f;
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) l += __shfl_xor(l, d, 64);
+#pragma unroll
+    for (int k = 0; k < most; k++) o[k] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < ahead; i++) {
+        const float fi = __shfl(f, group + i, 64);
+#pragma unroll
+        for (int k = 0; k < most; k++)
+            if (y && lane + 16 * k < quads && i < n) o[k] += fi * early[i][k];
+    }
+    for (int i = ahead; i < n; i++) {
+        const float fi = __shfl(f, group + i, 64);
+#pragma unroll
+        for (int k = 0; k < most; k++)
+            if (y && lane + 16 * k < quads) o[k] += fi * p.read(slot(i), col, 4 * lane + 64 * k);
+    }
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int k = 0; k < most; k++)
+        if (y && lane + 16 * k < quads)
+            *reinterpret_cast<u32x2*>(y + 4 * lane + 64 * k) = (u32x2){pack_bf16(o[k][0] * inv, o[k][1] * inv), pack_bf16(o[k][2] * inv, o[k][3] * inv)};
+}
+
 // Workgroup i: the tile, if there is one, that workgroup i of k_attn_token began and did not end.  WAVES: tiles of few parts
 // by waves.  (A kernel of its own: with both ways in it, eight tiles of 64 parts took 6.5 us in place of 5.7.)
-template <bool WAVES>
+template <bool WAVES, int COLS>
 __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) JoinLds lds;
-    const TileShape ts = tile_shape(kTokenCols, a.group);
     const int32_t* const d = &open_tile(a, blockIdx.x)->parts;
     const OpenTile t = {read_const(d, 0), read_const(d, 1), read_const(d, 2), read_const(d, 3), read_const(d, 4)};
     if (t.parts == 0) return;
+    const TileShape shape = tile_shape(COLS, a.group), ts = COLS == kTokenCols ? shape : even_shape(shape, t.n);
     const Partials p(a);
     // the first part is the one that starts the tile, the others start their workgroups
     const auto slot = [](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0); };
     const bool few = WAVES && t.parts <= kWaveParts;
-    for (int col = few ? blockIdx.y * 4 + uniform(threadIdx.x >> 6) : blockIdx.y; col < kTokenCols; col += (few ? 4 : 1) * gridDim.y) {
+    if (COLS != kTokenCols && few) {
+        for (int col = blockIdx.y * 16; col < COLS; col += 16 * gridDim.y) {
+            int row, head;
+            if (!tile_col(a, ts, t.tile, col, t.n, &row, &head)) break;
+            const int c = col + (threadIdx.x >> 4);
+            uint16_t* y = nullptr;
+            if (tile_col(a, ts, t.tile, c, t.n, &row, &head)) y = a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim;
+            join_four_columns(a, p, t.parts, c, y, 2 * (int)blockIdx.x);
+        }
+        return;
+    }
+    for (int col = few ? blockIdx.y * 4 + uniform(threadIdx.x >> 6) : blockIdx.y; col < COLS; col += (few ? 4 : 1) * gridDim.y) {
         int row, head;
         if (!tile_col(a, ts, t.tile, col, t.n, &row, &head)) break;   // columns without a query are the last ones
         uint16_t* const y = a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim;
@@ -178,7 +236,8 @@ struct Schedule {
     int64_t items;       // tiles x heads (at most)
     int workgroups;      // 16 columns: sequences shared out over so many (0: not)
     int splits;          // 128, 256 columns: parts per tile
-    int slots() const { return cols == kTokenCols ? 2 * workgroups : splits > 1 ? (int)items * splits : 0; }
+    bool token() const { return cols < 128; }
+    int slots() const { return workgroups > 0 || token() ? 2 * workgroups : splits > 1 ? (int)items * splits : 0; }
 };
 
 // Units that a sequence's rows see, of the `most` that it can have: with sinks and a window, those and the rows themselves.
@@ -196,6 +255,14 @@ Schedule schedule(const AttnArgs& a, bool share) {
     };
     const int64_t most = ((int64_t)a.s.table_ld * a.s.page) / kUnit, units = seen_units(a, most);   // of the longest sequence there can be
     s.splits = 1;
+    const int64_t pairs = (int64_t)a.s.rows * a.group;
+    if (a.parts && a.s.row_start && pairs > (int64_t)kTokenCols * a.s.batch && (a.tree_rows || pairs < (int64_t)kManyCols * a.s.batch)) {
+        if (pairs <= 64 * (int64_t)a.s.batch || a.dim == 256) items(32);
+        else items(pairs < 512 * (int64_t)a.s.batch ? 128 : 256);
+        if (share && units > kShareLeast && s.items * (most + kTileCost) <= 0x7FFFFFFF)
+            s.workgroups = s.cols == 256 || a.dim == 256 ? kShareWorkgroups / 2 : kShareWorkgroups;
+        return s;
+    }
     if (a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch) {
         // Twice as many columns share a conversion to fp16, with one workgroup per compute unit instead of two: in us, 256
         // and 128 columns, 2048 rows of 8 x 4 heads of 128 over 18432 tokens 610 and 712, two prompts of 2048 rows 95 and
@@ -214,6 +281,13 @@ Schedule schedule(const AttnArgs& a, bool share) {
             s.workgroups = kShareWorkgroups;
     }
     return s;
+}
+
+template <int COLS>
+void launch_join(const AttnArgs& a, int64_t items, int cols, hipStream_t s) {
+    constexpr int at_once = COLS == kTokenCols ? 4 : 16;   // columns of a workgroup
+    if (items * 8 >= a.workgroups) hipLaunchKernelGGL((k_attn_join_token<true, COLS>), dim3(a.workgroups - 1, (cols + at_once - 1) / at_once), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_attn_join_token<false, COLS>), dim3(a.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -239,8 +313,14 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     a.slots = c.slots();
     const TileShape ts = tile_shape(a.tile_cols, a.group);
     const int cols = std::min(a.tile_cols, (a.s.row_start ? ts.rows : 1) * a.group);   // that a tile can have
-    if (c.cols != kTokenCols) {
+    if (!c.token()) {
         const dim3 grid((unsigned)(c.items * c.splits));
+        if (c.workgroups) {
+            launch_parts_shared(a, dim3(c.workgroups), c.cols == 256, s);
+            if (c.cols == 256) launch_join<256>(a, c.items, cols, s);
+            else launch_join<128>(a, c.items, cols, s);
+            return hipGetLastError();
+        }
         if (a.parts) launch_parts_rows(a, grid, c.cols == 256, s);
         else launch_rows<false>(a, grid, c.cols == 256, s);
         if (c.splits > 1) hipLaunchKernelGGL(k_attn_join_rows, dim3((unsigned)c.items, std::min(cols, 64)), dim3(256), 0, s, a);
@@ -250,12 +330,16 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     // With at most a tile per compute unit eight waves share a tile's tokens (1024 tokens, 8 tiles of 4 x 128: 13.6 ->
     // 11.4 us; 80 tiles of 1500 x 64: 12.3 -> 10.3); with more, four (320 tiles of 1500 x 64: 20.2 -> 16.5 us).
     const bool few = !c.workgroups && c.items <= 256;
-    if (a.parts) launch_parts_token(a, grid, few, s);
+    if (c.cols != kTokenCols) launch_attn_wide(a, grid, s);
+    else if (a.parts) launch_parts_token(a, grid, few, s);
     else launch_token<false>(a, grid, few, s);
     // (with few tiles each has many parts, and a workgroup takes one column at a time, not four)
     if (c.workgroups) {
-        if (c.items * 8 >= c.workgroups) hipLaunchKernelGGL(k_attn_join_token<true>, dim3(c.workgroups - 1, (cols + 3) / 4), dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(k_attn_join_token<false>, dim3(c.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);
+        switch (c.cols) {
+        case kTokenCols: launch_join<kTokenCols>(a, c.items, cols, s); break;
+        case 32: launch_join<32>(a, c.items, cols, s); break;
+        default: launch_join<64>(a, c.items, cols, s); break;
+        }
     }
     return hipGetLastError();
 }

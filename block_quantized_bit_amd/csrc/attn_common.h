@@ -151,6 +151,12 @@ __device__ inline uint32_t seen_nodes(const AttnArgs& a, const SeqInfo& q, int i
 
 __device__ inline int tiles_of(const TileShape& ts, int n) { return (n + ts.rows - 1) / ts.rows * ts.ht; }
 
+// With as many tiles, the n rows spread evenly over them.
+__device__ inline TileShape even_shape(const TileShape& ts, int n) {
+    if (ts.ht != 1 || n <= ts.rows) return ts.ht == 1 && n > 0 ? TileShape{n, 1} : ts;
+    const int tiles = (n + ts.rows - 1) / ts.rows;
+    return TileShape{(n + tiles - 1) / tiles, 1};
+}
 struct TileCount {
     const AttnArgs& a;
     TileShape ts;

@@ -113,6 +113,12 @@ struct ColState {
     float ref, l;        // l: this lane's tokens only
 };
 
+// What a column sees besides drafted tokens, and its row; in LDS, as only units at an end of something need it.
+struct Column {
+    int lo, hi, row;
+    float sl2;   // scale of its scores
+};
+
 // What K is multiplied as: q4_0's codes less 8, which fp16 holds exactly, with a block's scale applied to its product in fp32;
 // q4_1's values d q + m, rounded to fp16 once.  Either way a product's terms are the keys' own, so its fp32 error follows
 // sum |q k^|.  (Terms that only cancel, codes from 128 on against a start of -136 sum q, or m sum q beside q4_1's codes, leave
@@ -425,11 +431,8 @@ __device__ void token_segment(const AttnArgs& a, const TileShape& ts, const SeqI
 // are; a tile that more than one workgroup has a part of is joined by k_attn_join_token.  With `workgroups` 0 every
 // workgroup has one whole tile.  (61 sequences of 1 to 8191 tokens, 8 x 4 heads of 128, q4_1: 80 us with 5 for the join,
 // 4.0 TB/s; counting what beginning a tile costs took it from 102 us to 81.)
-template <int NB, bool Q41, int NW, int D, bool PARTS>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_token(AttnArgs a) {
-    constexpr int ring_bytes = NW * D * UnitRing<NB, Q41>::bytes, join_bytes = NW * 16 * (32 * NB + 4 + 2) * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[ring_bytes > join_bytes ? ring_bytes : join_bytes];
-    const TileShape ts = tile_shape(kTokenCols, a.group);
+template <bool PARTS, class F>
+__device__ inline void each_segment(const AttnArgs& a, const TileShape& ts, F segment) {
     const int heads = a.s.heads;
     if (a.workgroups == 0) {
         const int item = blockIdx.x;
@@ -455,7 +458,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
         } else {
             row_units(a, q, first, end, &u0, &u1);
         }
-        token_segment<NB, Q41, NW, D, PARTS>(a, ts, q, seq, tile, h, un, u0, u1, nullptr, nullptr, lds);
+        segment(ts, q, seq, tile, h, un, u0, u1, nullptr, nullptr);
         return;
     }
     const TokenShare<PARTS> sh(a, ts);
@@ -469,8 +472,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
         const int units = span_units<PARTS>(a, q, &u0), span = kTileCost + units;
         UnitList un = {};
         if (PARTS && q.n > 0) un = row_parts(a, q, 0, q.n);
-        const uint32_t items = tiles_of(ts, q.n) * heads;
-        while (w < end && w - before < items * span) {
+        const int items = tiles_of(ts, q.n) * heads;
+        while (w < end && w - before < (uint32_t)(items * span)) {
             const int item = (w - before) / span, s0 = (w - before) - item * span, s1 = min((uint32_t)span, s0 + (end - w));
             const int tile = item / heads, h = item - tile * heads;
             float *po = nullptr, *pm = nullptr;
@@ -482,13 +485,96 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) vo
                 // (the rows' starts are the caller's: whatever they hold, the parts are workgroups)
                 if (s0 == 0) open = {(int)(min((w + span - 1) / sh.share, gridDim.x - 1) - blockIdx.x) + 1, tile, h, q.r0, q.n};
             }
-            token_segment<NB, Q41, NW, D, PARTS>(a, ts, q, seq, tile, h, un, u0 + max(0, s0 - kTileCost), u0 + max(0, s1 - kTileCost), po, pm, lds);
+            segment(ts, q, seq, tile, h, un, u0 + max(0, s0 - kTileCost), u0 + max(0, s1 - kTileCost), po, pm);
             w += s1 - s0;
         }
         before += items * span;
         seq++;
     }
     if (threadIdx.x == 0) *open_tile(a, blockIdx.x) = open;
+}
+
+// The same for a draft's tiles, with the segment's code once for both kinds of call.  A sequence's rows are spread evenly over
+// its tiles.
+template <class F>
+__device__ inline void each_part(const AttnArgs& a, const TileShape& shape, F segment) {
+    const int heads = a.s.heads;
+    const bool whole = a.workgroups == 0;
+    int seq, tiles = 0;
+    uint32_t w, end = 0, before, share = 1, span = 0;
+    if (whole) {
+        w = blockIdx.x;
+        seq = SeqTotals(a.s.batch, TileCount{a, shape}).find(w / heads, &before);
+        before *= heads;
+        if (seq < 0 || seq >= a.s.batch) return;
+    } else {
+        const TokenShare<true> sh(a, shape);
+        share = sh.share;
+        w = blockIdx.x * share;
+        end = min(w + share, sh.total);
+        seq = w < end ? sh.t.find(w, &before) : 0;
+    }
+    OpenTile open = {};
+    SeqInfo q;
+    UnitList un = {};
+    TileShape ts;
+    const auto begin = [&](int b) {
+        q = seq_info_uniform(a, b);
+        ts = even_shape(shape, q.n);
+        tiles = tiles_of(ts, q.n);
+        if (q.n > 0) un = row_parts(a, q, 0, q.n);
+        un = {uniform(un.far), uniform(un.near), uniform(un.count)};
+        span = kTileCost + un.count;
+    };
+    begin(seq);
+    while (whole || w < end) {
+        int tile, h, ua, ub;
+        uint32_t step = 0;
+        float *po = nullptr, *pm = nullptr;
+        if (whole) {
+            const int in = w - before;
+            tile = in / heads;
+            h = in - tile * heads;
+            const int first = ts.ht == 1 ? tile * ts.rows : tile / ts.ht;
+            if (first >= q.n) return;
+            un = row_parts(a, q, first, min(first + ts.rows, q.n));
+            un = {uniform(un.far), uniform(un.near), uniform(un.count)};
+            ua = 0;
+            ub = un.count;
+        } else {
+            while (w - before >= tiles * heads * span) {   // on to the sequence that has w
+                before += tiles * heads * span;
+                begin(++seq);
+            }
+            const int item = (w - before) / span, s0 = (w - before) - item * span, s1 = min(span, s0 + (end - w));
+            step = s1 - s0;
+            tile = item / heads;
+            h = item - tile * heads;
+            if (step < span) {
+                const Partials p(a);
+                const int slot = 2 * blockIdx.x + (s0 > 0 ? 0 : 1);
+                po = p.sums(slot, 0);
+                pm = p.stat(slot, 0);
+                // (the rows' starts are the caller's: whatever they hold, the parts are workgroups)
+                if (s0 == 0) open = {(int)(min((w + span - 1) / share, gridDim.x - 1) - blockIdx.x) + 1, tile, h, q.r0, q.n};
+            }
+            ua = max(0, s0 - kTileCost);
+            ub = max(0, s1 - kTileCost);
+        }
+        segment(ts, q, seq, uniform(tile), uniform(h), un, uniform(ua), uniform(ub), po, pm);
+        if (whole) return;
+        w += step;
+    }
+    if (threadIdx.x == 0) *open_tile(a, blockIdx.x) = open;
+}
+
+template <int NB, bool Q41, int NW, int D, bool PARTS>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_token(AttnArgs a) {
+    constexpr int ring_bytes = NW * D * UnitRing<NB, Q41>::bytes, join_bytes = NW * 16 * (32 * NB + 4 + 2) * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[ring_bytes > join_bytes ? ring_bytes : join_bytes];
+    each_segment<PARTS>(a, tile_shape(kTokenCols, a.group),
+                        [&](const TileShape& ts, const SeqInfo& q, int seq, int tile, int h, const UnitList& un, int ua, int ub, float* po,
+                            float* pm) { token_segment<NB, Q41, NW, D, PARTS>(a, ts, q, seq, tile, h, un, ua, ub, po, pm, lds); });
 }
 
 // ---------------------------------------------------------------------------------------------------------------
@@ -616,51 +702,36 @@ __device__ inline void store_pair(const Pair<Q41>& r, const PairPlace& at, uint3
 // The same rows and tokens, q4_0 and q4_1: heads of 64 402 and 425 us (292 GFLOP), of 96 526 and 528 (438 GFLOP), of 128 609 and
 // 643, 4 x 4 heads of 256 875 and 1552 (584 GFLOP).  Heads of 256 have one wave per SIMD and reload 18 (q4_0) and 25 (q4_1)
 // spilled registers inside the step loop, q4_1 with heads of 128 one (256 columns) or 6 (128 columns); the others none.
+template <int NB, int NW, int KS, bool PARTS>
+struct RowsLds {
+    // steps: keys are read a unit before their product, two before their use
+    static constexpr int dim = 32 * NB, unit = 64 * dim, buffer = 2 * KS * unit, ahead = KS > 1 ? 2 : 3;   // unit: fp16 bytes of its K, or V
+    __attribute__((aligned(16))) uint8_t ring[(ahead + 1) * buffer];
+    Column columns[PARTS ? NW * 32 : 1];
+};
+
+// A tile's columns x units [u0, u1) (with PARTS: of the list un) of one head, by the workgroup.  part: where the sums go (null:
+// the tile is whole, and y is written).
 template <int NB, bool Q41, int NW, int KS, bool PARTS>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows(AttnArgs a) {
+__device__ __forceinline__ void rows_segment(const AttnArgs& a, const TileShape& ts, const SeqInfo& q, int seq, int tile, int h,
+                                             const UnitList& un, int u0, int u1, float* part_o, float* part_ml,
+                                             RowsLds<NB, NW, KS, PARTS>& shared) {
     constexpr int dim = 32 * NB, unit_lds = 64 * dim, buffer = 2 * KS * unit_lds;   // fp16 bytes of a unit's K, or V; a step
     constexpr int threads = NW * 64, pairs = KS * 2 * dim, rounds = (pairs + threads - 1) / threads;
-    constexpr int ahead = KS > 1 ? 2 : 3;   // steps: keys are read a unit before their product, two before their use
-    __shared__ __attribute__((aligned(16))) uint8_t lds[(ahead + 1) * buffer];
-    const TileShape ts = tile_shape(NW * 32, a.group);
-    const int heads = a.s.heads, tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), hl = lane >> 5;
-    // heads vary fastest, so that a head's tiles (which read the same keys and values) tend to the same die; later tiles,
-    // which see more, come first
-    int at = blockIdx.x;
-    const int h = uniform(at % heads);
-    at = uniform(at / heads);
-    const int split = uniform(at % a.splits);
-    at = uniform(at / a.splits);
-    const int item = at * heads + h;        // of the parts' places: below the grid's bound whatever row_start holds
-    uint32_t before;
-    const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
-    if (seq < 0) return;
-    const SeqInfo q = seq_info_uniform(a, seq);
-    const int tile = uniform(tiles_of(ts, q.n) - 1 - (at - (int)before));
+    constexpr int ahead = RowsLds<NB, NW, KS, PARTS>::ahead;
+    uint8_t* const lds = shared.ring;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), hl = lane >> 5;
     const int first = uniform(ts.ht == 1 ? tile * ts.rows : tile / ts.ht), end = min(first + ts.rows, q.n);
-    int u0 = 0, u1;                         // (with PARTS: of the list)
-    UnitList un = {};
-    if constexpr (PARTS) {
-        un = row_parts(a, q, first, end);
-        un = {uniform(un.far), uniform(un.near), uniform(un.count)};
-        u1 = un.count;
-    } else {
-        row_units(a, q, first, end, &u0, &u1);
-        u0 = uniform(u0);
-        u1 = uniform(u1);
-    }
     const auto unit_no = [&](int i) { return PARTS ? un[i] : i; };
-    if (a.splits > 1) {
-        const int per = uniform(((u1 - u0 + a.splits - 1) / a.splits + KS - 1) / KS * KS);
-        u0 += split * per;
-        u1 = min(u1, u0 + per);
-    }
 
     // this wave's 32 columns
     int row, head, lo, hi, lo_most, hi_least, x;
     const bool valid = tile_col(a, ts, tile, wave * 32 + (lane & 31), q.n, &row, &head);
     if constexpr (PARTS) {
-        row_context(a, q, valid ? row : first, &lo, &hi);
+        Column c;
+        c.row = valid ? row : first;
+        row_context(a, q, c.row, &c.lo, &c.hi);
+        if (hl == 0) shared.columns[wave * 32 + lane] = c;   // (read by the same wave alone)
         parts_between(a, q, first, end - 1, &lo_most, &hi_least);
     } else {
         row_tokens(a, q, valid ? row : first, &lo, &hi);
@@ -785,9 +856,14 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     const auto settle = [&](int u, bool there) {
         const int t0 = unit_no(u) * kUnit;
         if (t0 < lo_most || t0 + kUnit > hi_least || !there) {
-            const int lo2 = there ? lo - t0 : kUnit, hi2 = hi - t0, far = PARTS && there ? a.sinks - t0 : 0;
             uint32_t nodes = 0;
-            if (PARTS && there) nodes = seen_nodes(a, q, valid ? row : first, t0);
+            if constexpr (PARTS) {
+                const Column c = shared.columns[wave * 32 + (lane & 31)];
+                lo = c.lo;
+                hi = c.hi;
+                if (there) nodes = seen_nodes(a, q, c.row, t0);
+            }
+            const int lo2 = there ? lo - t0 : kUnit, hi2 = hi - t0, far = PARTS && there ? a.sinks - t0 : 0;
             most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
@@ -811,18 +887,26 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
             for (int i = 0; i < 16; i++) e[i] = e[i] == -INFINITY ? -INFINITY : fmaf(s[i], sl2, -ref);
         }
     };
+    // a wave without a column makes its share of the conversions, and that is all
+    const bool idle = PARTS && wave * 32 >= (ts.ht == 1 ? (end - first) * a.group : a.group - (tile - first * ts.ht) * NW * 32);
     if (u0 < u1) {
         __syncthreads();
-        read_k(lds);
-        scores();
-        exponents();
-        settle(u0, has & 1);
-        read_k(lds + (KS > 1 ? unit_lds : buffer));
+        if (!idle) {
+            read_k(lds);
+            scores();
+            exponents();
+            settle(u0, has & 1);
+            read_k(lds + (KS > 1 ? unit_lds : buffer));
+        }
         uint8_t *lk = lds, *ln = lds + buffer, *lp = lds + ahead * buffer;   // this step's, the next one's, the one to fill
         const auto next = [&](uint8_t* at) { return at == lds + ahead * buffer ? lds : at + buffer; };
         for (int u = u0; u < u1; u += KS) {
             has |= got << (ahead * KS);
             clear(r, got, u + ahead * KS);
+            if (PARTS && idle) {
+                put(r, lp);
+                got = fetch(r);
+            } else
 #pragma unroll
             for (int k = 0; k < KS; k++) {
                 // (behind the last unit the scores are of zeros, and not used)
@@ -878,19 +962,17 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     }
     l += __shfl_xor(l, 32, 64);
     if (!valid) return;
-    if (a.splits > 1) {
-        const Partials p(a);
-        const int slot = item * a.splits + split, col = wave * 32 + (lane & 31);
-        float* const po = p.sums(slot, col);
+    if (part_o) {
+        const int col = wave * 32 + (lane & 31);
+        float* const po = part_o + col * dim;
 #pragma unroll
         for (int b = 0; b < NB; b++)
 #pragma unroll
             for (int k = 0; k < 4; k++)
                 *reinterpret_cast<f32x4*>(po + 32 * b + 8 * k + 4 * hl) = (f32x4){o[b][4 * k], o[b][4 * k + 1], o[b][4 * k + 2], o[b][4 * k + 3]};
         if (hl == 0) {
-            float* const st = p.stat(slot, col);
-            st[0] = ref;
-            st[1] = l;
+            part_ml[2 * col] = ref;
+            part_ml[2 * col + 1] = l;
         }
         return;
     }
@@ -902,6 +984,60 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
         for (int k = 0; k < 4; k++)
             *reinterpret_cast<u32x2*>(y + 32 * b + 8 * k + 4 * hl) = (u32x2){pack_bf16(o[b][4 * k] * inv, o[b][4 * k + 1] * inv),
                                                                             pack_bf16(o[b][4 * k + 2] * inv, o[b][4 * k + 3] * inv)};
+}
+
+template <int NB, bool Q41, int NW, int KS, bool PARTS>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows(AttnArgs a) {
+    __shared__ RowsLds<NB, NW, KS, PARTS> lds;
+    const TileShape ts = tile_shape(NW * 32, a.group);
+    const int heads = a.s.heads;
+    // heads vary fastest, so that a head's tiles (which read the same keys and values) tend to the same die; later tiles,
+    // which see more, come first
+    int at = blockIdx.x;
+    const int h = uniform(at % heads);
+    at = uniform(at / heads);
+    const int split = uniform(at % a.splits);
+    at = uniform(at / a.splits);
+    const int item = at * heads + h;        // of the parts' places: below the grid's bound whatever row_start holds
+    uint32_t before;
+    const int seq = SeqTotals(a.s.batch, TileCount{a, ts}).find(at, &before);
+    if (seq < 0) return;
+    const SeqInfo q = seq_info_uniform(a, seq);
+    const int tile = uniform(tiles_of(ts, q.n) - 1 - (at - (int)before));
+    const int first = uniform(ts.ht == 1 ? tile * ts.rows : tile / ts.ht), end = min(first + ts.rows, q.n);
+    int u0 = 0, u1;                         // (with PARTS: of the list)
+    UnitList un = {};
+    if constexpr (PARTS) {
+        un = row_parts(a, q, first, end);
+        un = {uniform(un.far), uniform(un.near), uniform(un.count)};
+        u1 = un.count;
+    } else {
+        row_units(a, q, first, end, &u0, &u1);
+        u0 = uniform(u0);
+        u1 = uniform(u1);
+    }
+    if (a.splits > 1) {
+        const int per = uniform(((u1 - u0 + a.splits - 1) / a.splits + KS - 1) / KS * KS);
+        u0 += split * per;
+        u1 = min(u1, u0 + per);
+    }
+
+    float *po = nullptr, *pm = nullptr;
+    if (a.splits > 1) {
+        const Partials p(a);
+        po = p.sums(item * a.splits + split, 0);
+        pm = p.stat(item * a.splits + split, 0);
+    }
+    rows_segment<NB, Q41, NW, KS, PARTS>(a, ts, q, seq, tile, h, un, u0, u1, po, pm, lds);
+}
+
+// The same with the work shared out evenly, as in k_attn_token.
+template <int NB, bool Q41, int NW, int KS>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows_shared(AttnArgs a) {
+    __shared__ RowsLds<NB, NW, KS, true> lds;
+    each_part(a, tile_shape(NW * 32, a.group),
+              [&](const TileShape& ts, const SeqInfo& q, int seq, int tile, int h, const UnitList& un, int ua, int ub, float* po,
+                  float* pm) { rows_segment<NB, Q41, NW, KS, true>(a, ts, q, seq, tile, h, un, ua, ub, po, pm, lds); });
 }
 
 // The launches: tiles of 16 columns (few: eight waves each), of 128 or 256 (wide).

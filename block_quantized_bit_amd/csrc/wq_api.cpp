@@ -249,8 +249,10 @@ wq_status check_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, 
 }
 
 // The same for rows that see first tokens and a window, or a tree.
-wq_status check_parts(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks, wq::AttnArgs* a) {
+wq_status check_parts(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks, bool tree,
+                      wq::AttnArgs* a) {
     a->parts = true;
+    a->tree_rows = tree;
     a->causal = true;
     a->window = std::max(window, 0);   // (a negative one is refused later, in the order of the other checks)
     a->sinks = std::max(sinks, 0);
@@ -559,7 +561,7 @@ wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, con
 wq_status wq_attn_sinks_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks,
                                        size_t* bytes) {
     wq::AttnArgs a{};
-    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    wq_status st = check_parts(d, s, q_heads, window, sinks, false, &a);
     if (st != WQ_OK) return st;
     if (window < 1 || sinks < 0 || !bytes) return WQ_ERR_INVALID_ARG;
     *bytes = a.s.rows == 0 || a.s.batch == 0 ? 0 : wq::attn_workspace_bytes(a);
@@ -570,7 +572,7 @@ wq_status wq_attn_sinks(const wq_cache_desc* d, const wq_seqs* s, int32_t q_head
                         const void* cache, float scale, int32_t window, int32_t sinks, uint16_t* y, int64_t ldy, void* ws,
                         size_t ws_bytes, void* stream) {
     wq::AttnArgs a{};
-    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    wq_status st = check_parts(d, s, q_heads, window, sinks, false, &a);
     if (st != WQ_OK) return st;
     const bool seen = window >= 1 && sinks >= 0;
     return run_attn(&a, d, q_heads, q, ldq, cache, scale, seen ? WQ_OK : WQ_ERR_INVALID_ARG, y, ldy, ws, ws_bytes, stream);
@@ -579,7 +581,7 @@ wq_status wq_attn_sinks(const wq_cache_desc* d, const wq_seqs* s, int32_t q_head
 wq_status wq_attn_tree_workspace_size(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, int32_t window, int32_t sinks,
                                       size_t* bytes) {
     wq::AttnArgs a{};
-    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    wq_status st = check_parts(d, s, q_heads, window, sinks, true, &a);
     if (st != WQ_OK) return st;
     if (!tree_window_ok(window, sinks) || !bytes) return WQ_ERR_INVALID_ARG;
     *bytes = a.s.rows == 0 || a.s.batch == 0 ? 0 : wq::attn_workspace_bytes(a);
@@ -590,7 +592,7 @@ wq_status wq_attn_tree(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads
                        const void* cache, float scale, int32_t window, int32_t sinks, const uint32_t* tree, int32_t tree_ld,
                        uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
     wq::AttnArgs a{};
-    wq_status st = check_parts(d, s, q_heads, window, sinks, &a);
+    wq_status st = check_parts(d, s, q_heads, window, sinks, true, &a);
     if (st != WQ_OK) return st;
     if (!tree_window_ok(window, sinks) || !tree || tree_ld < 1 || tree_ld > kMaxTreeWords) st = WQ_ERR_INVALID_ARG;
     else if (!aligned(tree, 4)) st = WQ_ERR_ALIGNMENT;

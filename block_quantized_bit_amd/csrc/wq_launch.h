@@ -122,6 +122,7 @@ struct AttnArgs {
     int32_t slots;         // partial results that the workspace holds
     bool q41, causal;
     bool parts;            // a row sees parts: the two below, or a tree
+    bool tree_rows;        // the rows are a tree
     int32_t sinks;         // first tokens that stay visible
     int32_t tree_ld;       // words of a row's mask
     const uint32_t* tree;  // null: the rows are no tree
@@ -130,7 +131,9 @@ bool attn_fits(const AttnArgs& a);
 size_t attn_workspace_bytes(const AttnArgs& a);
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 // Of its kernels, those for rows that see parts (attn_parts.hip): tiles of 16 columns, few of them; of 128 or 256 columns.
+void launch_attn_wide(const AttnArgs& a, dim3 grid, hipStream_t s);
 void launch_parts_token(const AttnArgs& a, dim3 grid, bool few, hipStream_t s);
+void launch_parts_shared(const AttnArgs& a, dim3 grid, bool wide, hipStream_t s);
 void launch_parts_rows(const AttnArgs& a, dim3 grid, bool wide, hipStream_t s);
 
 }  // namespace wq
