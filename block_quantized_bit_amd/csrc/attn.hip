@@ -170,29 +170,18 @@ __device__ inline void join_four_columns(const AttnArgs& a, const Partials& p, i
 
 // Workgroup i: the tile, if there is one, that workgroup i of k_attn_token began and did not end.  WAVES: tiles of few parts
 // by waves.  (A kernel of its own: with both ways in it, eight tiles of 64 parts took 6.5 us in place of 5.7.)
-template <bool WAVES, int COLS>
+template <bool WAVES>
 __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) JoinLds lds;
+    const TileShape ts = tile_shape(kTokenCols, a.group);
     const int32_t* const d = &open_tile(a, blockIdx.x)->parts;
     const OpenTile t = {read_const(d, 0), read_const(d, 1), read_const(d, 2), read_const(d, 3), read_const(d, 4)};
     if (t.parts == 0) return;
-    const TileShape shape = tile_shape(COLS, a.group), ts = COLS == kTokenCols ? shape : even_shape(shape, t.n);
     const Partials p(a);
     // the first part is the one that starts the tile, the others start their workgroups
     const auto slot = [](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0); };
     const bool few = WAVES && t.parts <= kWaveParts;
-    if (COLS != kTokenCols && few) {
-        for (int col = blockIdx.y * 16; col < COLS; col += 16 * gridDim.y) {
-            int row, head;
-            if (!tile_col(a, ts, t.tile, col, t.n, &row, &head)) break;
-            const int c = col + (threadIdx.x >> 4);
-            uint16_t* y = nullptr;
-            if (tile_col(a, ts, t.tile, c, t.n, &row, &head)) y = a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim;
-            join_four_columns(a, p, t.parts, c, y, 2 * (int)blockIdx.x);
-        }
-        return;
-    }
-    for (int col = few ? blockIdx.y * 4 + uniform(threadIdx.x >> 6) : blockIdx.y; col < COLS; col += (few ? 4 : 1) * gridDim.y) {
+    for (int col = few ? blockIdx.y * 4 + uniform(threadIdx.x >> 6) : blockIdx.y; col < kTokenCols; col += (few ? 4 : 1) * gridDim.y) {
         int row, head;
         if (!tile_col(a, ts, t.tile, col, t.n, &row, &head)) break;   // columns without a query are the last ones
         uint16_t* const y = a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim;
@@ -200,6 +189,49 @@ __global__ __launch_bounds__(256) void k_attn_join_token(AttnArgs a) {
         else join_column(a, p, t.parts, col, y, slot, lds);
     }
 }
+
+// The same for a draft's tiles, with COLS columns each, by workgroup (tile, run of columns).  FIND: few tiles, that have many parts
+// each: workgroup i takes the i-th tile there is (looking for it costs 2 us; a workgroup for each one that may have begun a
+// tile would leave most with nothing: 8 tiles of 128 columns in 64 parts took 70 us, and take 12).
+template <bool FIND, int COLS>
+__global__ __launch_bounds__(256) void k_attn_join_draft(AttnArgs a) {
+    __shared__ __attribute__((aligned(16))) JoinLds lds;
+    __shared__ int found;
+    int first = blockIdx.x;                   // the workgroup that began the tile
+    if (FIND) {
+        const int tid = threadIdx.x, i = 2 * tid;   // (at most 512)
+        const uint32_t one = i < a.workgroups && open_tile(a, i)->parts > 0, two = i + 1 < a.workgroups && open_tile(a, i + 1)->parts > 0;
+        const uint32_t in = wave_scan(one + two);
+        uint32_t* const sums = reinterpret_cast<uint32_t*>(lds.red);
+        if (tid == 0) found = -1;
+        if ((tid & 63) == 63) sums[tid >> 6] = in;
+        __syncthreads();
+        uint32_t before = in - one - two;
+        for (int w = 0; w < tid >> 6; w++) before += sums[w];
+        if (one && before == blockIdx.x) found = i;
+        if (two && before + one == blockIdx.x) found = i + 1;
+        __syncthreads();
+        first = uniform(found);
+        if (first < 0) return;
+    }
+    const int32_t* const d = &open_tile(a, first)->parts;
+    const OpenTile t = {read_const(d, 0), read_const(d, 1), read_const(d, 2), read_const(d, 3), read_const(d, 4)};
+    if (t.parts == 0) return;
+    const TileShape ts = even_shape(tile_shape(COLS, a.group), t.n);
+    const Partials p(a);
+    const auto slot = [&](int i) { return 2 * (first + i) + (i == 0); };
+    const auto to = [&](int col) {
+        int row, head;
+        return tile_col(a, ts, t.tile, col, t.n, &row, &head) ? a.y + (int64_t)(t.r0 + row) * a.ldy + (int64_t)(t.head * a.group + head) * a.dim : nullptr;
+    };
+    if (t.parts <= kWaveParts) {
+        for (int col = blockIdx.y * 16; col < COLS && to(col); col += 16 * gridDim.y)
+            join_four_columns(a, p, t.parts, col + (threadIdx.x >> 4), to(col + (threadIdx.x >> 4)), 2 * first);
+        return;
+    }
+    for (int col = blockIdx.y; col < COLS && to(col); col += gridDim.y) join_column(a, p, t.parts, col, to(col), slot, lds);
+}
+
 // Workgroup (tile, head): the tile's columns, each shared out over a.splits workgroups of k_attn_rows.
 __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) JoinLds lds;
@@ -232,9 +264,9 @@ constexpr int kRowItems = 128, kRowLeast = 16;
 
 // How a call runs.
 struct Schedule {
-    int cols;            // columns per tile: 16, 128 or 256
+    int cols;            // columns per tile: 16, 128 or 256; drafts: 32 too
     int64_t items;       // tiles x heads (at most)
-    int workgroups;      // 16 columns: sequences shared out over so many (0: not)
+    int workgroups;      // 16 columns, and drafts: sequences shared out over so many (0: not)
     int splits;          // 128, 256 columns: parts per tile
     bool token() const { return cols < 128; }
     int slots() const { return workgroups > 0 || token() ? 2 * workgroups : splits > 1 ? (int)items * splits : 0; }
@@ -247,6 +279,43 @@ int64_t seen_units(const AttnArgs& a, int64_t most) {
     return std::min(most, ((int64_t)a.sinks + kUnit - 1) / kUnit + (a.window + rows + kUnit - 1) / kUnit + 1);
 }
 
+// Drafts: `cols` columns per sequence on average, more than 16.  Measured in us, 8 x 4 heads of 128, q4_0, contexts of one length
+// (whole) or of 300 to so many tokens (shared out):
+//   tiles of                    16     32    128    256
+//   whole     4 x 128,  1500    22     38     64
+//            32 x  80,  1500    72     59     68
+//            32 x 128,   500    57     51     37
+//            32 x 256,  1500   214    148    103
+//            16 x 508,  3000   350    232    184    156
+//   shared   32 x  32,  8191    94     78    117    168
+//   out       8 x  64, 30000   150    123    121    161
+//            32 x 128,  8191   300    240    157    204
+//             8 x 256, 30000   507    399    264    237
+// Wider tiles share conversions, but take more registers and longer to begin: they pay where there are enough of them for the
+// chip, or they are shared out.  Sharing out costs some 15 us (finding the work, and the join), as for single tokens.  Heads of 256
+// leave tiles of 32 columns one wave per SIMD (16 x 200 columns of 4096 tokens, 2 heads: 115 and 106 us).
+void draft_schedule(const AttnArgs& a, bool share, int64_t most, int64_t units, int64_t cols, Schedule* s) {
+    const auto items = [&](int c) { return tile_bound(tile_shape(c, a.group), a.s.rows, a.s.batch, false) * a.s.heads; };
+    const auto take = [&](int c, int workgroups) {
+        s->cols = c;
+        s->items = items(c);
+        s->workgroups = share && s->items * (most + kTileCost) <= 0x7FFFFFFF ? workgroups : 0;
+    };
+    const bool lengthy = units > (items(kTokenCols) < 256 ? 64 : 128);
+    if (a.dim == 256) {
+        if (cols >= 512) take(128, lengthy ? kShareWorkgroups / 2 : 0);
+        else if (cols >= 160) take(32, lengthy && items(32) < 128 ? kShareWorkgroups / 2 : 0);
+        else take(kTokenCols, lengthy ? kShareWorkgroups : 0);
+    } else if (lengthy && share) {
+        if (cols > 64) take(cols < 256 ? 128 : 256, cols < 256 ? kShareWorkgroups : kShareWorkgroups / 2);
+        else take(32, kShareWorkgroups);
+    } else if (cols >= 112 && items(128) >= 256) {
+        take(cols >= 256 && items(256) >= 256 ? 256 : 128, 0);
+    } else {
+        take(items(32) >= 512 ? 32 : kTokenCols, 0);
+    }
+}
+
 Schedule schedule(const AttnArgs& a, bool share) {
     Schedule s{};
     const auto items = [&](int cols) {
@@ -255,12 +324,9 @@ Schedule schedule(const AttnArgs& a, bool share) {
     };
     const int64_t most = ((int64_t)a.s.table_ld * a.s.page) / kUnit, units = seen_units(a, most);   // of the longest sequence there can be
     s.splits = 1;
-    const int64_t pairs = (int64_t)a.s.rows * a.group;
-    if (a.parts && a.s.row_start && pairs > (int64_t)kTokenCols * a.s.batch && (a.tree_rows || pairs < (int64_t)kManyCols * a.s.batch)) {
-        if (pairs <= 64 * (int64_t)a.s.batch || a.dim == 256) items(32);
-        else items(pairs < 512 * (int64_t)a.s.batch ? 128 : 256);
-        if (share && units > kShareLeast && s.items * (most + kTileCost) <= 0x7FFFFFFF)
-            s.workgroups = s.cols == 256 || a.dim == 256 ? kShareWorkgroups / 2 : kShareWorkgroups;
+    const int64_t pairs = (int64_t)a.s.rows * a.group, batch = a.s.batch;
+    if (a.parts && a.s.row_start && pairs > kTokenCols * batch && (a.tree_rows || pairs < kManyCols * batch)) {
+        draft_schedule(a, share, most, units, pairs / batch, &s);
         return s;
     }
     if (a.s.row_start && (int64_t)a.s.rows * a.group >= (int64_t)kManyCols * a.s.batch) {
@@ -285,9 +351,8 @@ Schedule schedule(const AttnArgs& a, bool share) {
 
 template <int COLS>
 void launch_join(const AttnArgs& a, int64_t items, int cols, hipStream_t s) {
-    constexpr int at_once = COLS == kTokenCols ? 4 : 16;   // columns of a workgroup
-    if (items * 8 >= a.workgroups) hipLaunchKernelGGL((k_attn_join_token<true, COLS>), dim3(a.workgroups - 1, (cols + at_once - 1) / at_once), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_attn_join_token<false, COLS>), dim3(a.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);
+    if (items >= 64) hipLaunchKernelGGL((k_attn_join_draft<false, COLS>), dim3(a.workgroups - 1, (cols + 15) / 16), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_attn_join_draft<true, COLS>), dim3((unsigned)items, cols), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -317,8 +382,7 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
         const dim3 grid((unsigned)(c.items * c.splits));
         if (c.workgroups) {
             launch_parts_shared(a, dim3(c.workgroups), c.cols == 256, s);
-            if (c.cols == 256) launch_join<256>(a, c.items, cols, s);
-            else launch_join<128>(a, c.items, cols, s);
+            c.cols == 256 ? launch_join<256>(a, c.items, cols, s) : launch_join<128>(a, c.items, cols, s);
             return hipGetLastError();
         }
         if (a.parts) launch_parts_rows(a, grid, c.cols == 256, s);
@@ -335,11 +399,9 @@ hipError_t launch_attn(const AttnArgs& args, hipStream_t s) {
     else launch_token<false>(a, grid, few, s);
     // (with few tiles each has many parts, and a workgroup takes one column at a time, not four)
     if (c.workgroups) {
-        switch (c.cols) {
-        case kTokenCols: launch_join<kTokenCols>(a, c.items, cols, s); break;
-        case 32: launch_join<32>(a, c.items, cols, s); break;
-        default: launch_join<64>(a, c.items, cols, s); break;
-        }
+        if (c.cols == 32) launch_join<32>(a, c.items, cols, s);
+        else if (c.items * 8 >= c.workgroups) hipLaunchKernelGGL(k_attn_join_token<true>, dim3(c.workgroups - 1, (cols + 3) / 4), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL(k_attn_join_token<false>, dim3(c.workgroups - 1, std::min(cols, 8)), dim3(256), 0, s, a);
     }
     return hipGetLastError();
 }

@@ -114,10 +114,19 @@ struct ColState {
 };
 
 // What a column sees besides drafted tokens, and its row; in LDS, as only units at an end of something need it.
+constexpr int kNodeWords = 4;
 struct Column {
     int lo, hi, row;
-    float sl2;   // scale of its scores
+    float sl2;                    // scale of its scores
+    uint32_t nodes[kNodeWords];   // drafted tokens that it sees, of the first units that have any
 };
+__device__ inline int first_node_unit(const SeqInfo& q) { return clamped(q.pos0, q.tokens) / kUnit; }
+// (Read from memory in the loop, a word would also wait for all units that are on their way.)
+__device__ inline uint32_t column_nodes(const AttnArgs& a, const SeqInfo& q, const Column& c, int t0) {
+    if (!a.tree || t0 + kUnit <= q.pos0) return 0;
+    const int k = t0 / kUnit - first_node_unit(q);
+    return k < kNodeWords ? c.nodes[k] : seen_nodes(a, q, c.row, t0);
+}
 
 // What K is multiplied as: q4_0's codes less 8, which fp16 holds exactly, with a block's scale applied to its product in fp32;
 // q4_1's values d q + m, rounded to fp16 once.  Either way a product's terms are the keys' own, so its fp32 error follows
@@ -727,13 +736,7 @@ __device__ __forceinline__ void rows_segment(const AttnArgs& a, const TileShape&
     // this wave's 32 columns
     int row, head, lo, hi, lo_most, hi_least, x;
     const bool valid = tile_col(a, ts, tile, wave * 32 + (lane & 31), q.n, &row, &head);
-    if constexpr (PARTS) {
-        Column c;
-        c.row = valid ? row : first;
-        row_context(a, q, c.row, &c.lo, &c.hi);
-        if (hl == 0) shared.columns[wave * 32 + lane] = c;   // (read by the same wave alone)
-        parts_between(a, q, first, end - 1, &lo_most, &hi_least);
-    } else {
+    if constexpr (!PARTS) {
         row_tokens(a, q, valid ? row : first, &lo, &hi);
         row_tokens(a, q, first, &x, &hi_least);
         row_tokens(a, q, end - 1, &lo_most, &x);
@@ -810,6 +813,19 @@ __device__ __forceinline__ void rows_segment(const AttnArgs& a, const TileShape&
         }
     }
     got = fetch(r);
+    if constexpr (PARTS) {
+        Column* const to = &shared.columns[wave * 32 + (lane & 31)];   // (read by the same wave alone)
+        const int of = valid ? row : first;
+        row_context(a, q, of, &lo, &hi);
+        to->lo = lo;
+        to->hi = hi;
+        to->row = of;
+        if (a.tree) {
+#pragma unroll
+            for (int k = 0; k < kNodeWords / 2; k++) to->nodes[2 * k + hl] = seen_nodes(a, q, of, (first_node_unit(q) + 2 * k + hl) * kUnit);
+        }
+        parts_between(a, q, first, end - 1, &lo_most, &hi_least);
+    }
 
     uint32_t big = 0;
 #pragma unroll
@@ -858,10 +874,10 @@ __device__ __forceinline__ void rows_segment(const AttnArgs& a, const TileShape&
         if (t0 < lo_most || t0 + kUnit > hi_least || !there) {
             uint32_t nodes = 0;
             if constexpr (PARTS) {
-                const Column c = shared.columns[wave * 32 + (lane & 31)];
+                const Column& c = shared.columns[wave * 32 + (lane & 31)];
                 lo = c.lo;
                 hi = c.hi;
-                if (there) nodes = seen_nodes(a, q, c.row, t0);
+                if (there) nodes = column_nodes(a, q, c, t0);
             }
             const int lo2 = there ? lo - t0 : kUnit, hi2 = hi - t0, far = PARTS && there ? a.sinks - t0 : 0;
             most = -INFINITY;

@@ -69,15 +69,20 @@ __device__ inline bool wide_step(const AttnArgs& a, const SeqInfo& q, const uint
     float e[CT][8], most = -INFINITY;
 #pragma unroll
     for (int c = 0; c < CT; c++) {
-        const Column col = EDGE ? columns[16 * c + (lane & 15)] : Column{};
+        const Column& col = columns[16 * c + (lane & 15)];
         uint32_t nodes = 0;
-        if constexpr (EDGE) nodes = seen_nodes(a, q, col.row, t0);
+        int lo = 0, hi = 0;
+        if constexpr (EDGE) {
+            nodes = column_nodes(a, q, col, t0);
+            lo = col.lo;
+            hi = col.hi;
+        }
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             e[c][j] = fmaf(s[c][j >> 2][j & 3], sl2[c], -st->ref[c]);
             if constexpr (EDGE) {
                 const int t = t0 + (j >> 2) * 16 + 4 * g + (j & 3);
-                e[c][j] = (t < col.hi && (t >= col.lo || t < a.sinks)) || (nodes >> (t - t0) & 1) ? e[c][j] : -INFINITY;
+                e[c][j] = (t < hi && (t >= lo || t < a.sinks)) || (nodes >> (t - t0) & 1) ? e[c][j] : -INFINITY;
             }
             most = fmaxf(most, e[c][j]);
         }
@@ -212,16 +217,24 @@ __device__ void wide_segment(const AttnArgs& a, const TileShape& ts, const SeqIn
             qv[b] = (u32x4){0, 0, 0, 0};
             if (valid) qv[b] = *reinterpret_cast<const u32x4*>(qp + 32 * b);
         }
-        Column k;
-        k.row = valid ? row : first;
-        row_context(a, q, k.row, &k.lo, &k.hi);
+        const int of = valid ? row : first;
+        int lo, hi;
+        row_context(a, q, of, &lo, &hi);
+        const uint32_t nodes = a.tree ? seen_nodes(a, q, of, (first_node_unit(q) + g) * kUnit) : 0;
 #pragma unroll
         for (int b = 0; b < NB; b++) big = max(big, largest_bf16(qv[b]));
         big = max(big, (uint32_t)__shfl_xor((int)big, 16, 64));
         big = max(big, (uint32_t)__shfl_xor((int)big, 32, 64));
         const int up = query_shift(big);
-        k.sl2 = ldexpf(a.scale_log2, -up);
-        if (g == 0) lds.columns[16 * c + col] = k;
+        Column* const to = &lds.columns[16 * c + col];
+        if (g == 0) {
+            to->lo = lo;
+            to->hi = hi;
+            to->row = of;
+            to->sl2 = ldexpf(a.scale_log2, -up);
+        }
+        static_assert(kNodeWords == 4);
+        to->nodes[g] = nodes;
 #pragma unroll
         for (int b = 0; b < NB; b++) *reinterpret_cast<f16x8*>(lds.queries + ((c * NB + b) * 64 + lane) * 16) = query_f16(qv[b], up);
     }
@@ -320,21 +333,23 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(EU))) v
                            float* pm) { wide_segment<NB, Q41, NW, D, CT>(a, ts, q, seq, tile, h, un, ua, ub, po, pm, lds); });
 }
 
-template <int NB, int NW, int D, int CT, int EU>
+constexpr int kTiles = 2;
+
+// Rings of two units leave LDS for three workgroups per compute unit, and EU 3 the registers for as many waves per SIMD.
+template <int NB, int NW, int D, int EU>
 void launch_as(const AttnArgs& a, dim3 grid, hipStream_t s) {
-    if (a.q41) hipLaunchKernelGGL((k_attn_wide<NB, true, NW, D, CT, EU>), grid, dim3(NW * 64), 0, s, a);
-    else hipLaunchKernelGGL((k_attn_wide<NB, false, NW, D, CT, EU>), grid, dim3(NW * 64), 0, s, a);
+    if (a.q41) hipLaunchKernelGGL((k_attn_wide<NB, true, NW, D, kTiles, EU>), grid, dim3(NW * 64), 0, s, a);
+    else hipLaunchKernelGGL((k_attn_wide<NB, false, NW, D, kTiles, EU>), grid, dim3(NW * 64), 0, s, a);
 }
 
 }  // namespace
 
 void launch_attn_wide(const AttnArgs& a, dim3 grid, hipStream_t s) {
-    const bool four = a.tile_cols == 64;
     switch (a.dim) {
-    case 64: four ? launch_as<2, 4, 4, 4, 2>(a, grid, s) : launch_as<2, 4, 4, 2, 2>(a, grid, s); break;
-    case 96: four ? launch_as<3, 4, 3, 4, 1>(a, grid, s) : launch_as<3, 4, 3, 2, 2>(a, grid, s); break;
-    case 128: four ? launch_as<4, 4, 3, 4, 1>(a, grid, s) : launch_as<4, 4, 3, 2, 2>(a, grid, s); break;
-    default: launch_as<8, 4, 3, 2, 1>(a, grid, s); break;
+    case 64: launch_as<2, 4, 3, 3>(a, grid, s); break;
+    case 96: launch_as<3, 4, 2, 3>(a, grid, s); break;
+    case 128: launch_as<4, 4, 2, 3>(a, grid, s); break;
+    default: launch_as<8, 4, 2, 1>(a, grid, s); break;
     }
 }
 

@@ -226,13 +226,13 @@ def test_offsets_past_32_bits(orc):
 def test_rows_claimed_twice_stay_in_the_workspace(orc):
     """Starts that do not ascend: the outputs are not specified, but parts stay inside the workspace and masks are read
     inside their array."""
-    c = Case(Q4_0, 64, 1, 64, [160, 0, 160], [2000, 0, 1900], seed=33, pad_rows=5)
+    c = Case(Q4_0, 64, 1, 64, [160, 0, 160], [6000, 0, 5900], seed=33, pad_rows=5)
     c.fill(*c.random_kv())
     c.d_start.copy_(torch.tensor([0, 160, 0, 160], dtype=torch.int32))
     s = wq.seqs(3, 165, c.d_len, c.d_table, row_start=c.d_start)
     tree = torch.full((165, 5), -1, dtype=torch.int32, device=DEV)
     q = torch.ones((165, 256), dtype=torch.bfloat16, device=DEV)
-    for window, sinks in ((0, 0), (1500, 40)):
+    for window, sinks in ((0, 0), (4500, 40)):
         need = wq.wq_attn_tree_workspace_size(c.desc, s, 4, window, sinks)
         assert need > 0
         ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
