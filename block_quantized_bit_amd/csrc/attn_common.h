@@ -149,6 +149,12 @@ __device__ inline uint32_t seen_nodes(const AttnArgs& a, const SeqInfo& q, int i
     return q.tokens - t0 < kUnit ? bits & ((1u << (q.tokens - t0)) - 1) : bits;
 }
 
+// Which of the 32 tokens from t0 on are seen, a bit each, where [lo, hi), the first `sinks` below hi and `nodes` are.
+__device__ inline uint32_t bits_below(int n) { return n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u; }
+__device__ inline uint32_t seen_tokens(int lo, int hi, int sinks, uint32_t nodes, int t0) {
+    return (bits_below(hi - t0) & (~bits_below(lo - t0) | bits_below(sinks - t0))) | nodes;
+}
+
 __device__ inline int tiles_of(const TileShape& ts, int n) { return (n + ts.rows - 1) / ts.rows * ts.ht; }
 
 // With as many tiles, the n rows spread evenly over them.

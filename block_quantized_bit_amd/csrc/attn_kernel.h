@@ -180,12 +180,13 @@ __device__ inline void unit_step(const uint8_t* unit, const f16x8 (&qf)[NB], flo
     }
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};    // token pairs that are in the cache: what lies behind them is anything
     float e[8];
+    const uint32_t seen = PARTS && MASKED ? seen_tokens(lo, hi, sinks, nodes, t0) >> (4 * g) : 0;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         e[j] = fmaf(x[j], sl2, -st->ref);
         if constexpr (MASKED) {
             const int t = t0 + (j >> 2) * 16 + 4 * g + (j & 3);
-            if constexpr (PARTS) e[j] = (t < hi && (t >= lo || t < sinks)) || (nodes >> (t - t0) & 1) ? e[j] : -INFINITY;
+            if constexpr (PARTS) e[j] = seen >> ((j >> 2) * 16 + (j & 3)) & 1 ? e[j] : -INFINITY;
             else e[j] = t >= lo && t < hi ? e[j] : -INFINITY;
             if (t >= tokens) keep[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
         }
@@ -872,19 +873,17 @@ __device__ __forceinline__ void rows_segment(const AttnArgs& a, const TileShape&
     const auto settle = [&](int u, bool there) {
         const int t0 = unit_no(u) * kUnit;
         if (t0 < lo_most || t0 + kUnit > hi_least || !there) {
-            uint32_t nodes = 0;
+            uint32_t seen = 0;
             if constexpr (PARTS) {
                 const Column& c = shared.columns[wave * 32 + (lane & 31)];
-                lo = c.lo;
-                hi = c.hi;
-                if (there) nodes = column_nodes(a, q, c, t0);
+                if (there) seen = seen_tokens(c.lo, c.hi, a.sinks, column_nodes(a, q, c, t0), t0) >> (4 * hl);
             }
-            const int lo2 = there ? lo - t0 : kUnit, hi2 = hi - t0, far = PARTS && there ? a.sinks - t0 : 0;
+            const int lo2 = there ? lo - t0 : kUnit, hi2 = hi - t0;
             most = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
                 const int t = 8 * (i >> 2) + 4 * hl + (i & 3);
-                if constexpr (PARTS) e[i] = (t < hi2 && (t >= lo2 || t < far)) || (nodes >> t & 1) ? e[i] : -INFINITY;
+                if constexpr (PARTS) e[i] = seen >> (8 * (i >> 2) + (i & 3)) & 1 ? e[i] : -INFINITY;
                 else e[i] = t >= lo2 && t < hi2 ? e[i] : -INFINITY;
                 most = fmaxf(most, e[i]);
             }

@@ -70,20 +70,12 @@ __device__ inline bool wide_step(const AttnArgs& a, const SeqInfo& q, const uint
 #pragma unroll
     for (int c = 0; c < CT; c++) {
         const Column& col = columns[16 * c + (lane & 15)];
-        uint32_t nodes = 0;
-        int lo = 0, hi = 0;
-        if constexpr (EDGE) {
-            nodes = column_nodes(a, q, col, t0);
-            lo = col.lo;
-            hi = col.hi;
-        }
+        uint32_t seen = 0;
+        if constexpr (EDGE) seen = seen_tokens(col.lo, col.hi, a.sinks, column_nodes(a, q, col, t0), t0) >> (4 * g);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             e[c][j] = fmaf(s[c][j >> 2][j & 3], sl2[c], -st->ref[c]);
-            if constexpr (EDGE) {
-                const int t = t0 + (j >> 2) * 16 + 4 * g + (j & 3);
-                e[c][j] = (t < hi && (t >= lo || t < a.sinks)) || (nodes >> (t - t0) & 1) ? e[c][j] : -INFINITY;
-            }
+            if constexpr (EDGE) e[c][j] = seen >> ((j >> 2) * 16 + (j & 3)) & 1 ? e[c][j] : -INFINITY;
             most = fmaxf(most, e[c][j]);
         }
     }
