@@ -34,8 +34,10 @@ __device__ inline int64_t block_scan(int64_t v, int64_t* before, int64_t* lds) {
     return total;
 }
 
+// A division by the page's 32s takes five instructions this way, where the compiler's takes some 25.
+__device__ inline uint32_t page_of(const PagesArgs& a, uint32_t token) { return (uint32_t)((uint64_t)(token / kUnit) * a.times >> a.shift); }
 __device__ inline int pages_of(const PagesArgs& a, int tokens) {
-    return (int)min((tokens + (int64_t)a.page - 1) / a.page, (int64_t)a.table_ld);
+    return (int)min(page_of(a, (uint32_t)tokens + (uint32_t)a.page - 1), (uint32_t)a.table_ld);   // (below 2^31 + 2^24)
 }
 __device__ inline bool is_page(const PagesArgs& a, int p) { return p >= 0 && p < a.pages; }
 
@@ -53,6 +55,11 @@ __global__ __launch_bounds__(256) void k_pages_init(int pages, int32_t* pool) {
 // entry that is given back or from the list itself, not from the table; what is put on the list goes where nothing was; and
 // the lengths and counts are written by the workgroup that is the last to be done with reading.
 constexpr int kSeqsAtOnce = 8192, kAtOnce = 4;   // kAtOnce: items of a thread that are on their way together
+// What bounds it: the sums' instructions, which every workgroup has for itself, and the way to memory and back (lengths, table,
+// list, one after the other, and the count of workgroups that are done).  In us, a call that takes and one that gives back: 96
+// sequences of one row 3.6 and 4.2, 61 prompts of 282 thousand rows and 4400 pages 11.6 and 8.0, 4096 drafts of 139 thousand rows and
+// 4300 pages 13.8 and 14.2.  Up to kFewSeqs sequences take little LDS (with that of more, the 96 take 6.1 and 5.4).
+constexpr int kFewSeqs = 1024;
 
 // a + b, at most `most`: associative for numbers that are at most that.
 __device__ inline uint32_t add_to(uint32_t a, uint32_t b, uint32_t most) { return min(a + b, most); }
@@ -62,11 +69,12 @@ __device__ inline uint32_t add_dpp_to(uint32_t v, uint32_t most) {
     return add_to(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false), most);
 }
 
+template <int SEQS>
 struct PagesLds {
     uint32_t wave[3][kThreads / 64];
     int last;
-    uint32_t row[kSeqsAtOnce + 1], come[kSeqsAtOnce + 1], gone[kSeqsAtOnce + 1];   // before a sequence
-    int had[kSeqsAtOnce];                                                          // its pages
+    uint32_t row[SEQS + 1], come[SEQS + 1], gone[SEQS + 1];   // before a sequence
+    int had[SEQS];                                            // its pages
 };
 
 // The last sequence whose sum before it is at most i (that has the i-th item, for an i below the total).
@@ -85,8 +93,8 @@ struct SumArrays {
 };
 // Numbers per sequence become the sums before each (one entry more: the total), K arrays at once.  A thread has `per`
 // neighbouring sequences, an odd number, so that the threads' places are in different banks.
-template <int K>
-__device__ inline void sums_before(const SumArrays& arrays, int batch, const uint32_t* most, PagesLds& lds, uint32_t* total) {
+template <int K, int SEQS>
+__device__ inline void sums_before(const SumArrays& arrays, int batch, const uint32_t* most, PagesLds<SEQS>& lds, uint32_t* total) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = ((batch + kThreads - 1) / kThreads) | 1, b0 = min(tid * per, batch), b1 = min(b0 + per, batch);
     uint32_t sum[K];
@@ -124,19 +132,33 @@ __device__ inline void sums_before(const SumArrays& arrays, int batch, const uin
     __syncthreads();
 }
 
+template <int SEQS>
 __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
-    __shared__ PagesLds lds;
+    __shared__ PagesLds<SEQS> lds;
     const int tid = threadIdx.x, batch = a.batch;
     const uint32_t most[3] = {0x7FFFFFFFu, 0x7FFFFFFFu, (uint32_t)a.rows};
     const int free0 = a.pool[0];
     const uint32_t free = (uint32_t)(free0 < 0 ? 0 : min(free0, a.pages));
     int32_t* const list = a.pool + 4;
-    for (int b = tid; b < batch; b += kThreads) {
-        const int len = max(a.len[b], 0), want = max(a.want[b], 0), had = pages_of(a, len), gets = pages_of(a, want);
-        lds.row[b] = (uint32_t)min(max(want - len, 0), a.rows);
-        lds.come[b] = (uint32_t)max(gets - had, 0);
-        lds.gone[b] = (uint32_t)max(had - gets, 0);
-        lds.had[b] = had;
+    for (int b0 = 0; b0 < batch; b0 += kAtOnce * kThreads) {   // (what a run of sequences leaves out is left out by all)
+        int len[kAtOnce], want[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++) {
+            if (b0 + k * kThreads >= batch) break;
+            const int b = min(b0 + k * kThreads + tid, batch - 1);
+            len[k] = a.len[b];
+            want[k] = a.want[b];
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++) {
+            if (b0 + k * kThreads >= batch) break;
+            const int b = b0 + k * kThreads + tid, l = max(len[k], 0), w = max(want[k], 0), had = pages_of(a, l), gets = pages_of(a, w);
+            if (b >= batch) continue;
+            lds.row[b] = (uint32_t)min(max(w - l, 0), a.rows);
+            lds.come[b] = (uint32_t)max(gets - had, 0);
+            lds.gone[b] = (uint32_t)max(had - gets, 0);
+            lds.had[b] = had;
+        }
     }
     __syncthreads();
     uint32_t total[3];
@@ -151,14 +173,23 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
         return a.table[(int64_t)b * a.table_ld + (lds.had[b] - (int)(lds.gone[b + 1] - i))];
     };
     bool holes = false;
+    int first[kAtOnce];                       // entries tid + k kThreads
     if (gone > 0) {
         int bad = 0;
-        for (uint32_t i0 = tid; i0 < gone; i0 += kAtOnce * kThreads) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++)
+            if (tid + k * kThreads < gone) first[k] = entry(tid + k * kThreads);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++)
+            if (tid + k * kThreads < gone) bad |= !is_page(a, first[k]);
+        for (uint32_t i0 = tid + kAtOnce * kThreads; i0 < gone; i0 += kAtOnce * kThreads) {
             int p[kAtOnce];
 #pragma unroll
-            for (int k = 0; k < kAtOnce; k++) p[k] = i0 + k * kThreads < gone ? entry(i0 + k * kThreads) : 0;
+            for (int k = 0; k < kAtOnce; k++)
+                if (i0 + k * kThreads < gone) p[k] = entry(i0 + k * kThreads);
 #pragma unroll
-            for (int k = 0; k < kAtOnce; k++) bad |= !is_page(a, p[k]);
+            for (int k = 0; k < kAtOnce; k++)
+                if (i0 + k * kThreads < gone) bad |= !is_page(a, p[k]);
         }
         holes = __syncthreads_or(bad);
     }
@@ -205,30 +236,38 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
             if (i < come) a.table[(int64_t)b[k] * a.table_ld + lds.had[b[k]] + (i - lds.come[b[k]])] = p[k];
         }
     }
-    for (uint32_t i0 = come + last; i0 < gone; i0 += kAtOnce * threads) {
+    const auto put = [&](uint32_t i, int page) {
+        if (i >= come && i < gone && top - 1 - i < (uint32_t)a.pages) list[top - 1 - i] = page;
+    };
+    const bool kept = gridDim.x == 1 && !holes;
+    if (kept) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++) put(tid + k * kThreads, first[k]);
+    }
+    const uint32_t behind = kept ? kAtOnce * kThreads : 0;
+    for (uint32_t i0 = max(come, behind) + last; i0 < gone; i0 += kAtOnce * threads) {
         int p[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; k++)
             if (i0 + k * threads < gone) p[k] = returned(i0 + k * threads);
 #pragma unroll
-        for (int k = 0; k < kAtOnce; k++) {
-            const uint32_t i = i0 + k * threads;
-            if (i < gone && top - 1 - i < (uint32_t)a.pages) list[top - 1 - i] = p[k];
-        }
+        for (int k = 0; k < kAtOnce; k++) put(i0 + k * threads, p[k]);
     }
     if (a.pos || a.slot) {
         for (uint32_t r0 = at; r0 < rows; r0 += kAtOnce * threads) {
             int b[kAtOnce], t[kAtOnce], j[kAtOnce], p[kAtOnce];
 #pragma unroll
             for (int k = 0; k < kAtOnce; k++) {
-                const uint32_t r = min(r0 + k * threads, rows - 1);
+                const uint32_t r = r0 + k * threads;
+                if (r >= rows) break;
                 b[k] = holder(lds.row, batch, r);
                 t[k] = max(a.want[b[k]], 0) - (int)(lds.row[b[k] + 1] - r);
             }
             if (a.slot) {
 #pragma unroll
                 for (int k = 0; k < kAtOnce; k++) {
-                    j[k] = t[k] / a.page;
+                    if (r0 + k * threads >= rows) break;
+                    j[k] = (int)page_of(a, (uint32_t)t[k]);
                     const int had = lds.had[b[k]];
                     p[k] = -1;
                     if (j[k] < had) p[k] = a.table[(int64_t)b[k] * a.table_ld + j[k]];
@@ -257,7 +296,20 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
     } else {
         __syncthreads();
     }
-    for (int b = tid; b < batch; b += kThreads) a.len[b] = max(a.want[b], 0);
+    for (int b0 = 0; b0 < batch; b0 += kAtOnce * kThreads) {
+        int want[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++) {
+            if (b0 + k * kThreads >= batch) break;
+            want[k] = a.want[min(b0 + k * kThreads + tid, batch - 1)];
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; k++) {
+            if (b0 + k * kThreads >= batch) break;
+            const int b = b0 + k * kThreads + tid;
+            if (b < batch) a.len[b] = max(want[k], 0);
+        }
+    }
     if (tid == 0) {
         a.pool[0] = (int)min(top > come ? top - come : 0u, (uint32_t)a.pages);
         a.pool[1] = (int)(come > top ? come - top : 0u);
@@ -353,8 +405,10 @@ hipError_t launch_pages_init(int pages, int32_t* pool, hipStream_t s) {
 hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s) {
     if (a.batch <= kSeqsAtOnce && (int64_t)a.batch * a.table_ld <= 0x7FFFFFFF) {
         const int64_t rows = a.pos || a.slot ? a.rows : 0;
+        const bool few = a.batch <= kFewSeqs;
         const int64_t n = std::max<int64_t>(1, std::min<int64_t>(128, (rows + kThreads - 1) / kThreads));
-        hipLaunchKernelGGL(k_pages_assign, dim3((unsigned)n), dim3(kThreads), 0, s, a);
+        if (few) hipLaunchKernelGGL((k_pages_assign<kFewSeqs>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((k_pages_assign<kSeqsAtOnce>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(k_pages_assign_many, dim3(1), dim3(kThreads), 0, s, a);

@@ -623,7 +623,10 @@ wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, c
     if ((int64_t)table_ld * q.page > 0x7FFFFFFF) return WQ_ERR_SHAPE;
     if (want == len) return WQ_ERR_INVALID_ARG;   // (lengths are written while others are still read)
     if (batch == 0) return WQ_OK;
-    const wq::PagesArgs a = {len, want, table, pool, row_start, pos, slot, batch, table_ld, q.page, (int)q.pages, rows};
+    wq::PagesArgs a = {len, want, table, pool, row_start, pos, slot, batch, table_ld, q.page, (int)q.pages, rows, 0, 0};
+    // with 2^(shift - 27) >= upp, times is off by less than upp / 2^shift of itself, and x of 27 bits makes less than 1 / upp of that
+    for (a.shift = 27; (1 << (a.shift - 27)) < q.upp; a.shift++) {}
+    a.times = (uint32_t)(((uint64_t(1) << a.shift) + q.upp - 1) / q.upp);
     return from_hip(wq::launch_pages_assign(a, static_cast<hipStream_t>(stream)));
 }
 

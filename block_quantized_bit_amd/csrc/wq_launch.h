@@ -101,6 +101,8 @@ struct PagesArgs {
     int32_t* pos;          // [rows], or null
     int64_t* slot;         // [rows], or null
     int32_t batch, table_ld, page, pages, rows;
+    uint32_t times;        // a whole number x below 2^27 has x / (page / 32) = x times >> shift
+    int32_t shift;
 };
 hipError_t launch_pages_init(int pages, int32_t* pool, hipStream_t s);
 hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s);
