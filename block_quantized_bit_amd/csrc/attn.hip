@@ -359,8 +359,8 @@ void launch_join(const AttnArgs& a, int64_t items, int cols, hipStream_t s) {
 
 // A launch has fewer than 2^32 threads.
 bool attn_fits(const AttnArgs& a) {
-    const Schedule s = schedule(a, true);
-    return s.items * s.splits < (int64_t(1) << 23);
+    const Schedule s = schedule(a, true), w = schedule(a, false);   // with and without a workspace
+    return std::max(s.items * s.splits, w.items) < (int64_t(1) << 23);
 }
 
 size_t attn_workspace_bytes(const AttnArgs& a) {

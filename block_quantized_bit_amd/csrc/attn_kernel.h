@@ -552,10 +552,11 @@ __device__ inline void each_part(const AttnArgs& a, const TileShape& shape, F se
             ua = 0;
             ub = un.count;
         } else {
-            while (w - before >= tiles * heads * span) {   // on to the sequence that has w
+            while (w - before >= tiles * heads * span && seq + 1 < a.s.batch) {   // on to the sequence that has w
                 before += tiles * heads * span;
                 begin(++seq);
             }
+            if (w - before >= tiles * heads * span) break;   // (none has: the lengths are others than when they were summed)
             const int item = (w - before) / span, s0 = (w - before) - item * span, s1 = min(span, s0 + (end - w));
             step = s1 - s0;
             tile = item / heads;

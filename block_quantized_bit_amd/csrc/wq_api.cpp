@@ -647,7 +647,7 @@ wq_status wq_cache_keep(const wq_cache_desc* d, const wq_seqs* s, const int32_t*
             if (caches[i] == caches[j]) return WQ_ERR_INVALID_ARG;   // its rows would be moved twice
         a.cache[i] = static_cast<uint8_t*>(caches[i]);
     }
-    if (want && want == s->len) return WQ_ERR_INVALID_ARG;           // (other workgroups still read the lengths)
+    if (want && (want == s->len || want == count || want == path)) return WQ_ERR_INVALID_ARG;   // (other workgroups still read them)
     if (a.s.batch == 0) return WQ_OK;
     a.path = path;
     a.path_ld = path_ld;

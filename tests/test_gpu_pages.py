@@ -60,7 +60,8 @@ class DevPages:
 
 # page, pages, batch, pages per sequence, rows
 POOLS = [(32, 1, 1, 1, 40), (32, 40, 1, 20, 700), (64, 100, 5, 12, 4000), (96, 500, 64, 9, 60000), (32, 3000, 65, 50, 120000),
-         (32, 900, 300, 9, 90000), (448, 700, 1025, 2, 500000), (32, 5000, 4100, 4, 600000), (2048, 70, 3, 30, 200000)]
+         (32, 900, 300, 9, 90000), (448, 700, 1025, 2, 500000), (32, 5000, 4100, 4, 600000), (2048, 70, 3, 30, 200000),
+         (32, 20000, 8192, 6, 1100000), (32, 9000, 9001, 3, 900000)]
 
 
 @pytest.mark.parametrize("i", range(len(POOLS)))
@@ -160,6 +161,37 @@ def test_pages_graph_replays():
         out = h.assign(w, 20000)
         g.replay()
         d.check(h, out, f"replay {k}")
+
+
+def test_two_pools_on_two_streams():
+    rng = np.random.default_rng(9)
+    h, d = ([f(64, 600, 40, 20) if f is HostPages else f(64, 600, 40, 20, 40000) for _ in range(2)] for f in (HostPages, DevPages))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wants = [_i32(rng.integers(0, 900, 40)) for _ in range(10)]
+    torch.cuda.synchronize()
+    out = [None, None]
+    for k in range(5):
+        for i in range(2):
+            w = wants[2 * k + i]
+            out[i] = h[i].assign(w.cpu().tolist(), 40000)
+            x = d[i]
+            wq.wq_pages_assign(x.desc, 40, x.len, w, x.table, 20, x.pool, 40000, x.start, x.pos, x.slot, stream=streams[i])
+    for i in range(2):
+        d[i].check(h[i], out[i], f"pool {i}")
+
+
+def test_keep_in_many_caches():
+    """As many caches as a call takes; each has its own bytes moved."""
+    c = Case(Q4_1, 64, 1, 32, [9, 4], [40, 33], seed=2)
+    caches = [torch.from_numpy(c.rng.integers(0, 256, c.cache.numel(), dtype=np.uint8)).to(DEV) for _ in range(64)]
+    before = [x.clone() for x in caches]
+    path, count = _i32([[1, 4, 8], [0, 3, 9]]), _i32([3, 3])
+    wq.wq_cache_keep(c.desc, c.seqs, path, 3, count, caches)
+    for x, y in zip(caches, before):
+        wq.wq_cache_keep(c.desc, c.seqs, path, 3, count, [y])
+        assert torch.equal(x, y)
+    a, z = _rows_of(c, caches[63], 0, np.array([31, 32, 33])), _rows_of(c, before[63], 0, np.array([31, 32, 33]))
+    assert all(np.array_equal(x, y) for x, y in zip(a, z))
 
 
 def _rows_of(c, cache, b, tokens, fmt=None):

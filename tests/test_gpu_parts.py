@@ -302,3 +302,40 @@ def test_calls_on_two_streams(orc):
     torch.cuda.synchronize()
     for i in range(2):
         assert np.array_equal(Y[i].cpu().numpy().view(np.uint16).reshape(want[i].shape), want[i])
+
+
+def test_one_row_each_without_starts(orc):
+    """A draft of one token per sequence, without row starts and in pages without a table; lengths below zero and past the
+    last page."""
+    for fmt, dim, group in ((Q4_0, 64, 2), (Q4_1, 128, 20)):
+        c = Case(fmt, dim, 2, 64, [1] * 5, [0, 1, 64, 40, 17], seed=12, one_row=True, paged=False)
+        _check(orc, c, group, 0, 0, trees(c.rng, c.counts, "tree"))
+        _check(orc, c, group, 10, 3, trees(c.rng, c.counts, "any"))
+        _check(orc, c, group, 7, 5)
+    c = Case(Q4_0, 64, 2, 64, [1, 7, 1], [100, 90, 30], seed=13)
+    c.fill(*c.random_kv())
+    q = _q(c, 2)
+    tree = dev_words(words(trees(c.rng, c.counts, "chain"), 1, c.rows))
+    want = run_seen(c, q, 2, 0.1, 0, 0, tree)[1]
+    c.d_len.copy_(torch.tensor([100, -3, 30], dtype=torch.int32))
+    for t, window, sinks in ((tree, 0, 0), (tree, 9, 3), (None, 9, 3)):
+        got = run_seen(c, q, 2, 0.1, window, sinks, t)[1]
+        assert not got[1:8].any()
+        if not window:
+            assert np.array_equal(got[0], want[0]) and np.array_equal(got[8], want[8])
+    c.d_len.copy_(torch.tensor([100000, 90, 2**31 - 1], dtype=torch.int32))
+    for t, window, sinks in ((tree, 0, 0), (None, 9, 3)):
+        got = run_seen(c, q, 2, 0.1, window, sinks, t)[0]
+        assert np.isfinite(got[1:8]).all()                            # (others' pages hold anything past their lengths)
+
+
+def test_every_width_of_tile(orc):
+    """Calls of the sizes at which tiles of 16, 32, 128 and 256 columns are taken, whole and shared out, with and without a
+    workspace."""
+    for dim, heads, batch, rows, length in ((128, 8, 40, 12, 70), (128, 20, 10, 32, 90), (64, 20, 12, 128, 140), (96, 16, 30, 9, 100),
+                                            (256, 4, 6, 45, 120), (128, 1, 2, 20, 5000), (64, 1, 1, 60, 4300), (96, 1, 1, 130, 4400)):
+        say("width", dim, heads, batch, rows, length)
+        c = Case(Q4_0 if rows % 2 else Q4_1, dim, heads, 64, [max(1, rows - i % 3) for i in range(batch)], [length - i for i in range(batch)], seed=rows)
+        masks = trees(c.rng, c.counts, "tree")
+        _check(orc, c, 4 if dim * rows < 8000 else 2, 0, 0, masks)
+        _check(orc, c, 3, 60, 5, masks)

@@ -92,6 +92,7 @@ def test_keep_refusals():
     for name in ("path", "count"):
         assert _keep(**{name: None}) == 1 and _keep(**{name: FAKE + 2}) == 4, name
     assert _keep(want=FAKE + 1) == 4 and _keep(want=FAKE) == 1        # the lengths are still read
+    assert _keep(want=5 * FAKE, count=5 * FAKE) == 1 and _keep(want=5 * FAKE, path=5 * FAKE) == 1
     assert _keep(ld=0) == 1 and _keep(ld=-1) == 1
     assert _keep(caches=[]) == 1 and _keep(caches=[FAKE, None]) == 1 and _keep(caches=[FAKE, 2 * FAKE + 8]) == 4
     assert _keep(caches=[FAKE, 2 * FAKE, FAKE]) == 1                  # one cache twice
@@ -122,6 +123,15 @@ def test_more_tiles_than_a_launch_has():
         s = _seqs(batch=batch, rows=batch)
         assert _status(wq.wq_attn_tree_workspace_size, d, s, 128, 0, 0) == want
         assert _status(wq.wq_attn_sinks_workspace_size, d, s, 128, 9, 0) == want
+
+
+def test_more_tiles_without_a_workspace():
+    """Whole tiles of a call without a workspace can be narrower, and more, than those that are shared out."""
+    d = _desc(head_dim=64, kv_heads=64)
+    s = _seqs(batch=40000, rows=4000000, row_start=FAKE, table_ld=1000)   # 100 columns: 4.5 million tiles of 128, 10.5 of 32
+    assert _status(wq.wq_attn_tree_workspace_size, d, s, 64, 0, 0) == 3
+    s = _seqs(batch=20000, rows=2000000, row_start=FAKE, table_ld=1000)
+    assert _status(wq.wq_attn_tree_workspace_size, d, s, 64, 0, 0) == 0
 
 
 @pytest.mark.parametrize("past", [1 << 32, -(1 << 32), 1 << 31])
