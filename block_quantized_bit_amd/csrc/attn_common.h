@@ -332,7 +332,7 @@ struct Partials {
         : o(reinterpret_cast<float*>(a.ws)), ml(o + (int64_t)a.slots * a.tile_cols * a.dim), dim(a.dim), cols(a.tile_cols) {}
     __device__ float* sums(int slot, int col) const { return o + ((int64_t)slot * cols + col) * dim; }
     __device__ float* stat(int slot, int col) const { return ml + ((int64_t)slot * cols + col) * 2; }
-    // (at most 1024 slots of 16 columns, or 256 of 128, of 256 channels: offsets fit 32 bits)
+    // (at most 2^17 columns of 256 channels: offsets fit 32 bits)
     __device__ f32x4 read(int slot, int col, int ch) const {
         return load_at<f32x4>((global_bytes)(uintptr_t)o, (uint32_t)(((slot * cols + col) * dim + ch) * 4));
     }

@@ -504,8 +504,8 @@ __device__ inline void each_segment(const AttnArgs& a, const TileShape& ts, F se
     if (threadIdx.x == 0) *open_tile(a, blockIdx.x) = open;
 }
 
-// The same for a draft's tiles, with the segment's code once for both kinds of call.  A sequence's rows are spread evenly over
-// its tiles.
+// The same for a draft's tiles of 32 columns or more, with the segment's code once for both kinds of call.  A sequence's rows are
+// spread evenly over its tiles.
 template <class F>
 __device__ inline void each_part(const AttnArgs& a, const TileShape& shape, F segment) {
     const int heads = a.s.heads;
@@ -1047,7 +1047,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
     rows_segment<NB, Q41, NW, KS, PARTS>(a, ts, q, seq, tile, h, un, u0, u1, po, pm, lds);
 }
 
-// The same with the work shared out evenly, as in k_attn_token.
+// The same with the work shared out evenly (each_part).  Beginning a tile takes some 12 us here (three steps' conversions before the
+// first product), so wide tiles are shared out over fewer workgroups: one draft of 127 rows over 100003 tokens, 8 x 8 heads of 128, q4_0
+// (four tiles of 256 columns for each head; 416 GFLOP), 451 us with the join, 924 TFLOP/s.
 template <int NB, bool Q41, int NW, int KS>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows_shared(AttnArgs a) {
     __shared__ RowsLds<NB, NW, KS, true> lds;

@@ -10,6 +10,7 @@ void launch_shared_as(const AttnArgs& a, dim3 grid, hipStream_t s) {
     if (a.q41) hipLaunchKernelGGL((k_attn_rows_shared<NB, true, NW, KS>), grid, dim3(NW * 64), 0, s, a);
     else hipLaunchKernelGGL((k_attn_rows_shared<NB, false, NW, KS>), grid, dim3(NW * 64), 0, s, a);
 }
+
 }  // namespace
 
 void launch_parts_shared(const AttnArgs& a, dim3 grid, bool wide, hipStream_t s) {

@@ -1,10 +1,14 @@
 // attn_wide.hip -- attention of drafts, whose rows and heads are several tiles of 16 columns per key/value head: a wave takes
-// CT of them together.
+// CT of them together (two).
 //
 // As in k_attn_token a wave has units of its own, fetched into a ring in LDS, and a lane's words are the operands of the
 // products as they lie; here a unit's words are made fp16 once for 16 CT columns.  Per unit of 128 channels that is some 224
-// instructions beside 8 CT + 8 CT products of 16 x 16 x 32 and some 45 instructions and 8 exponentials per tile of columns, so
-// four tiles cost little more than twice what one does.  No values go through LDS, no wave waits for another before the end.
+// instructions beside 16 CT products of 16 x 16 x 32 and some 45 instructions and 8 exponentials per tile of columns.  No values
+// go through LDS, and no wave waits for another before the end.
+//
+// Bound by the vector unit and the matrix unit, which take turns more than they overlap: 32 sequences of 300 to 8191 tokens with
+// 8 drafted rows each, 8 x 4 heads of 128, q4_0: 78 us, tiles of 16 columns 94.  Four tiles (64 columns) leave one wave per SIMD and
+// were slower wherever tiles of 128 columns were not the better choice anyway.
 #include "attn_kernel.h"
 
 namespace wq {
@@ -321,8 +325,8 @@ template <int NB, bool Q41, int NW, int D, int CT, int EU>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(EU))) void k_attn_wide(AttnArgs a) {
     __shared__ WideLds<NB, Q41, NW, D, CT> lds;
     each_part(a, tile_shape(16 * CT, a.group),
-                       [&](const TileShape& ts, const SeqInfo& q, int seq, int tile, int h, const UnitList& un, int ua, int ub, float* po,
-                           float* pm) { wide_segment<NB, Q41, NW, D, CT>(a, ts, q, seq, tile, h, un, ua, ub, po, pm, lds); });
+              [&](const TileShape& ts, const SeqInfo& q, int seq, int tile, int h, const UnitList& un, int ua, int ub, float* po,
+                  float* pm) { wide_segment<NB, Q41, NW, D, CT>(a, ts, q, seq, tile, h, un, ua, ub, po, pm, lds); });
 }
 
 constexpr int kTiles = 2;

@@ -317,8 +317,8 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
     }
 }
 
-// More sequences, or more entries than 32 bits count: one workgroup, and the rows by a launch of their own.  First what is given back goes on the list's end (its front), the first sequence's first page last; then what
-// is wanted is taken from there.
+// More sequences, or more entries than 32 bits count: one workgroup, and the rows by a launch of their own.  First what is given
+// back goes on the list's end (its front), the first sequence's first page last; then what is wanted is taken from there.
 __global__ __launch_bounds__(kThreads) void k_pages_assign_many(PagesArgs a) {
     __shared__ int64_t lds[kThreads / 64];
     int32_t* const list = a.pool + 4;

@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <iterator>
 #include <mutex>
 
 #include "wq.h"
@@ -621,8 +622,10 @@ wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, c
         !aligned(pos, 4) || !aligned(slot, 8))
         return WQ_ERR_ALIGNMENT;
     if ((int64_t)table_ld * q.page > 0x7FFFFFFF) return WQ_ERR_SHAPE;
-    if (want == len) return WQ_ERR_INVALID_ARG;   // (lengths are written while others are still read)
     if (batch == 0) return WQ_OK;
+    const void* const arrays[] = {len, want, table, pool, row_start, pos, slot};
+    for (const void* const* i = arrays; i != std::end(arrays); i++)   // (some are written while others are still read)
+        if (*i && std::find(std::begin(arrays), i, *i) != i) return WQ_ERR_INVALID_ARG;
     wq::PagesArgs a = {len, want, table, pool, row_start, pos, slot, batch, table_ld, q.page, (int)q.pages, rows, 0, 0};
     // with 2^(shift - 27) >= upp, times is off by less than upp / 2^shift of itself, and x of 27 bits makes less than 1 / upp of that
     for (a.shift = 27; (1 << (a.shift - 27)) < q.upp; a.shift++) {}
@@ -639,6 +642,7 @@ wq_status wq_cache_keep(const wq_cache_desc* d, const wq_seqs* s, const int32_t*
     if ((st = check_seqs(s, &a.s)) != WQ_OK) return st;
     if (!path || !count || !caches || path_ld < 1 || n_caches < 1) return WQ_ERR_INVALID_ARG;
     if (n_caches > wq::kKeepCaches) return WQ_ERR_UNSUPPORTED;
+    if ((int64_t)a.s.batch * a.s.heads * n_caches >= (int64_t(1) << 24)) return WQ_ERR_SHAPE;   // workgroups: fewer than 2^32 threads
     if (!aligned(path, 4) || !aligned(count, 4) || !aligned(want, 4)) return WQ_ERR_ALIGNMENT;
     for (int i = 0; i < n_caches; i++) {
         if (!caches[i]) return WQ_ERR_INVALID_ARG;

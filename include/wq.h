@@ -389,8 +389,9 @@ wq_status wq_attn_sinks_workspace_size(const wq_cache_desc* d, const wq_seqs* s,
  * the tokens t <= p with t > p - window or t < sinks.
  *   window : 1 .., tokens of the sliding window (the row's own among them)
  *   sinks  : 0 .., first tokens of a sequence that every row at or behind them sees
- * All else (arguments, refusals, rounding and error bound) as for wq_attn.  Tokens between
- * the sinks and the window are not read. */
+ * All else (arguments, refusals, rounding and error bound) as for wq_attn, but that a tile may
+ * have 32 pairs too; the call has fewer than 2^23 tiles.  Tokens between the sinks and the
+ * window are not read. */
 wq_status wq_attn_sinks(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq,
                         const void* cache, float scale, int32_t window, int32_t sinks, uint16_t* y, int64_t ldy, void* ws,
                         size_t ws_bytes, void* stream);
@@ -412,7 +413,7 @@ wq_status wq_attn_tree_workspace_size(const wq_cache_desc* d, const wq_seqs* s, 
  *             whatever n is)
  *   sinks   : with a window, the context's first `sinks` tokens are seen too; else 0
  * A row that sees nothing gets zeros.  The masks are read when the work runs.  All else as
- * for wq_attn. */
+ * for wq_attn_sinks. */
 wq_status wq_attn_tree(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq,
                        const void* cache, float scale, int32_t window, int32_t sinks, const uint32_t* tree, int32_t tree_ld,
                        uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
@@ -449,7 +450,8 @@ wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
  * depend on timing.  Where there are not enough, the last wanted ones' entries become -1
  * (their tokens are absent: see wq_seqs) and word 1 of the pool says how many; tokens past
  * table_ld pages are absent too.  Negative lengths count as 0; entries that are no page are
- * not given back.  Calls on one pool or table must not run at the same time. */
+ * not given back.  No two of the arrays may overlap (WQ_ERR_INVALID_ARG where two start at
+ * one place), and calls on one pool or table must not run at the same time. */
 wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, const int32_t* want, int32_t* table,
                           int32_t table_ld, int32_t* pool, int32_t rows, int32_t* row_start, int32_t* pos, int64_t* slot,
                           void* stream);
@@ -462,7 +464,8 @@ wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, c
  *   path_ld  : 1 ..
  *   count    : device int32 [batch], entries of each path (at most path_ld count)
  *   caches   : host array of n_caches different device buffers of descriptor d, 16-byte aligned
- *   n_caches : 1 .. 64 (else WQ_ERR_UNSUPPORTED)
+ *   n_caches : 1 .. 64 (else WQ_ERR_UNSUPPORTED); batch * kv_heads * n_caches is below 2^24
+ *              (else WQ_ERR_SHAPE)
  *   want     : device int32 [batch] or NULL, out: the tokens of each sequence that are then
  *              in place, its context and the kept rows: what wq_pages_assign takes next
  * The places of rows that are not kept hold anything that was there before or was moved. */

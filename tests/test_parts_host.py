@@ -100,6 +100,23 @@ def test_keep_refusals():
     assert _keep(s=_seqs(batch=0)) == 0
 
 
+def test_pages_arrays_are_different_ones():
+    apart = dict(len=FAKE, want=2 * FAKE, table=3 * FAKE, pool=4 * FAKE, start=5 * FAKE, pos=6 * FAKE, slot=7 * FAKE)
+    for a in apart:
+        for b in apart:
+            if a != b:
+                assert _pages(**{**apart, a: apart[b]}) == 1, (a, b)
+    assert _pages(**{**apart, "pos": None, "slot": None, "pool": FAKE}) == 1
+
+
+def test_keep_more_workgroups_than_a_launch_has():
+    many = [FAKE * (i + 1) for i in range(64)]
+    s = _seqs(batch=1 << 18, rows=1 << 18)
+    assert _keep(d=_desc(kv_heads=1), s=s, caches=many) == 3
+    assert _keep(d=_desc(kv_heads=64), s=s, caches=many[:1]) == 3
+    assert _keep(d=_desc(kv_heads=8), s=_seqs(batch=1 << 20, rows=1 << 20), caches=many[:2]) == 3
+
+
 def test_nothing_to_do_is_no_launch():
     for s in (_seqs(rows=0, row_start=FAKE), _seqs(batch=0)):
         assert _sinks(s=s) == 0 and _tree(s=s) == 0
