@@ -9,6 +9,8 @@
 // Bound by the vector unit and the matrix unit, which take turns more than they overlap: 32 sequences of 300 to 8191 tokens with
 // 8 drafted rows each, 8 x 4 heads of 128, q4_0: 78 us, tiles of 16 columns 94.  Four tiles (64 columns) leave one wave per SIMD and
 // were slower wherever tiles of 128 columns were not the better choice anyway.
+// Heads of 256 have one wave per SIMD, which nothing hides the reads of LDS for: issued early (below) they take 16 sequences' 25 rows
+// over 4096 tokens and 4 first ones, 2 x 8 heads, q4_1, from 97 to 87 us.  A ring of three units there gained nothing.
 #include "attn_kernel.h"
 
 namespace wq {
@@ -28,27 +30,58 @@ template <int NB, bool Q41, bool EDGE, int CT>
 __device__ inline bool wide_step(const AttnArgs& a, const SeqInfo& q, const uint8_t* unit, const uint8_t* queries, const float (&sl2)[CT],
                                  int t0, const Column* columns, uint32_t f1024, f16x2 s16, WideState<NB, CT>* st) {
     using R = UnitRing<NB, Q41>;
+    // Heads of 256 leave one wave per SIMD, so reads of LDS are issued well before their use, which takes registers that there are.
+    constexpr bool early = NB > 4;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     f32x4 s[CT][2];
-    uint32_t kw[2 * NB];
+    uint32_t kw[2 * NB], vw[2 * NB], vd[2][NB][2], vm[2][NB][2];
+    const auto read_values = [&]() {
+        read_words<NB>(unit + R::half, lane, vw);
+#pragma unroll
+        for (int tile = 0; tile < 2; tile++) {
+            read_scales<NB, NB>(unit + R::half + 16 * R::dim, g, tile, 0, vd[tile]);
+            if constexpr (Q41) read_scales<NB, NB>(unit + R::half + 16 * R::dim + R::plane, g, tile, 0, vm[tile]);
+        }
+    };
     read_words<NB>(unit, lane, kw);
 #pragma unroll
     for (int c = 0; c < CT; c++) s[c][0] = s[c][1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
     // (the lane's words are one token's: 4 (r / 4) + r % 4 of the tile)
     const uint8_t* const sc = unit + 16 * R::dim + ((lane & 15) >> 2) * NB * 8 + (lane & 3) * 2;
-#pragma unroll
-    for (int b = 0; b < NB; b++) {
-        f16x8 k[2];
+    _Float16 kd[2][NB], km[2][NB];
+    const auto read_key_scales = [&](int b) {
 #pragma unroll
         for (int tile = 0; tile < 2; tile++) {
             const uint8_t* const at = sc + (tile * 4 * NB + b) * 8;
-            const _Float16 d1 = *reinterpret_cast<const _Float16*>(at);
-            const f16x2 d = {d1, d1};
+            kd[tile][b] = *reinterpret_cast<const _Float16*>(at);
+            if constexpr (Q41) km[tile][b] = *reinterpret_cast<const _Float16*>(at + R::plane);
+        }
+    };
+    f16x8 qf[2][CT];
+    const auto read_queries = [&](int b) {
+#pragma unroll
+        for (int c = 0; c < CT; c++) qf[b & 1][c] = *reinterpret_cast<const f16x8*>(queries + ((c * NB + b) * 64 + lane) * 16);
+    };
+    if constexpr (early) {
+#pragma unroll
+        for (int b = 0; b < NB; b++) read_key_scales(b);
+        read_queries(0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+        if constexpr (early) {
+            if (b + 1 < NB) read_queries(b + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            read_key_scales(b);
+        }
+        f16x8 k[2];
+#pragma unroll
+        for (int tile = 0; tile < 2; tile++) {
+            const f16x2 d = {kd[tile][b], kd[tile][b]};
             f16x2 m = {};
-            if constexpr (Q41) {
-                const _Float16 m1 = *reinterpret_cast<const _Float16*>(at + R::plane);
-                m = (f16x2){m1, m1};
-            }
+            if constexpr (Q41) m = (f16x2){km[tile][b], km[tile][b]};
             u32x4 u;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -57,11 +90,11 @@ __device__ inline bool wide_step(const AttnArgs& a, const SeqInfo& q, const uint
             }
             k[tile] = __builtin_bit_cast(f16x8, u);
         }
+        if constexpr (!early) read_queries(b);
 #pragma unroll
         for (int c = 0; c < CT; c++) {
-            const f16x8 qf = *reinterpret_cast<const f16x8*>(queries + ((c * NB + b) * 64 + lane) * 16);
-            s[c][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[0], qf, s[c][0], 0, 0, 0);
-            s[c][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[1], qf, s[c][1], 0, 0, 0);
+            s[c][0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[0], qf[b & 1][c], s[c][0], 0, 0, 0);
+            s[c][1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[1], qf[b & 1][c], s[c][1], 0, 0, 0);
         }
     }
     uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};    // token pairs that are in the cache: what lies behind them is anything
@@ -69,6 +102,10 @@ __device__ inline bool wide_step(const AttnArgs& a, const SeqInfo& q, const uint
 #pragma unroll
         for (int j = 0; j < 8; j++)
             if (t0 + (j >> 2) * 16 + 4 * g + (j & 3) >= q.tokens) keep[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+    if constexpr (early) {
+        read_values();
+        __builtin_amdgcn_sched_barrier(0);
     }
     float e[CT][8], most = -INFINITY;
 #pragma unroll
@@ -115,45 +152,33 @@ __device__ inline bool wide_step(const AttnArgs& a, const SeqInfo& q, const uint
         for (int j = 0; j < 4; j++) p[j] = pack_f16(x[2 * j], x[2 * j + 1]);
         pf[c] = __builtin_bit_cast(f16x8, p);
     }
-    // (at most four blocks' scales in registers at a time)
-    constexpr int BG = NB > 4 ? 4 : NB;
+    if constexpr (!early) read_values();
 #pragma unroll
-    for (int b0 = 0; b0 < NB; b0 += BG) {
-        if (b0 > 0) asm volatile("" ::: "memory");
-        uint32_t vw[2 * BG], vd[2][BG][2], vm[2][BG][2];
-        read_words<BG>(unit + R::half + b0 * 512, lane, vw);
+    for (int b = 0; b < NB; b++) {
+        u32x4 vlo, vhi;
 #pragma unroll
         for (int tile = 0; tile < 2; tile++) {
-            read_scales<NB, BG>(unit + R::half + 16 * R::dim, g, tile, b0, vd[tile]);
-            if constexpr (Q41) read_scales<NB, BG>(unit + R::half + 16 * R::dim + R::plane, g, tile, b0, vm[tile]);
+            const uint32_t w = vw[2 * b + tile], wl = w & 0x0F0F0F0Fu, wh = w & 0xF0F0F0F0u;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const uint32_t in = EDGE ? keep[2 * tile + i] : ~0u;
+                const f16x2 d = as_f16x2(vd[tile][b][i] & in);
+                const f16x2 cl = byte_pair(wl, i) - (_Float16)(Q41 ? 1024.0f : 1032.0f), ch = sixteenth<Q41 ? 0 : 8>(byte_pair(wh, i), s16);
+                f16x2 lo2 = cl * d, hi2 = ch * d;
+                if constexpr (Q41) {
+                    const f16x2 m = as_f16x2(vm[tile][b][i] & in);
+                    lo2 = __builtin_elementwise_fma(cl, d, m);
+                    hi2 = __builtin_elementwise_fma(ch, d, m);
+                }
+                vlo[2 * tile + i] = __builtin_bit_cast(uint32_t, lo2);
+                vhi[2 * tile + i] = __builtin_bit_cast(uint32_t, hi2);
+            }
         }
 #pragma unroll
-        for (int b = 0; b < BG; b++) {
-            u32x4 vlo, vhi;
-#pragma unroll
-            for (int tile = 0; tile < 2; tile++) {
-                const uint32_t w = vw[2 * b + tile], wl = w & 0x0F0F0F0Fu, wh = w & 0xF0F0F0F0u;
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const uint32_t in = EDGE ? keep[2 * tile + i] : ~0u;
-                    const f16x2 d = as_f16x2(vd[tile][b][i] & in);
-                    const f16x2 cl = byte_pair(wl, i) - (_Float16)(Q41 ? 1024.0f : 1032.0f), ch = sixteenth<Q41 ? 0 : 8>(byte_pair(wh, i), s16);
-                    f16x2 lo2 = cl * d, hi2 = ch * d;
-                    if constexpr (Q41) {
-                        const f16x2 m = as_f16x2(vm[tile][b][i] & in);
-                        lo2 = __builtin_elementwise_fma(cl, d, m);
-                        hi2 = __builtin_elementwise_fma(ch, d, m);
-                    }
-                    vlo[2 * tile + i] = __builtin_bit_cast(uint32_t, lo2);
-                    vhi[2 * tile + i] = __builtin_bit_cast(uint32_t, hi2);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < CT; c++) {
-                f32x4* const o = st->o[c] + 2 * (b0 + b);
-                o[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vlo), pf[c], o[0], 0, 0, 0);
-                o[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vhi), pf[c], o[1], 0, 0, 0);
-            }
+        for (int c = 0; c < CT; c++) {
+            f32x4* const o = st->o[c] + 2 * (b);
+            o[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vlo), pf[c], o[0], 0, 0, 0);
+            o[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, vhi), pf[c], o[1], 0, 0, 0);
         }
     }
     return true;
