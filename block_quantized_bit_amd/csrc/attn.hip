@@ -292,8 +292,18 @@ int64_t seen_units(const AttnArgs& a, int64_t most) {
 //            32 x 128,  8191   300    240    157    204
 //             8 x 256, 30000   507    399    264    237
 // Wider tiles share conversions, but take more registers and longer to begin: they pay where there are enough of them for the
-// chip, or they are shared out.  Sharing out costs some 15 us (finding the work, and the join), as for single tokens.  Heads of 256
-// leave tiles of 32 columns one wave per SIMD (16 x 200 columns of 4096 tokens, 2 heads: 115 and 106 us).
+// chip, or they are shared out.  Sharing out costs some 15 us (finding the work, and the join), as for single tokens.
+// Heads of 256 leave tiles of 32 columns one wave per SIMD, and those of 128 one workgroup per compute unit.  2 x 8 heads, q4_1
+// (=: all of that length):
+//   tiles of                    16     32    128
+//   whole    16 x 200,  4000   107     86    281
+//            32 x 200,  1000    67     69     91
+//            64 x 512,   500   174    207    133
+//   shared   16 x  96, =12000  131    109    129
+//   out      16 x 200, =12000  276    209    238
+//            16 x 200, 20000   251    245    217
+//            16 x 512,  8191   276    285    216
+//             4 x 512, =8000   123     92    120
 void draft_schedule(const AttnArgs& a, bool share, int64_t most, int64_t units, int64_t cols, Schedule* s) {
     const auto items = [&](int c) { return tile_bound(tile_shape(c, a.group), a.s.rows, a.s.batch, false) * a.s.heads; };
     const auto take = [&](int c, int workgroups) {
@@ -303,9 +313,10 @@ void draft_schedule(const AttnArgs& a, bool share, int64_t most, int64_t units, 
     };
     const bool lengthy = units > (items(kTokenCols) < 256 ? 64 : 128);
     if (a.dim == 256) {
-        if (cols >= 512) take(128, lengthy ? kShareWorkgroups / 2 : 0);
-        else if (cols >= 160) take(32, lengthy && items(32) < 128 ? kShareWorkgroups / 2 : 0);
-        else take(kTokenCols, lengthy ? kShareWorkgroups : 0);
+        const bool out = lengthy && share;
+        if (cols >= 160 && items(128) >= (out ? 64 : 256) && (!out || units >= 256 || cols >= 512)) take(128, out ? kShareWorkgroups / 2 : 0);
+        else if (units >= 64 && cols >= (out ? 80 : 160)) take(32, out && (items(32) < 192 || units >= 256) ? kShareWorkgroups / 2 : 0);
+        else take(kTokenCols, out ? kShareWorkgroups : 0);
     } else if (lengthy && share) {
         if (cols > 64) take(cols < 256 ? 128 : 256, cols < 256 ? kShareWorkgroups : kShareWorkgroups / 2);
         else take(32, kShareWorkgroups);
