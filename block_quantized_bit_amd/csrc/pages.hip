@@ -49,14 +49,16 @@ __global__ __launch_bounds__(256) void k_pages_init(int pages, int32_t* pool) {
     if (i < (uint32_t)pages) pool[4 + (int64_t)i] = pages - 1 - (int)i;
 }
 
-// The call in one launch, for up to kSeqsAtOnce sequences.  Every workgroup makes the sums over all sequences for itself, in LDS
-// (rows, pages wanted, pages given back, each before a sequence), and then does its share of the rows, of the table's new
-// entries and of the list's.  Nothing that a workgroup reads is written by another: the page of a wanted entry comes from the
-// entry that is given back or from the list itself, not from the table; what is put on the list goes where nothing was; and
-// the lengths and counts are written by the workgroup that is the last to be done with reading.
+// The call for up to kSeqsAtOnce sequences.  Every workgroup makes the sums over all sequences for itself, in LDS (rows, pages
+// wanted, pages given back, each before a sequence), and then does its share of the rows, of the table's new entries and of the
+// list's.  Nothing that a workgroup reads is written by another: the page of a wanted entry comes from the entry that is given
+// back or from the list itself, not from the table; what is put on the list goes where nothing was; and the lengths and the
+// count of free pages, which all of them read, are written by a launch after it (k_pages_settle) if there are several.  (The
+// workgroup that is the last to be done could write them, by a counter in the pool; but that goes by what the caller has there,
+// and its round trips cost more: two calls, of 4096 drafts 28.3 us and 27.0 now, of 61 prompts 19.3 and 17.7.)
 constexpr int kSeqsAtOnce = 8192, kAtOnce = 4;   // kAtOnce: items of a thread that are on their way together
 // What bounds it: the sums' instructions, which every workgroup has for itself, and the way to memory and back (lengths, table,
-// list, one after the other, and the count of workgroups that are done).  In us, a call that takes and one that gives back: 96
+// list, one after the other).  In us, a call that takes and one that gives back: 96
 // sequences of one row 3.6 and 4.2, 61 prompts of 282 thousand rows and 4400 pages 11.6 and 8.0, 4096 drafts of 139 thousand rows and
 // 4300 pages 13.8 and 14.2.  Up to kFewSeqs sequences take little LDS (with that of more, the 96 take 6.1 and 5.4).
 constexpr int kFewSeqs = 1024;
@@ -72,7 +74,6 @@ __device__ inline uint32_t add_dpp_to(uint32_t v, uint32_t most) {
 template <int SEQS>
 struct PagesLds {
     uint32_t wave[3][kThreads / 64];
-    int last;
     uint32_t row[SEQS + 1], come[SEQS + 1], gone[SEQS + 1];   // before a sequence
     int had[SEQS];                                            // its pages
 };
@@ -285,17 +286,15 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
     }
     for (int b = at; b <= batch; b += threads) a.row_start[b] = (int)lds.row[b];
     // what others may still read
+    const int left = (int)min(top > come ? top - come : 0u, (uint32_t)a.pages), lacking = (int)(come > top ? come - top : 0u);
     if (gridDim.x > 1) {
-        __syncthreads();
-        if (tid == 0) {
-            __threadfence();
-            lds.last = atomicAdd(reinterpret_cast<uint32_t*>(a.pool + 2), 1u) == gridDim.x - 1;
+        if (at == 0) {
+            a.pool[1] = lacking;
+            a.pool[2] = left;
         }
-        __syncthreads();
-        if (!lds.last) return;
-    } else {
-        __syncthreads();
+        return;
     }
+    __syncthreads();
     for (int b0 = 0; b0 < batch; b0 += kAtOnce * kThreads) {
         int want[kAtOnce];
 #pragma unroll
@@ -311,8 +310,18 @@ __global__ __launch_bounds__(kThreads) void k_pages_assign(PagesArgs a) {
         }
     }
     if (tid == 0) {
-        a.pool[0] = (int)min(top > come ? top - come : 0u, (uint32_t)a.pages);
-        a.pool[1] = (int)(come > top ? come - top : 0u);
+        a.pool[0] = left;
+        a.pool[1] = lacking;
+        a.pool[2] = 0;
+    }
+}
+
+// What the workgroups of k_pages_assign read, and the pool's count, which the first of them left in word 2.
+__global__ __launch_bounds__(256) void k_pages_settle(PagesArgs a) {
+    const int b = blockIdx.x * 256 + threadIdx.x;
+    if (b < a.batch) a.len[b] = max(a.want[b], 0);
+    if (b == 0) {
+        a.pool[0] = a.pool[2];
         a.pool[2] = 0;
     }
 }
@@ -409,6 +418,7 @@ hipError_t launch_pages_assign(const PagesArgs& a, hipStream_t s) {
         const int64_t n = std::max<int64_t>(1, std::min<int64_t>(128, (rows + kThreads - 1) / kThreads));
         if (few) hipLaunchKernelGGL((k_pages_assign<kFewSeqs>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
         else hipLaunchKernelGGL((k_pages_assign<kSeqsAtOnce>), dim3((unsigned)n), dim3(kThreads), 0, s, a);
+        if (n > 1) hipLaunchKernelGGL(k_pages_settle, dim3((a.batch + 255) / 256), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(k_pages_assign_many, dim3(1), dim3(kThreads), 0, s, a);

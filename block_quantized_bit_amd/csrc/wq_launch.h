@@ -96,7 +96,7 @@ struct PagesArgs {
     int32_t* len;          // [batch]
     const int32_t* want;   // [batch]
     int32_t* table;        // [batch][table_ld]
-    int32_t* pool;         // free pages, pages lacking, two words of the kernel's own, the list: the next page to take last
+    int32_t* pool;         // free pages, pages lacking, two words of the kernels' own, the list: the next page to take last
     int32_t* row_start;    // [batch + 1]
     int32_t* pos;          // [rows], or null
     int64_t* slot;         // [rows], or null

@@ -419,8 +419,8 @@ wq_status wq_attn_tree(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads
                        uint16_t* y, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
 /* A pool's free pages: device int32 [4 + pages].  Word 0 is how many are free, word 1 how
- * many the last wq_pages_assign lacked, words 2 and 3 are the library's own (0 between
- * calls); then the list, the next page to be taken last.  What lies behind the list's end
+ * many the last wq_pages_assign lacked, words 2 and 3 are the library's own (a call goes by
+ * word 0 and the list alone, whatever words 1 to 3 hold); then the list, the next page to be taken last.  What lies behind the list's end
  * is anything.  wq_pages_init makes all pages free, page 0 the first to be taken; a caller
  * may also write such an array itself.  pages: 1 .. 2^31 - 1. */
 wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
@@ -439,7 +439,8 @@ wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
  *   rows      : rows of the batch, 0 ..: what pos and slot have room for, and the most that
  *               a row start says
  *   row_start : device int32 [batch + 1], out: the sequences that grow have
- *               want[b] - len[b] rows each, in order (as wq_seqs takes it), the others none
+ *               want[b] - len[b] rows each, in order (as wq_seqs takes it), the others none;
+ *               where `rows` cuts some off, the rows left are the sequence's last tokens
  *   pos       : device int32 [rows] or NULL, out: the token that a row is, in its sequence
  *   slot      : device int64 [rows] or NULL, out: page * (entry of the table) + the token's
  *               place in the page; -1 where it has no page.  Entries of pos and slot
