@@ -46,3 +46,50 @@ def test_a_pools_other_words_can_hold_anything(batch, rows, word):
         d.assign(want)
         d.pool[2:4] = 0
         d.check(h, out, f"call {step}")
+
+
+@pytest.mark.parametrize("maps", [False, True], ids=["no maps", "maps"])
+@pytest.mark.parametrize("holes", [[], [0], [4095, 4096, 8191], "some", "all"], ids=str)
+@pytest.mark.parametrize("batch,per", [(1, 9000), (3, 5000), (40, 300), (1200, 9)])
+def test_thousands_of_entries_given_back(batch, per, holes, maps):
+    """More than a workgroup looks at together, with entries among them that are no page, while other sequences take some of
+    them; then others take the rest."""
+    say("given back", batch, per, holes, maps)
+    page, pages, rows = 32, batch * per + 50, 40000 if maps else 0
+    h, d = Pages(page, pages, batch + 2, per), DevPages(page, pages, batch + 2, per, rows)
+    rng = np.random.default_rng(per)
+    full = np.array([per * page] * batch + [1, 0])
+    wants = [full, np.array([0 if b % 5 else 40 for b in range(batch)] + [per * page - 3, 20]),
+             np.array([int(x) for x in rng.integers(0, 2 * page * per, batch + 2)])]
+    for step, want in enumerate(wants):
+        if step == 1:
+            at = np.arange(batch * per)
+            at = at if holes == "all" else rng.permutation(at)[:batch * per // 3] if holes == "some" else np.array(holes, int)
+            table = d.table.cpu().numpy()
+            for k, i in enumerate(at):
+                table[i // per, i % per] = h.table[i // per][i % per] = (-1, pages, -2**31)[k % 3]
+            d.table.copy_(torch.from_numpy(table))
+        out = h.assign(want, rows)
+        d.assign(want, maps)
+        d.check(h, out if maps else (out[0], None, None), f"call {step}")
+
+
+def test_a_missing_page_does_not_cost_what_the_others_do():
+    """One entry that is no page among 30000 that are given back: their pages are still looked at once or twice each."""
+    took = []
+    for hole in (False, True, False, True):
+        d = DevPages(32, 30000, 1, 30000, 0)
+        d.assign([960000], maps=False)
+        if hole:
+            d.table[0, 7] = -1
+        d.want = _i32([0])
+        events = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        torch.cuda.synchronize()
+        events[0].record()
+        wq.wq_pages_assign(d.desc, 1, d.len, d.want, d.table, 30000, d.pool, 0, d.start)
+        events[1].record()
+        torch.cuda.synchronize()
+        assert d.pool[:2].tolist() == [30000 - hole, 0]
+        took.append(events[0].elapsed_time(events[1]))
+    say("us", [round(1000 * t, 1) for t in took])
+    assert min(took[1], took[3]) < 30 * min(took[0], took[2])      # (each one looked up from the start: some 2000 times)
