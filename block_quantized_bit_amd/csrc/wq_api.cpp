@@ -132,6 +132,12 @@ bool windows_overlap(const void* pa, int64_t lda, int64_t wa, const void* pb, in
     return false;
 }
 
+// Whether two arrays of 32-bit words (null: none) share a byte.
+bool words_overlap(const void* pa, int64_t na, const void* pb, int64_t nb) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(pa), b = reinterpret_cast<uintptr_t>(pb);
+    return pa && pb && (a < b ? b - a < (uintptr_t)na * 4 : a - b < (uintptr_t)nb * 4);
+}
+
 // NVFP4 activations: k a multiple of 16 and m*k <= 2^34 (chunk indices of 8 values fit 32 bits).
 bool act_shape_ok(int64_t m, int64_t k) {
     if (m < 0 || k <= 0 || k % 16 != 0 || k > (int64_t(1) << 24)) return false;
@@ -651,8 +657,12 @@ wq_status wq_cache_keep(const wq_cache_desc* d, const wq_seqs* s, const int32_t*
             if (caches[i] == caches[j]) return WQ_ERR_INVALID_ARG;   // its rows would be moved twice
         a.cache[i] = static_cast<uint8_t*>(caches[i]);
     }
-    if (want && (want == s->len || want == count || want == path)) return WQ_ERR_INVALID_ARG;   // (other workgroups still read them)
     if (a.s.batch == 0) return WQ_OK;
+    const int64_t batch = a.s.batch;   // (a sequence's other workgroups still read what the call takes when want is written)
+    if (words_overlap(want, batch, s->len, batch) || words_overlap(want, batch, s->row_start, batch + 1) ||
+        words_overlap(want, batch, s->table, batch * a.s.table_ld) || words_overlap(want, batch, path, batch * path_ld) ||
+        words_overlap(want, batch, count, batch))
+        return WQ_ERR_INVALID_ARG;
     a.path = path;
     a.path_ld = path_ld;
     a.count = count;

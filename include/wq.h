@@ -468,7 +468,9 @@ wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, c
  *   n_caches : 1 .. 64 (else WQ_ERR_UNSUPPORTED); batch * kv_heads * n_caches is below 2^24
  *              (else WQ_ERR_SHAPE)
  *   want     : device int32 [batch] or NULL, out: the tokens of each sequence that are then
- *              in place, its context and the kept rows: what wq_pages_assign takes next
+ *              in place, its context and the kept rows: what wq_pages_assign takes next.  It
+ *              must not share a byte with the call's other arrays (WQ_ERR_INVALID_ARG where
+ *              it does with path, count or those of s)
  * The places of rows that are not kept hold anything that was there before or was moved. */
 wq_status wq_cache_keep(const wq_cache_desc* d, const wq_seqs* s, const int32_t* path, int32_t path_ld, const int32_t* count,
                         void* const* caches, int32_t n_caches, int32_t* want, void* stream);

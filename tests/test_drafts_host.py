@@ -1,0 +1,22 @@
+"""Refusals of the calls of a step with drafts that need no GPU: arrays that share bytes; and what the schedules ask for."""
+import pytest
+
+from test_cache_host import FAKE, _desc, _seqs
+from test_parts_host import _keep
+
+
+@pytest.mark.parametrize("name", ["len", "row_start", "table", "path", "count"])
+def test_keep_writes_over_none_of_its_inputs(name):
+    """Every workgroup reads a sequence's lengths, starts, pages and path, when another may have written `want` already."""
+    at = dict(len=10 * FAKE, row_start=20 * FAKE, table=30 * FAKE, path=40 * FAKE, count=50 * FAKE)
+    ints = dict(len=4, row_start=5, table=4 * 10, path=4 * 4, count=4)
+
+    def call(want, **kw):
+        s = _seqs(rows=9, **{k: at[k] for k in ("len", "row_start", "table")}, **kw)
+        return _keep(s=s, path=at["path"], count=at["count"], want=want)
+
+    for first in (0, ints[name] - 1, -3):                   # want has 4 words: the array's first, its last, the one behind want's
+        assert call(at[name] + 4 * first) == 1, first
+
+    s = _seqs(rows=9, row_start=None, len=at["len"], table=None, table_ld=0)
+    assert _keep(s=s, path=at["path"], count=at["count"], want=at["len"] + 12) == 1
