@@ -629,9 +629,14 @@ wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, c
         return WQ_ERR_ALIGNMENT;
     if ((int64_t)table_ld * q.page > 0x7FFFFFFF) return WQ_ERR_SHAPE;
     if (batch == 0) return WQ_OK;
-    const void* const arrays[] = {len, want, table, pool, row_start, pos, slot};
-    for (const void* const* i = arrays; i != std::end(arrays); i++)   // (some are written while others are still read)
-        if (*i && std::find(std::begin(arrays), i, *i) != i) return WQ_ERR_INVALID_ARG;
+    const struct {
+        const void* at;
+        int64_t words;
+    } arrays[] = {{len, batch}, {want, batch}, {table, (int64_t)batch * table_ld}, {pool, 4 + q.pages}, {row_start, (int64_t)batch + 1},
+                  {pos, rows}, {slot, 2 * (int64_t)rows}};
+    for (const auto* i = arrays; i != std::end(arrays); i++)   // (some are written while others are still read)
+        for (const auto* j = arrays; j != i; j++)
+            if (i->at == j->at ? i->at != nullptr : words_overlap(i->at, i->words, j->at, j->words)) return WQ_ERR_INVALID_ARG;
     wq::PagesArgs a = {len, want, table, pool, row_start, pos, slot, batch, table_ld, q.page, (int)q.pages, rows, 0, 0};
     // with 2^(shift - 27) >= upp, times is off by less than upp / 2^shift of itself, and x of 27 bits makes less than 1 / upp of that
     for (a.shift = 27; (1 << (a.shift - 27)) < q.upp; a.shift++) {}

@@ -451,8 +451,8 @@ wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
  * depend on timing.  Where there are not enough, the last wanted ones' entries become -1
  * (their tokens are absent: see wq_seqs) and word 1 of the pool says how many; tokens past
  * table_ld pages are absent too.  Negative lengths count as 0; entries that are no page are
- * not given back.  No two of the arrays may overlap (WQ_ERR_INVALID_ARG where two start at
- * one place), and calls on one pool or table must not run at the same time. */
+ * not given back.  No two of the arrays may share a byte (WQ_ERR_INVALID_ARG), and calls on
+ * one pool or table must not run at the same time. */
 wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, const int32_t* want, int32_t* table,
                           int32_t table_ld, int32_t* pool, int32_t rows, int32_t* row_start, int32_t* pos, int64_t* slot,
                           void* stream);

@@ -2,7 +2,7 @@
 import pytest
 
 from test_cache_host import FAKE, _desc, _seqs
-from test_parts_host import _keep
+from test_parts_host import _keep, _pages
 
 
 @pytest.mark.parametrize("name", ["len", "row_start", "table", "path", "count"])
@@ -20,3 +20,15 @@ def test_keep_writes_over_none_of_its_inputs(name):
 
     s = _seqs(rows=9, row_start=None, len=at["len"], table=None, table_ld=0)
     assert _keep(s=s, path=at["path"], count=at["count"], want=at["len"] + 12) == 1
+
+
+def test_page_arrays_share_no_byte():
+    """Each of a call's arrays, moved to the last bytes of each other one, or so that its own last bytes are the other's first."""
+    words = dict(len=4, want=4, table=40, pool=104, start=5, pos=9, slot=18)     # batch 4, 10 entries each, 100 pages, 9 rows
+    apart = {k: FAKE * (i + 1) for i, k in enumerate(words)}
+    for a in words:
+        for b in words:
+            if a != b:
+                step = 2 if a == "slot" else 1                                   # (aligned to its entries)
+                for at in (4 * ((words[b] - 1) // step * step), -4 * ((words[a] - 1) // step * step)):
+                    assert _pages(**{**apart, a: apart[b] + at}) == 1, (a, b, at)
