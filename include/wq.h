@@ -378,7 +378,10 @@ wq_status wq_attn(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, con
  *   wq_cache_write    the drafts' keys and values
  *   wq_attn_tree      (or wq_attn_sinks, wq_attn)
  *   wq_cache_keep     the accepted rows moved into place, in every layer's cache
- *   wq_pages_assign   back to the accepted length (the next step's first call does it too) */
+ *   wq_pages_assign   back to the accepted length: what wq_cache_keep wrote to `want`, rows 0
+ * The last call belongs to every step, before the next one's first: the rows of a call are what
+ * its lengths grow by, so from a length that counts dropped rows the next draft would get too
+ * few rows, behind tokens of the old draft. */
 
 /* Host-only.  Workspace bytes wq_attn_sinks can use for such a call, as
  * wq_attn_workspace_size; window and sinks as for the call. */
@@ -420,8 +423,8 @@ wq_status wq_attn_tree(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads
 
 /* A pool's free pages: device int32 [4 + pages].  Word 0 is how many are free, word 1 how
  * many the last wq_pages_assign lacked, words 2 and 3 are the library's own (a call goes by
- * word 0 and the list alone, whatever words 1 to 3 hold); then the list, the next page to be taken last.  What lies behind the list's end
- * is anything.  wq_pages_init makes all pages free, page 0 the first to be taken; a caller
+ * word 0 and the list alone, whatever words 1 to 3 hold); then the list, the next page to be
+ * taken last.  What lies behind the list's end is anything.  wq_pages_init makes all pages free, page 0 the first to be taken; a caller
  * may also write such an array itself.  pages: 1 .. 2^31 - 1. */
 wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
 

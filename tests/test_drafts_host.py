@@ -1,7 +1,10 @@
 """Refusals of the calls of a step with drafts that need no GPU: arrays that share bytes; and what the schedules ask for."""
 import pytest
 
-from test_cache_host import FAKE, _desc, _seqs
+from block_quantized_bit_amd import build
+
+from parts_helpers import HostPages
+from test_cache_host import FAKE, _seqs
 from test_parts_host import _keep, _pages
 
 
@@ -32,3 +35,23 @@ def test_page_arrays_share_no_byte():
                 step = 2 if a == "slot" else 1                                   # (aligned to its entries)
                 for at in (4 * ((words[b] - 1) // step * step), -4 * ((words[a] - 1) // step * step)):
                     assert _pages(**{**apart, a: apart[b] + at}) == 1, (a, b, at)
+
+
+def test_a_step_ends_with_the_accepted_length():
+    """The header's step: a draft's rows are what the lengths grow by, so the call back to the accepted length cannot be left
+    to the next step's first call."""
+    def draft(closed):
+        h = HostPages(32, 20, 1, 10)
+        h.assign([100], 200)
+        h.assign([113], 200)                                # 13 drafted tokens, of which 5 are kept
+        if closed:
+            h.assign([105], 0)
+        return h.assign([118], 200)[1]                      # 13 more
+
+    assert draft(True) == list(range(105, 118)) and draft(False) == list(range(113, 118))
+    header = open(build.ROOT + "/include/wq.h").read()
+    at = header.index("A step of serving with drafted tokens")
+    step = header[at:header.index("*/", at)]
+    calls = [x.split()[1] for x in step.splitlines() if x.startswith(" *   wq_")]
+    assert calls == ["wq_pages_assign", "wq_cache_write", "wq_attn_tree", "wq_cache_keep", "wq_pages_assign"]
+    assert "does it too" not in step and "belongs to every step" in step

@@ -5,9 +5,11 @@ import pytest
 import torch
 
 from block_quantized_bit_amd import wq
+from block_quantized_bit_amd.inputs import bf16_bits_to_f32, f32_to_bf16_bits
 
-from gpu_helpers import DEV, require_gpu, say
-from parts_helpers import HostPages
+from cache_helpers import Q4_0, Q4_1, check_attn
+from gpu_helpers import DEV, dev_bf16, require_gpu, say
+from parts_helpers import HostPages, attend_seen, dev_words, sees_tree, trees, words
 from test_gpu_pages import DevPages, _i32
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +95,93 @@ def test_a_missing_page_does_not_cost_what_the_others_do():
         took.append(events[0].elapsed_time(events[1]))
     say("us", [round(1000 * t, 1) for t in took])
     assert min(took[1], took[3]) < 30 * min(took[0], took[2])      # (each one looked up from the start: some 2000 times)
+
+
+@pytest.mark.parametrize("fmt,dim,heads,group,page", [(Q4_0, 128, 2, 4, 64), (Q4_1, 64, 3, 1, 32)], ids=["q4_0", "q4_1"])
+def test_a_captured_step_with_its_last_call(orc, fmt, dim, heads, group, page):
+    """The header's step, whole, as one graph: what wq_cache_keep wrote is what the lengths go back to and the next replay starts
+    from, with nothing made on the host but the drafts."""
+    batch, most, per, pages, ld = 4, 14, 8, 40, 5
+    width, hq = heads * dim, heads * group
+    rng = np.random.default_rng(dim)
+    desc = wq.cache_desc(fmt, dim, heads, page, pages)
+    caches = [torch.from_numpy(rng.integers(0, 256, wq.wq_cache_size(desc), dtype=np.uint8)).to(DEV) for _ in range(2)]
+    zeros = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)  # noqa: E731
+    pool, length, grow, want, kept, table = zeros(4 + pages), zeros(batch), zeros(batch), zeros(batch), zeros(batch), zeros(batch, per)
+    wq.wq_pages_init(pages, pool)
+    rows = batch * most
+    start, after, pos, slot = zeros(batch + 1), zeros(batch + 1), zeros(rows), torch.zeros(rows, dtype=torch.int64, device=DEV)
+    path, count, tree = zeros(batch, ld), zeros(batch), zeros(rows, 1)
+    seqs = wq.seqs(batch, rows, length, table, start)
+    K, V, Q = (torch.zeros((rows, w), dtype=torch.int16, device=DEV) for w in (width, width, hq * dim))
+    Y = torch.zeros_like(Q)
+    n = wq.wq_attn_tree_workspace_size(desc, seqs, hq, 0, 0)
+    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+    scale = dim ** -0.5
+
+    def step():
+        torch.add(length, grow, out=want)
+        wq.wq_pages_assign(desc, batch, length, want, table, per, pool, rows, start, pos, slot)
+        for cache in caches:
+            wq.wq_cache_write(desc, seqs, K, width, V, width, wq.WQ_BF16, cache)
+        wq.wq_attn_tree(desc, seqs, hq, Q, hq * dim, caches[1], scale, 0, 0, tree, 1, Y, hq * dim, ws, n)
+        wq.wq_cache_keep(desc, seqs, path, ld, count, caches, kept)
+        wq.wq_pages_assign(desc, batch, length, kept, table, per, pool, 0, after)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step()                                                # (nothing grows: no rows)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    host_k, host_v = ([np.zeros((0, heads, dim), np.uint16) for _ in range(batch)] for _ in range(2))
+    for t in range(8):
+        counts = rng.integers(1, most + 1, batch)
+        if t % 3 == 1:
+            counts[rng.integers(0, batch)] = 0
+        at = np.concatenate([[0], np.cumsum(counts)])
+        m = int(at[-1])
+        masks = trees(rng, counts, "tree")
+        tree[:m] = dev_words(words(masks, 1, m))
+        kb, vb, qb = (f32_to_bf16_bits(rng.standard_normal((rows, w), dtype=np.float32)) for w in (width, width, hq * dim))
+        for x, y in ((K, kb), (V, vb), (Q, qb)):
+            x.copy_(dev_bf16(y))
+        paths = [np.flatnonzero(x[int(rng.integers(0, a))])[:ld] if a else np.zeros(0, int) for a, x in zip(counts, masks)]
+        p = np.full((batch, ld), -1, np.int32)
+        for b, x in enumerate(paths):
+            p[b, :len(x)] = x
+        path.copy_(torch.from_numpy(p).to(DEV))
+        count.copy_(_i32([len(x) for x in paths]))
+        grow.copy_(_i32(counts))
+        Y.fill_(0x7BAD)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert start.cpu().tolist() == at.tolist() and after.cpu().tolist() == [0] * (batch + 1), t
+        place = [(b, len(host_k[b]) + j) for b in range(batch) for j in range(counts[b])]
+        assert pos.cpu().tolist()[:m] == [x for _, x in place], t
+
+        class Now:
+            pass
+
+        now = Now()
+        now.fmt, now.dim, now.heads, now.batch, now.rows = fmt, dim, heads, batch, rows
+        now.lens, now.counts, now.start = [len(x) + int(a) for x, a in zip(host_k, counts)], [int(x) for x in counts], at
+        now.present = lambda b: np.ones(now.lens[b], bool)  # noqa: B023
+        full = [[np.concatenate([x[b], y.reshape(rows, heads, dim)[at[b]:at[b + 1]]]) for b in range(batch)]
+                for x, y in ((host_k, kb), (host_v, vb))]
+        ref, ab, A = attend_seen(now, orc, full[0], full[1], bf16_bits_to_f32(qb).reshape(rows, hq, dim), group, scale,
+                                 sees_tree(now, masks, 1, 0, 0))
+        y = Y.cpu().numpy().view(np.uint16)
+        check_attn(bf16_bits_to_f32(y).reshape(rows, hq, dim)[:m], ref[:m], ab[:m], A[:m], f"step {t}")
+        assert np.all(y[m:] == 0x7BAD)
+        for b in range(batch):
+            pick = at[b] + paths[b]
+            host_k[b] = np.concatenate([host_k[b], kb.reshape(rows, heads, dim)[pick]])
+            host_v[b] = np.concatenate([host_v[b], vb.reshape(rows, heads, dim)[pick]])
+        lens = [len(x) for x in host_k]
+        assert kept.cpu().tolist() == lens and length.cpu().tolist() == lens, t
+        held = [int(x) for b in range(batch) for x in table[b, :-(-lens[b] // page)].cpu()]
+        free = pool[4:4 + int(pool[0])].cpu().tolist()
+        assert sorted(held + free) == list(range(pages)) and pool[1].item() == 0, t
