@@ -452,8 +452,12 @@ wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
  * and their pages, then the wanted ones are taken from its front in the same order; so what a
  * call has taken, a call that takes it back puts where it was, and the result does not
  * depend on timing.  Where there are not enough, the last wanted ones' entries become -1
- * (their tokens are absent: see wq_seqs) and word 1 of the pool says how many; tokens past
- * table_ld pages are absent too.  Negative lengths count as 0; entries that are no page are
+ * (their tokens are absent: see wq_seqs) and word 1 of the pool says how many this call left
+ * so.  They stay -1 as long as the sequence does not shrink below them, and later calls do
+ * not count them again: a page that came later would hold none of the tokens that were
+ * written meanwhile.  So where word 1 is not 0, give the call back (want: the lengths before
+ * it), or end a sequence, and grow again when pages are free.  Tokens past table_ld pages
+ * are absent too.  Negative lengths count as 0; entries that are no page are
  * not given back.  No two of the arrays may share a byte (WQ_ERR_INVALID_ARG), and calls on
  * one pool or table must not run at the same time. */
 wq_status wq_pages_assign(const wq_cache_desc* d, int32_t batch, int32_t* len, const int32_t* want, int32_t* table,

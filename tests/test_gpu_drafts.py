@@ -185,3 +185,36 @@ def test_a_captured_step_with_its_last_call(orc, fmt, dim, heads, group, page):
         held = [int(x) for b in range(batch) for x in table[b, :-(-lens[b] // page)].cpu()]
         free = pool[4:4 + int(pool[0])].cpu().tolist()
         assert sorted(held + free) == list(range(pages)) and pool[1].item() == 0, t
+
+
+@pytest.mark.parametrize("others", [0, 9000])
+def test_pages_that_were_lacking(others):
+    """Entries that got no page stay without one while their sequence goes on, and get one when it has shrunk and grows again."""
+    page, per = 32, 8
+    h, d = Pages(page, 4 + others, 2 + others, per), DevPages(page, 4 + others, 2 + others, per, 200 + others)
+
+    def call(a, b):
+        want = np.array([a, b] + [1] * others)
+        out = h.assign(want, 200 + others)
+        d.assign(want)
+        d.check(h, out, f"{a} and {b}")
+        slot = d.slot.cpu().tolist()[out[0][1]:out[0][2]]          # of the second sequence's rows
+        return d.pool[1].item(), d.table[1].cpu().tolist()[:-(-b // page)], slot
+
+    def first():                                              # the others take theirs
+        want = np.array([0, 0] + [1] * others)
+        out = h.assign(want, 200 + others)
+        d.assign(want)
+        d.check(h, out, "the others")
+
+    first()
+    lacking, table, slot = call(64, 96)
+    assert lacking == 1 and table[2] == -1 and slot[64:] == [-1] * 32 and -1 not in slot[:64]
+    lacking, table, slot = call(0, 96)                        # two pages are free again
+    assert lacking == 0 and table[2] == -1 and d.pool[0].item() == 2
+    lacking, table, slot = call(0, 97)                        # a page for the token that is new, none for the hole
+    assert lacking == 0 and table[2] == -1 and table[3] >= 0 and len(slot) == 1 and slot[0] >= 0
+    lacking, table, slot = call(0, 64)                        # back to before, and on: all are there
+    assert lacking == 0 and d.pool[0].item() == 2
+    lacking, table, slot = call(0, 97)
+    assert lacking == 0 and min(table) >= 0 and len(slot) == 33 and min(slot) >= 0
