@@ -432,7 +432,8 @@ wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
  * that its table has ceil(want[b] / page) of them, and len[b] becomes want[b].  One call
  * serves sequences that grow, shrink and end (want 0) alike.
  *   d         : of the cache(s); its page and pages are what counts
- *   batch     : sequences, 0 .. 2^20
+ *   batch     : sequences, 1 .. 2^20 (0: the call does nothing, and row_start[0] and the pool's
+ *               words stay as they were)
  *   len       : device int32 [batch], in and out
  *   want      : device int32 [batch], an array of its own
  *   table     : device int32 [batch][table_ld], in and out; the entries of pages that a

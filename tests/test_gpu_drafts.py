@@ -218,3 +218,13 @@ def test_pages_that_were_lacking(others):
     assert lacking == 0 and d.pool[0].item() == 2
     lacking, table, slot = call(0, 97)
     assert lacking == 0 and min(table) >= 0 and len(slot) == 33 and min(slot) >= 0
+
+
+def test_no_sequences_is_no_call():
+    """With a batch of 0 nothing is written: neither row starts nor counts."""
+    d = DevPages(32, 10, 3, 4, 50)
+    d.assign([40, 0, 7])
+    before = [x.clone() for x in (d.pool, d.len, d.table, d.start, d.pos, d.slot)]
+    wq.wq_pages_assign(d.desc, 0, d.len, d.want, d.table, 4, d.pool, 50, d.start, d.pos, d.slot)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(before, (d.pool, d.len, d.table, d.start, d.pos, d.slot)))
