@@ -11,9 +11,13 @@
 //
 // Rounded to fp16, because the matrix instructions take 16-bit operands and fp16 has three bits more than bf16: probabilities
 // (2^(x - ref), at most 2^15; the sum that divides is of the unrounded ones), values, queries (times a power of two per row and
-// head, mostly exact), and keys, but for q4_0 in calls with few rows, whose codes are exact there.  Each is off by half a step,
-// 2^-11 of itself.  In calls with ordinary scores the outputs' error is that of their own rounding to bf16 (0.0017 of their
-// magnitude against 64 bits, as for the same computed in fp32).
+// head, mostly exact), and keys, but for q4_0 in tiles of 16 columns, whose codes are multiplied as they are.  (Wider tiles are
+// taken by wq_attn for more than 128 columns per sequence on average, by drafts and rows with sinks for more than 16 where
+// draft_schedule says so.)  Each is off by half a step at most, 2^-11 of itself.  q4_0's values and keys are fp16 numbers all the
+// same where their rows were written as bf16: a block's scale has 8 bits then, and a code less 8 three more at most.  q4_1's scale
+// and offset have all of fp16's bits, so that its values and keys are rounded.
+// The outputs, in calls with ordinary scores, are off against 64 bits (2-norm, bf16, rows written as bf16) by 0.00164 to 0.00169 of
+// their magnitude in q4_0 and by 0.00172 to 0.00174 in q4_1; the same in fp32, rounded to bf16, by 0.00164 to 0.00168.
 #pragma once
 
 #include <hip/hip_runtime.h>

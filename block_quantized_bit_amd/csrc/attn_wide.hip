@@ -7,8 +7,12 @@
 // go through LDS, and no wave waits for another before the end.
 //
 // Bound by the vector unit and the matrix unit, which take turns more than they overlap: 32 sequences of 300 to 8191 tokens with
-// 8 drafted rows each, 8 x 4 heads of 128, q4_0: 78 us, tiles of 16 columns 94.  Four tiles (64 columns) leave one wave per SIMD and
+// 8 drafted rows each, 8 x 4 heads of 128, q4_0: 71 us, tiles of 16 columns 94.  Four tiles (64 columns) leave one wave per SIMD and
 // were slower wherever tiles of 128 columns were not the better choice anyway.
+// Keys are made fp16 in both formats.  q4_0's codes as they are, each block's products scaled in fp32 (as k_attn_token has it),
+// need a product of their own per block and tile and 16 multiplications more, and registers for both: 71 -> 83 us for those 32
+// sequences (67 registers spilled), 62 -> 64 with heads of 96, 49 -> 54 with 64, and 81 -> 112 with the 16 sequences below (159
+// spilled), with the same error to four digits.
 // Heads of 256 have one wave per SIMD, which nothing hides the reads of LDS for: issued early (below) they take 16 sequences' 25 rows
 // over 4096 tokens and 4 first ones, 2 x 8 heads, q4_1, from 97 to 87 us.  A ring of three units there gained nothing.
 #include "attn_kernel.h"

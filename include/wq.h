@@ -392,9 +392,11 @@ wq_status wq_attn_sinks_workspace_size(const wq_cache_desc* d, const wq_seqs* s,
  * the tokens t <= p with t > p - window or t < sinks.
  *   window : 1 .., tokens of the sliding window (the row's own among them)
  *   sinks  : 0 .., first tokens of a sequence that every row at or behind them sees
- * All else (arguments, refusals, rounding and error bound) as for wq_attn, but that a tile may
- * have 32 pairs too; the call has fewer than 2^23 tiles.  Tokens between the sinks and the
- * window are not read. */
+ * All else (arguments, refusals, rounding and error bound) as for wq_attn, but that calls with
+ * more than 16 pairs of a row and a query head per sequence may have tiles of 32, 128 or 256
+ * pairs, and round q4_0's keys to fp16 as wq_attn does in calls with many rows (a key of
+ * ordinary size whose row was written as bf16 is one already); the call has fewer than 2^23
+ * tiles.  Tokens between the sinks and the window are not read. */
 wq_status wq_attn_sinks(const wq_cache_desc* d, const wq_seqs* s, int32_t q_heads, const uint16_t* q, int64_t ldq,
                         const void* cache, float scale, int32_t window, int32_t sinks, uint16_t* y, int64_t ldy, void* ws,
                         size_t ws_bytes, void* stream);

@@ -1,8 +1,12 @@
-"""Refusals of the calls of a step with drafts that need no GPU: arrays that share bytes; and what the schedules ask for."""
+"""Of the calls of a step with drafts, what needs no GPU: refusals of arrays that share bytes, the step's rule, what fp16 holds of
+the cache's values."""
+import numpy as np
 import pytest
 
 from block_quantized_bit_amd import build
+from block_quantized_bit_amd.inputs import bf16_bits_to_f32, f32_to_bf16_bits
 
+from cache_helpers import Q4_0, stored
 from parts_helpers import HostPages
 from test_cache_host import FAKE, _seqs
 from test_parts_host import _keep, _pages
@@ -55,3 +59,12 @@ def test_a_step_ends_with_the_accepted_length():
     calls = [x.split()[1] for x in step.splitlines() if x.startswith(" *   wq_")]
     assert calls == ["wq_pages_assign", "wq_cache_write", "wq_attn_tree", "wq_cache_keep", "wq_pages_assign"]
     assert "does it too" not in step and "belongs to every step" in step
+
+
+def test_q4_0_of_bf16_rows_is_exact_in_fp16(orc):
+    """A scale of 8 bits times a code less 8: what the kernels hold as fp16 is then the value itself."""
+    rng = np.random.default_rng(1)
+    for std in (2.0 ** -6, 1.0, 300.0):
+        x = bf16_bits_to_f32(f32_to_bf16_bits((rng.standard_normal((200, 256)) * std).astype(np.float32)))
+        y = stored(orc, Q4_0, x)
+        assert np.array_equal(y.astype(np.float16).astype(np.float32), y)

@@ -7,9 +7,9 @@ import torch
 from block_quantized_bit_amd import wq
 from block_quantized_bit_amd.inputs import bf16_bits_to_f32, f32_to_bf16_bits
 
-from cache_helpers import Q4_0, Q4_1, check_attn
+from cache_helpers import Q4_0, Q4_1, Case, check_attn, stored
 from gpu_helpers import DEV, dev_bf16, require_gpu, say
-from parts_helpers import HostPages, attend_seen, dev_words, sees_tree, trees, words
+from parts_helpers import HostPages, attend_seen, dev_words, run_seen, sees_sinks, sees_tree, trees, words
 from test_gpu_pages import DevPages, _i32
 
 pytestmark = pytest.mark.gpu
@@ -228,3 +228,87 @@ def test_no_sequences_is_no_call():
     wq.wq_pages_assign(d.desc, 0, d.len, d.want, d.table, 4, d.pool, 50, d.start, d.pos, d.slot)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(before, (d.pool, d.len, d.table, d.start, d.pos, d.slot)))
+
+
+# rows and tokens of the sequences, heads, group: single tokens, and drafts whose tiles have 16, 32, 128 and 256 columns, whole and
+# (over 3001 tokens) shared out
+WIDTHS = {"token": ([1, 1], [70, 33], 2, 4), "16": ([3, 70], [80, 300], 1, 4), "32": ([12] * 40, [70] * 40, 8, 4),
+          "128": ([32] * 8, [150] * 8, 16, 4), "256": ([128] * 8, [140] * 8, 16, 2), "token shared": ([1], [3001], 1, 4),
+          "32 shared": ([10, 3], [3001, 70], 1, 4), "128 shared": ([30], [3001], 1, 4), "256 shared": ([70], [3001], 1, 4)}
+WIDTH = pytest.mark.parametrize("width", WIDTHS)
+
+
+def _scores(orc, fmt, dim, width, k_of, q_of, scale, tol, what):
+    """wq_attn_sinks and wq_attn_tree of one case within `tol`(A, Q) sum (p + 2^-23) |v^| and the output's own rounding, values 1
+    and 0 by turns, so that a wrong probability shows."""
+    counts, lens, heads, group = WIDTHS[width]
+    c = Case(fmt, dim, heads, 64, counts, lens, seed=dim)
+    k = [k_of(c, t) for t in lens]
+    v = [np.zeros((t, heads, dim), np.float32) for t in lens]
+    for x in v:
+        x[::2] = 1.0
+    v = [f32_to_bf16_bits(x) for x in v]
+    c.fill(k, v)
+    q = f32_to_bf16_bits(q_of(c, (c.rows, heads * group, dim)))
+    qf = bf16_bits_to_f32(q)
+    masks = trees(c.rng, counts, "tree")
+    ld = -(-max(counts) // 32)
+    most = max(np.abs(stored(orc, fmt, bf16_bits_to_f32(x)).astype(np.float64)).sum(-1).max() for x in k)
+    Q = abs(scale) * np.abs(qf.astype(np.float64)).max(-1)[..., None] * most
+    for window, sinks, tree in ((max(lens), 0, None), (50, 20, None), (0, 0, masks), (100, 7, masks)):
+        sees = sees_sinks(c, window, sinks) if tree is None else sees_tree(c, masks, ld, window, sinks)
+        ref, ab, A = attend_seen(c, orc, k, v, qf, group, scale, sees)
+        bound = tol(A, Q) * ab + 2.0 ** -8 * np.abs(ref) + 1e-30
+        for ws in ("asked", None):
+            y = run_seen(c, q, group, scale, window, sinks, None if tree is None else dev_words(words(masks, ld, c.rows)), ws=ws)[0]
+            err = np.abs(y.astype(np.float64) - ref)
+            bad = ~(err <= bound)
+            assert not bad.any(), f"{what} {width} {window} {sinks} ws={ws}: {bad.sum()} of {bad.size} outside, {np.nanmax(err / bound):.3g} of the bound"
+
+
+@WIDTH
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+def test_q4_0_keys_of_bf16_rows_are_exact(orc, dim, width):
+    """|y - ref| <= (2^-9 + 2^-14 A) sum (p + 2^-23) |v^| + 2^-8 |ref|, a 32nd of what the scores may be off in general.
+
+    A block's scale is a bf16 number over -8, of 8 bits, and a code less 8 has 3 (8 itself is a power of two): their products have
+    11, and are fp16 numbers whether the kernel multiplies codes or values.  Queries of these sizes are exact too, and so is a product of
+    the two in fp32.  What is left of a score's error is the fp32 sum of at most 256 of them, 2^-24 of the sum of their magnitudes
+    each and as much again for the order that the matrix unit has: 2^-15 A, and a probability twice that."""
+    say("exact keys", dim, width)
+    _scores(orc, Q4_0, dim, width, lambda c, t: f32_to_bf16_bits(c.rng.standard_normal((t, c.heads, dim), dtype=np.float32) + 0.3),
+            lambda c, n: c.rng.standard_normal(n, dtype=np.float32), 24 * dim ** -0.5, lambda A, Q: 2.0 ** -9 + 2.0 ** -14 * A, "exact keys")
+
+
+def _general(A, Q):
+    """The header's bound: half steps of fp16 (2^-11) of probabilities, values, and keys and queries in a score, and what small
+    queries beside a large one lose."""
+    return 2.0 ** -9 + 2.0 ** -9 * A + 2.0 ** -38 * Q
+
+
+@WIDTH
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("outlier", [30.0, -30000.0])
+def test_outlier_keys_of_drafts(orc, fmt, outlier, width):
+    """Each block of a key has one large channel, where the query is zero: every true score is 0, and all tokens count alike."""
+    def keys(c, t):
+        k = np.zeros((t, c.heads, 64), np.float32)
+        k[::2, :, 5::32], k[1::4, :, 5::32] = outlier, -outlier
+        return f32_to_bf16_bits(k)
+
+    def queries(c, n):
+        q = c.rng.standard_normal(n, dtype=np.float32) * np.exp2(c.rng.integers(-10, 10, n)).astype(np.float32)
+        q[..., 5::32] = 0.0
+        return q
+
+    say("outlier", fmt, outlier, width)
+    _scores(orc, fmt, 64, width, keys, queries, 0.125, _general, f"outlier {outlier}")
+
+
+@WIDTH
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("qs,scale", [(2.0 ** 122, 2.0 ** -124), (2.0 ** -122, 2.0 ** 119), (2.0 ** -129, 2.0 ** 126)], ids=["largest", "small", "subnormal"])
+def test_drafts_queries_of_any_magnitude(orc, fmt, qs, scale, width):
+    say("magnitude", fmt, qs, width)
+    _scores(orc, fmt, 128, width, lambda c, t: f32_to_bf16_bits(c.rng.standard_normal((t, c.heads, 128), dtype=np.float32)),
+            lambda c, n: (c.rng.standard_normal(n) * qs).astype(np.float32), scale, _general, f"queries of {qs}")
