@@ -279,31 +279,44 @@ int64_t seen_units(const AttnArgs& a, int64_t most) {
     return std::min(most, ((int64_t)a.sinks + kUnit - 1) / kUnit + (a.window + rows + kUnit - 1) / kUnit + 1);
 }
 
-// Drafts: `cols` columns per sequence on average, more than 16.  Measured in us, 8 x 4 heads of 128, q4_0, contexts of one length
-// (whole) or of 300 to so many tokens (shared out):
-//   tiles of                    16     32    128    256
-//   whole     4 x 128,  1500    22     38     64
-//            32 x  80,  1500    72     59     68
-//            32 x 128,   500    57     51     37
-//            32 x 256,  1500   214    148    103
-//            16 x 508,  3000   350    232    184    156
-//   shared   32 x  32,  8191    94     78    117    168
-//   out       8 x  64, 30000   150    123    121    161
-//            32 x 128,  8191   300    240    157    204
-//             8 x 256, 30000   507    399    264    237
+// Drafts: `cols` columns per sequence on average, more than 16.  Measured in us, q4_0, 8 x 4 heads of 128 / of 96 / of 64, contexts of
+// one length (whole) or of 300 to so many tokens (shared out, over 256 workgroups for tiles of 256, else 512):
+//   tiles of                          16           32          128          256
+//   whole     4 x 128,  1500     21/ 18/ 16   31/ 26/ 21   58/ 52/ 40   48/ 44/ 40
+//            32 x  80,  1500     68/ 51/ 39   54/ 48/ 37   62/ 58/ 41   52/ 48/ 42
+//            32 x 128,   500     55/ 39/ 29   43/ 37/ 31   33/ 28/ 23   30/ 27/ 24
+//            32 x 200,  1000    121/ 88/ 64   89/ 77/ 61   68/ 57/ 46   57/ 50/ 42
+//            64 x 28 to 320, 300 to 1000
+//                               156/111/ 83  118/101/ 80  100/ 88/ 69  113/101/ 87
+//            32 x 256,  1500    204/140/105  132/112/ 89   92/ 79/ 63   84/ 72/ 58
+//            16 x 512,  3000    345/237/178  206/174/135  152/134/106  135/117/ 98
+//   shared   32 x  32,  8191     95/ 78/ 64   73/ 63/ 51   95/ 91/ 67  121/120/104
+//   out       8 x  64, 30000    147/123/ 96  109/ 97/ 75  105/100/ 74  120/117/ 99
+//            32 x 128,  8191    286/244/189  209/186/145  143/122/ 94  155/138/122
+//            32 x 28 to 256, 8191
+//                               323/275/216  232/200/156  181/159/123  179/158/136
+//            32 x 200,  8191    358/305/236  272/240/187  211/182/147  184/159/137   (120 to 200)
+//             8 x 256, 30000    488/417/327  343/308/237  214/183/143  188/154/130
 // Wider tiles share conversions, but take more registers and longer to begin: they pay where there are enough of them for the
-// chip, or they are shared out.  Sharing out costs some 15 us (finding the work, and the join), as for single tokens.
+// chip, or they are shared out.  Sharing out costs some 15 us (finding the work, and the join), as for single tokens.  Between 129
+// and 255 columns equal drafts would gain up to a fifth by tiles of 256, and unequal ones, that the average says nothing of, lose up to a
+// fifth: those of 128 are taken.
 // Heads of 256 leave tiles of 32 columns one wave per SIMD, and those of 128 one workgroup per compute unit.  2 x 8 heads, q4_1
-// (=: all of that length):
+// (=: all of that length), shared out over 512 workgroups for tiles of 16, else 256:
 //   tiles of                    16     32    128
-//   whole    16 x 200,  4000   107     86    281
-//            32 x 200,  1000    67     69     91
-//            64 x 512,   500   174    207    133
-//   shared   16 x  96, =12000  131    109    129
-//   out      16 x 200, =12000  276    209    238
-//            16 x 200, 20000   251    245    217
-//            16 x 512,  8191   276    285    216
-//             4 x 512, =8000   123     92    120
+//   whole    16 x 200,  4000   103     81    280
+//            32 x 200,  1000    67     70     91
+//            64 x 512,   500   164    196    126
+//   shared   16 x  96, =12000  130    108    128
+//   out      16 x 200, =12000  257    200    236
+//            16 x 200,  12000  154    177    151
+//            16 x 200,  20000  237    243    215
+//            16 x 512,   8191  252    273    204
+//             8 x 200, =12000  140    118    138
+//             8 x 200,  30000  197    227    182
+//             4 x 512,  =8000  113     90    118
+// Shared out, contexts of one length are faster in tiles of 32, unequal ones in tiles of 128, and the table's width, which is all that the
+// host knows, does not say which there are: with 64 tiles or more it goes by unequal ones, with fewer by equal ones.
 void draft_schedule(const AttnArgs& a, bool share, int64_t most, int64_t units, int64_t cols, Schedule* s) {
     const auto items = [&](int c) { return tile_bound(tile_shape(c, a.group), a.s.rows, a.s.batch, false) * a.s.heads; };
     const auto take = [&](int c, int workgroups) {
