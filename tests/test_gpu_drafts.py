@@ -10,7 +10,7 @@ from block_quantized_bit_amd.inputs import bf16_bits_to_f32, f32_to_bf16_bits
 from cache_helpers import Q4_0, Q4_1, Case, check_attn, stored
 from gpu_helpers import DEV, dev_bf16, require_gpu, say
 from parts_helpers import HostPages, attend_seen, dev_words, run_seen, sees_sinks, sees_tree, trees, words
-from test_gpu_pages import DevPages, _i32
+from test_gpu_pages import KEEP, DevPages, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -312,3 +312,139 @@ def test_drafts_queries_of_any_magnitude(orc, fmt, qs, scale, width):
     say("magnitude", fmt, qs, width)
     _scores(orc, fmt, 128, width, lambda c, t: f32_to_bf16_bits(c.rng.standard_normal((t, c.heads, 128), dtype=np.float32)),
             lambda c, n: (c.rng.standard_normal(n) * qs).astype(np.float32), scale, _general, f"queries of {qs}")
+
+
+@pytest.mark.parametrize("batch,rows", [(20, 20000), (300, 90000), (9001, 90000)])
+def test_taking_back_puts_the_pages_where_they_were(batch, rows):
+    """After a call that takes and one that takes it back the list is the one from before, entry by entry, and so are the lengths
+    and the tables' live entries."""
+    d = DevPages(64, 30 * batch, batch, 30, rows)
+    rng = np.random.default_rng(3)
+    at = rng.integers(0, 9 if batch > 1000 else 250, batch)
+    d.assign(at)
+    d.assign(rng.permutation(at))
+    at = d.len.cpu().numpy()
+    for grow in (1, 7, 200):
+        torch.cuda.synchronize()
+        n = int(d.pool[0])
+        pool, table = d.pool[4:4 + n].clone(), d.table.clone()
+        more = at + np.minimum(rng.integers(0, grow + 1, batch), rows // batch)
+        d.assign(more)
+        torch.cuda.synchronize()
+        assert int(d.pool[0]) == n - int((-(-more // 64) - -(-at // 64)).sum()) and d.pool[1].item() == 0
+        d.assign(at)
+        torch.cuda.synchronize()
+        assert int(d.pool[0]) == n and torch.equal(d.pool[4:4 + n], pool)
+        assert d.len.cpu().numpy().tolist() == at.tolist() and d.start[-1].item() == 0
+        live = torch.arange(30, device=DEV)[None] < (_i32(at)[:, None] + 63) // 64
+        assert torch.equal(d.table[live], table[live])
+
+
+def _row_bytes(dim, q41):
+    """Byte offsets of each of a unit's 32 tokens [32, bytes of a row], by the layout's rule: K's words of 8 channels, V's bytes of
+    two, a scale (and an offset) for 32 channels of each."""
+    nb, half, plane = dim // 32, dim * (20 if q41 else 18), 2 * dim
+
+    def word(wi, lane):
+        c = wi // 4
+        return c * 1024 + lane * (16 if 4 * c + 4 <= 2 * nb else 8) + wi % 4 * 4
+
+    out = []
+    for t in range(32):
+        at = [word(t // 16 * nb + b, g * 16 + t % 16) + i for b in range(nb) for g in range(4) for i in range(4)]
+        at += [half + word(2 * b + t // 16, t % 16 // 4 * 16 + c) + t % 4 for b in range(nb) for c in range(16)]
+        at += [v + 16 * dim + m + 2 * ((t // 4 * nb + b) * 4 + t % 4) + i for v in (0, half) for m in ((0, plane) if q41 else (0,))
+               for b in range(nb) for i in range(2)]
+        out.append(at)
+    out = np.array(out)
+    assert sorted(out.ravel()) == list(range(2 * half))
+    return out
+
+
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("i", range(len(KEEP)))
+def test_keep_moves_the_kept_rows_and_nothing_else(fmt, i):
+    """Every byte of every cache against the same moves on the host: rows that stay, and the places of other tokens, past a
+    sequence's end and in other pages too, hold what they held."""
+    dim, heads, page, counts, lens, paths = KEEP[i]
+    say("keep", fmt, KEEP[i][:5])
+    c = Case(fmt, dim, heads, page, counts, lens, seed=70 + i)
+    caches = [torch.from_numpy(c.rng.integers(0, 256, c.cache.numel(), dtype=np.uint8)).to(DEV) for _ in range(3)]
+    want = [x.cpu().numpy().copy() for x in caches]
+    rows, upp = _row_bytes(dim, fmt == Q4_1), page // 32
+    unit = rows.size
+    for b, p in enumerate(paths):
+        def place(t):
+            page_no = int(c.table[b, t // page])
+            return [((page_no * heads + h) * upp + t % page // 32) * unit + rows[t % 32] for h in range(heads)]
+        for j, row in enumerate(p):
+            pos0 = lens[b] - counts[b]
+            for to, at in zip(place(pos0 + j), place(pos0 + row)):
+                for x in want:
+                    x[to] = x[at]
+    ld = max(1, max(len(p) for p in paths))
+    path = np.full((c.batch, ld), -1, np.int32)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = p
+    wq.wq_cache_keep(c.desc, c.seqs, torch.from_numpy(path).to(DEV), ld, _i32([len(p) for p in paths]), caches)
+    torch.cuda.synchronize()
+    for x, y in zip(caches, want):
+        assert np.array_equal(x.cpu().numpy(), y)
+
+
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+@pytest.mark.parametrize("dim,group,counts,lens,paged", [(128, 300, [3, 1], [3001, 70], True), (64, 300, [3] * 40, [40] * 40, True),
+                                                         (96, 150, [2, 5], [2500, 5], True), (256, 260, [2, 1], [3001, 33], True),
+                                                         (128, 3, [9, 14], [3000, 2999], False), (64, 2, [100, 1], [3001, 17], False)])
+def test_heads_of_several_tiles_and_long_pages(orc, fmt, dim, group, counts, lens, paged):
+    """More heads for a key/value head than a tile has columns, whole and shared out; sequences that are one page each, without a
+    table."""
+    say("wide groups", fmt, dim, group, counts, paged)
+    c = Case(fmt, dim, 1, 64 if paged else 3104, counts, lens, seed=group, paged=paged)
+    k, v = c.random_kv()
+    c.fill(k, v)
+    q = f32_to_bf16_bits(c.rng.standard_normal((c.rows, group, dim), dtype=np.float32))
+    masks = trees(c.rng, counts, "tree")
+    ld = -(-max(counts) // 32)
+    for window, sinks, tree in ((0, 0, True), (2100, 70, True), (2100, 70, False), (33, 4, False)):
+        sees = sees_tree(c, masks, ld, window, sinks) if tree else sees_sinks(c, window, sinks)
+        ref, ab, A = attend_seen(c, orc, k, v, bf16_bits_to_f32(q), group, dim ** -0.5, sees)
+        for ws in ("asked", None):
+            y = run_seen(c, q, group, dim ** -0.5, window, sinks, dev_words(words(masks, ld, c.rows)) if tree else None, ws=ws)[0]
+            check_attn(y, ref, ab, A, f"{window} {sinks} {tree} ws={ws}")
+
+
+@pytest.mark.parametrize("batch,rows", [(3, 90), (60, 9000), (9001, 30000)])
+def test_one_of_the_two_maps(batch, rows):
+    h, d = Pages(32, 4 * batch, batch, 4), DevPages(32, 4 * batch, batch, 4, rows)
+    want = np.random.default_rng(batch).integers(0, 128, batch)
+    start, pos, slot = h.assign(want, rows)
+    for a, b in ((d.pos, None), (None, d.slot)):
+        d.want = _i32(want)
+        wq.wq_pages_assign(d.desc, batch, d.len, d.want, d.table, 4, d.pool, rows, d.start, a, b)
+        torch.cuda.synchronize()
+        assert d.start.cpu().tolist() == start
+        assert (a if b is None else b).cpu().tolist()[:start[-1]] == (pos if b is None else slot)
+        d.assign(np.zeros(batch, int), maps=False)
+
+
+@pytest.mark.parametrize("fmt", [Q4_0, Q4_1], ids=["q4_0", "q4_1"])
+def test_keep_in_sequences_of_one_page(fmt):
+    """Without a table; the rows' lengths past the page are absent, where a path ends."""
+    c = Case(fmt, 96, 2, 96, [40, 30, 5], [90, 96, 5], seed=9, paged=False)
+    c.d_len.copy_(_i32([90, 120, 5]))                          # the second one's rows are tokens 90 .. 119 of a page of 96
+    cache = torch.from_numpy(c.rng.integers(0, 256, c.cache.numel(), dtype=np.uint8)).to(DEV)
+    want, rows = cache.cpu().numpy().copy(), _row_bytes(96, fmt == Q4_1)
+    paths, kept = [[0, 2, 3, 39], [1, 4, 5, 6, 29], [4]], [4, 3, 1]
+    for b, (p, first) in enumerate(zip(paths, (50, 90, 0))):
+        for j, row in enumerate(p[:kept[b]]):
+            for h in range(2):
+                to, at = (((b * 2 + h) * 3 + t // 32) * rows.size + rows[t % 32] for t in (first + j, first + row))
+                want[to] = want[at]
+    path = np.full((3, 5), -1, np.int32)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = p
+    got = torch.zeros(3, dtype=torch.int32, device=DEV)
+    wq.wq_cache_keep(c.desc, c.seqs, torch.from_numpy(path).to(DEV), 5, _i32([len(p) for p in paths]), [cache], got)
+    torch.cuda.synchronize()
+    assert got.cpu().tolist() == [54, 93, 1] and np.array_equal(cache.cpu().numpy(), want)
