@@ -714,9 +714,14 @@ __device__ inline void store_pair(const Pair<Q41>& r, const PairPlace& at, uint3
 // conversions and their loads come on top of the products, which is why 256 columns share each of them.  64 columns per wave
 // would halve them again, but the accumulators then leave no registers (spills, and moves to and from the accumulation
 // registers every step: slower); a ring of 4 buffers, or two units per step with 128 columns of heads of 128, gained nothing.
-// The same rows and tokens, q4_0 and q4_1: heads of 64 402 and 425 us (292 GFLOP), of 96 526 and 528 (438 GFLOP), of 128 609 and
-// 643, 4 x 4 heads of 256 875 and 1552 (584 GFLOP).  Heads of 256 have one wave per SIMD and reload 18 (q4_0) and 25 (q4_1)
-// spilled registers inside the step loop, q4_1 with heads of 128 one (256 columns) or 6 (128 columns); the others none.
+// The same rows and tokens, q4_0 and q4_1: heads of 64 421 and 427 us (292 GFLOP), of 96 504 and 531 (438 GFLOP), of 128 608 and
+// 640, 4 x 4 heads of 256 876 and 1296 (584 GFLOP).  Heads of 256 have one wave per SIMD.
+// Vector registers that the compiler spills, by its report, q4_0 and q4_1 (heads of 64 and 96: none):
+//                                  128, 256 columns   128, 128 columns   heads of 256
+//   one range of tokens               2      7           none    7         23     38
+//   with PARTS                        3      7             3     8          2     18
+//   shared out (with PARTS)          10     16             7    10         18     30
+// Shared out, 103 to 139 scalars besides (the list walk's) are kept in lanes of vector registers.
 template <int NB, int NW, int KS, bool PARTS>
 struct RowsLds {
     // steps: keys are read a unit before their product, two before their use
@@ -1053,7 +1058,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 
 
 // The same with the work shared out evenly (each_part).  Beginning a tile takes some 12 us here (three steps' conversions before the
 // first product), so wide tiles are shared out over fewer workgroups: one draft of 127 rows over 100003 tokens, 8 x 8 heads of 128, q4_0
-// (four tiles of 256 columns for each head; 416 GFLOP), 451 us with the join, 924 TFLOP/s.
+// (four tiles of 256 columns for each head; 416 GFLOP), 451-474 us with the join, 880-924 TFLOP/s.
 template <int NB, bool Q41, int NW, int KS>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NB > 4 ? 1 : 2))) void k_attn_rows_shared(AttnArgs a) {
     __shared__ RowsLds<NB, NW, KS, true> lds;

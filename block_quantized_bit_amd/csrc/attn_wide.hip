@@ -15,6 +15,7 @@
 // spilled), with the same error to four digits.
 // Heads of 256 have one wave per SIMD, which nothing hides the reads of LDS for: issued early (below) they take 16 sequences' 25 rows
 // over 4096 tokens and 4 first ones, 2 x 8 heads, q4_1, from 97 to 87 us.  A ring of three units there gained nothing.
+// (The compiler spills registers for heads of 128 in q4_1 alone, 6.)
 #include "attn_kernel.h"
 
 namespace wq {

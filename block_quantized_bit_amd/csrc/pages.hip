@@ -58,9 +58,11 @@ __global__ __launch_bounds__(256) void k_pages_init(int pages, int32_t* pool) {
 // and its round trips cost more: two calls, of 4096 drafts 28.3 us and 27.0 now, of 61 prompts 19.3 and 17.7.)
 constexpr int kSeqsAtOnce = 8192, kAtOnce = 4;   // kAtOnce: items of a thread that are on their way together
 // What bounds it: the sums' instructions, which every workgroup has for itself, and the way to memory and back (lengths, table,
-// list, one after the other).  In us, a call that takes and one that gives back: 96
-// sequences of one row 3.6 and 4.2, 61 prompts of 282 thousand rows and 4400 pages 11.6 and 8.0, 4096 drafts of 139 thousand rows and
-// 4300 pages 13.8 and 14.2.  Up to kFewSeqs sequences take little LDS (with that of more, the 96 take 6.1 and 5.4).
+// list, one after the other).  In us as traced, a call that takes and one that gives back: 96 sequences of one row 4.9 and 4.9, 61
+// prompts of 282 thousand rows and 4400 pages 7.7, with 1.3 of k_pages_settle, and 8.1, 4096 drafts of 139 thousand rows and 4300 pages
+// 11.1, with 4.0, and 14.4.  The workgroups go by the rows, so that pages are given back without rows by one: 200 thousand of 40
+// sequences 227 us.  Up to kFewSeqs sequences take little LDS, which leaves a compute unit room for others' workgroups, and some 0.05 us
+// a call (two calls of the 96 in a replayed graph 9.8 us, with the LDS of more 9.9).
 constexpr int kFewSeqs = 1024;
 
 // a + b, at most `most`: associative for numbers that are at most that.
@@ -333,7 +335,8 @@ __global__ __launch_bounds__(256) void k_pages_settle(PagesArgs a) {
 }
 
 // More sequences, or more entries than 32 bits count: one workgroup, and the rows by a launch of their own.  First what is given
-// back goes on the list's end (its front), the first sequence's first page last; then what is wanted is taken from there.
+// back goes on the list's end (its front), the first sequence's first page last; then what is wanted is taken from there.  Bound by
+// the one workgroup's three walks, one after the other (with 11 registers spilled): 16384 sequences of a row each 87 us, 65536 316.
 __global__ __launch_bounds__(kThreads) void k_pages_assign_many(PagesArgs a) {
     __shared__ int64_t lds[kThreads / 64];
     int32_t* const list = a.pool + 4;

@@ -432,7 +432,8 @@ wq_status wq_pages_init(int64_t pages, int32_t* pool, void* stream);
 
 /* Lengths become what is wanted: sequence b, of len[b] tokens, gets or gives back pages so
  * that its table has ceil(want[b] / page) of them, and len[b] becomes want[b].  One call
- * serves sequences that grow, shrink and end (want 0) alike.
+ * serves sequences that grow, shrink and end (want 0) alike.  A sequence keeps all its pages
+ * until it shrinks, those whose tokens have left an attention window too.
  *   d         : of the cache(s); its page and pages are what counts
  *   batch     : sequences, 1 .. 2^20 (0: the call does nothing, and row_start[0] and the pool's
  *               words stay as they were)
